@@ -19,7 +19,7 @@ LIBRARY = os.path.join(HERE, "libtw.so")
 PEAK_PROBE = os.path.join(HERE, "peak_probe")  # achievable-peak program (csrc/peak_probe.hip)
 
 SOURCES = ["gate_twell.hip", "pack_dense.hip", "sparse_updown.hip", "dense_ffn.hip", "hybrid.hip",
-           "tw_api.cpp"]
+           "layer_norm.hip", "quant_gemm.hip", "tw_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -684,3 +684,248 @@ tw_status tw_hybrid_bwd_dw(const uint16_t *x, const uint16_t *dy, int M, int K, 
 }
 
 }  // extern "C"
+
+namespace {
+
+// ---- layer norm and int8 products ------------------------------------------
+
+bool float_type(int t) { return t == TW_BF16 || t == TW_F32; }
+
+// Rows of x: a known type, x_stride elements apart.
+tw_status check_rows(int M, int K, int max_k, int x_type, int64_t x_stride) {
+    if (M < 0 || K <= 0) return fail(TW_EINVAL, "M=%d K=%d: need M >= 0, K > 0", M, K);
+    if (K > max_k) return fail(TW_EUNSUPPORTED, "K=%d: at most %d", K, max_k);
+    if (!float_type(x_type)) return fail(TW_EINVAL, "x_type=%d: TW_BF16 or TW_F32", x_type);
+    if (x_stride < K)
+        return fail(TW_EINVAL, "x_stride=%lld is below K=%d", (long long)x_stride, K);
+    if (x_stride > (int64_t(1) << 40))
+        return fail(TW_EUNSUPPORTED, "x_stride=%lld: at most 2^40", (long long)x_stride);
+    return TW_OK;
+}
+
+// What the layer norm's forward entry points share (the norm's inputs and
+// the stored sum).
+tw_status check_norm(const void *x, int x_type, int64_t x_stride, const void *add, int add_type,
+                     const float *gamma, const float *beta, float eps, int M, int K,
+                     const void *sum) {
+    TW_TRY(check_rows(M, K, tw::kNormMaxK, x_type, x_stride));
+    if (!(eps >= 0.0f)) return fail(TW_EINVAL, "eps=%g: need eps >= 0", (double)eps);
+    TW_NEED_M(x);
+    TW_NEED(gamma);
+    if (add && !float_type(add_type))
+        return fail(TW_EINVAL, "add_type=%d: TW_BF16 or TW_F32", add_type);
+    if (add) TW_NEED(add);
+    if (beta) TW_NEED(beta);
+    if (sum && !add && M > 0) return fail(TW_EINVAL, "sum is given without add");
+    if (sum) TW_NEED(sum);
+    return TW_OK;
+}
+
+// Shapes of an int8 product, for both products and their workspace.
+tw_status check_product(int M, int K, int N, int max_k) {
+    if (M < 0 || K <= 0 || N <= 0)
+        return fail(TW_EINVAL, "M=%d K=%d N=%d: need M >= 0, K, N > 0", M, K, N);
+    if (K % 16) return fail(TW_EUNSUPPORTED, "K=%d: must be a multiple of 16", K);
+    if (K > max_k) return fail(TW_EUNSUPPORTED, "K=%d: at most %d", K, max_k);
+    const int most = 1 << 24;
+    if (M > most || N > most) return fail(TW_EUNSUPPORTED, "M=%d N=%d: at most 2^24 each", M, N);
+    // the grid of 256 x 128 tiles
+    if (((int64_t)M + 255) / 256 * (((int64_t)N + 127) / 128) > (int64_t(1) << 22))
+        return fail(TW_EUNSUPPORTED, "M=%d N=%d: at most 2^37 outputs", M, N);
+    return TW_OK;
+}
+
+size_t quant_ws(int M, int K) {
+    return round_up((size_t)M * K, 256) + round_up((size_t)M * 4, 256);
+}
+
+// The int8 rows and scales a product reads: the caller's, or those the
+// quantisation is about to write to the workspace.
+struct QuantIn {
+    const int8_t *q;
+    const float *scale;
+    int8_t *q_out;  // null: x is int8 already
+    float *scale_out;
+};
+tw_status check_quant_in(const void *x, int x_type, int64_t x_stride, const float *x_scale, int M,
+                         int K, int max_k, void *ws, size_t ws_bytes, QuantIn *in) {
+    if (x_type == TW_INT8) {
+        if (x_stride != K)
+            return fail(TW_EINVAL, "x_stride=%lld: int8 rows are contiguous (K=%d)",
+                        (long long)x_stride, K);
+        TW_NEED_M(x);
+        TW_NEED_M(x_scale);
+        *in = QuantIn{static_cast<const int8_t *>(x), x_scale, nullptr, nullptr};
+        return TW_OK;
+    }
+    TW_TRY(check_rows(M, K, max_k, x_type, x_stride));
+    if (x_scale) return fail(TW_EINVAL, "x_scale is given, but x is not int8");
+    TW_NEED_M(x);
+    TW_NEED_M(ws);
+    const size_t need = quant_ws(M, K);
+    if (M > 0 && ws_bytes < need)
+        return fail(TW_EINVAL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    int8_t *q = static_cast<int8_t *>(ws);
+    float *sc = M > 0 ? reinterpret_cast<float *>(q + round_up((size_t)M * K, 256)) : nullptr;
+    *in = QuantIn{q, sc, q, sc};
+    return TW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tw_status tw_layernorm_fwd(const void *x, int x_type, int64_t x_stride, const void *add,
+                           int add_type, const float *gamma, const float *beta, float eps, int M,
+                           int K, void *sum, void *y, int y_type, float *mean, float *rstd,
+                           void *stream, void *const *events) {
+    TW_TRY(check_norm(x, x_type, x_stride, add, add_type, gamma, beta, eps, M, K, sum));
+    if (!float_type(y_type)) return fail(TW_EINVAL, "y_type=%d: TW_BF16 or TW_F32", y_type);
+    TW_NEED_M(y);
+    if (mean) TW_NEED(mean);
+    if (rstd) TW_NEED(rstd);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_layernorm(x, x_type, x_stride, add, add_type, gamma, beta, eps, M,
+                                         K, sum, y, y_type, mean, rstd, s),
+                    "layer norm launch"));
+    TW_TRY(record(events, 1, s));
+    return TW_OK;
+}
+
+size_t tw_layernorm_bwd_workspace_bytes(int M, int K) {
+    if (M < 0 || K <= 0 || K > tw::kNormMaxK) return 0;
+    return (size_t)tw::layernorm_bwd_groups(M, K) * 2 * K * 4;
+}
+
+tw_status tw_layernorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
+                           int64_t x_stride, const float *gamma, const float *mean,
+                           const float *rstd, const void *dres, int M, int K, void *dx,
+                           int dx_type, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                           void *stream, void *const *events) {
+    TW_TRY(check_rows(M, K, tw::kNormMaxK, x_type, x_stride));
+    if (!float_type(dy_type)) return fail(TW_EINVAL, "dy_type=%d: TW_BF16 or TW_F32", dy_type);
+    if (!float_type(dx_type)) return fail(TW_EINVAL, "dx_type=%d: TW_BF16 or TW_F32", dx_type);
+    TW_NEED_M(dy);
+    TW_NEED_M(x);
+    TW_NEED(gamma);
+    TW_NEED_M(mean);
+    TW_NEED_M(rstd);
+    TW_NEED_M(dx);
+    if (dres) TW_NEED(dres);
+    if (dgamma) TW_NEED(dgamma);
+    if (dbeta) TW_NEED(dbeta);
+    if (dgamma || dbeta) {
+        TW_NEED(ws);
+        const size_t need = tw_layernorm_bwd_workspace_bytes(M, K);
+        if (ws_bytes < need)
+            return fail(TW_EINVAL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_layernorm_bwd(dy, dy_type, x, x_type, x_stride, gamma, mean, rstd,
+                                             dres, M, K, dx, dx_type, dgamma, dbeta,
+                                             static_cast<float *>(ws), s,
+                                             events ? static_cast<hipEvent_t>(events[1]) : nullptr),
+                    "layer norm gradient launch"));
+    TW_TRY(record(events, 2, s));
+    return TW_OK;
+}
+
+tw_status tw_quant_rows(const void *x, int x_type, int64_t x_stride, int M, int K, int8_t *q,
+                        float *scale, void *stream, void *const *events) {
+    TW_TRY(check_rows(M, K, tw::kQuantMaxK, x_type, x_stride));
+    TW_NEED_M(x);
+    TW_NEED_M(q);
+    TW_NEED_M(scale);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_quant_rows(x, x_type, x_stride, M, K, q, scale, s),
+                    "row quantisation launch"));
+    TW_TRY(record(events, 1, s));
+    return TW_OK;
+}
+
+tw_status tw_layernorm_quant(const void *x, int x_type, int64_t x_stride, const void *add,
+                             int add_type, const float *gamma, const float *beta, float eps, int M,
+                             int K, void *sum, int8_t *q, float *scale, void *stream,
+                             void *const *events) {
+    TW_TRY(check_norm(x, x_type, x_stride, add, add_type, gamma, beta, eps, M, K, sum));
+    TW_NEED_M(q);
+    TW_NEED_M(scale);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_layernorm_quant(x, x_type, x_stride, add, add_type, gamma, beta,
+                                               eps, M, K, sum, q, scale, s),
+                    "layer norm launch"));
+    TW_TRY(record(events, 1, s));
+    return TW_OK;
+}
+
+size_t tw_quant_workspace_bytes(int M, int K) {
+    if (M < 0 || K <= 0 || K % 16 || K > tw::kQuantMaxK || M > (1 << 24)) return 0;
+    return quant_ws(M, K) + 256;
+}
+
+tw_status tw_quant_linear(const void *x, int x_type, int64_t x_stride, const float *x_scale,
+                          const int8_t *w, const float *w_scale, const float *bias, int M, int K,
+                          int N, void *y, int y_type, void *ws, size_t ws_bytes, void *stream,
+                          void *const *events) {
+    TW_TRY(check_product(M, K, N, tw::kQuantMaxK));
+    if (!float_type(y_type)) return fail(TW_EINVAL, "y_type=%d: TW_BF16 or TW_F32", y_type);
+    TW_NEED(w);
+    TW_NEED(w_scale);
+    if (bias) TW_NEED(bias);
+    TW_NEED_M(y);
+    QuantIn in;
+    TW_TRY(check_quant_in(x, x_type, x_stride, x_scale, M, K, tw::kQuantMaxK, ws, ws_bytes, &in));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    if (in.q_out)
+        TW_TRY(launched(tw::launch_quant_rows(x, x_type, x_stride, M, K, in.q_out, in.scale_out, s),
+                        "row quantisation launch"));
+    TW_TRY(record(events, 1, s));
+    TW_TRY(launched(tw::launch_quant_linear(in.q, in.scale, w, w_scale, bias, M, K, N, y, y_type, s),
+                    "int8 product launch"));
+    TW_TRY(record(events, 2, s));
+    return TW_OK;
+}
+
+tw_status tw_quant_gateup(const void *x, int x_type, int64_t x_stride, const float *x_scale,
+                          const float *gamma, const float *beta, float eps, const int8_t *wg,
+                          const float *g_scale, const int8_t *wu, const float *u_scale, int M,
+                          int K, int N, void *h, int h_type, void *ws, size_t ws_bytes,
+                          void *stream, void *const *events) {
+    const int max_k = gamma ? tw::kNormMaxK : tw::kQuantMaxK;
+    TW_TRY(check_product(M, K, N, max_k));
+    if (!float_type(h_type)) return fail(TW_EINVAL, "h_type=%d: TW_BF16 or TW_F32", h_type);
+    if (gamma && x_type == TW_INT8) return fail(TW_EINVAL, "gamma is given, but x is int8");
+    if (beta && !gamma) return fail(TW_EINVAL, "beta is given without gamma");
+    if (gamma && !(eps >= 0.0f)) return fail(TW_EINVAL, "eps=%g: need eps >= 0", (double)eps);
+    if (gamma) TW_NEED(gamma);
+    if (beta) TW_NEED(beta);
+    TW_NEED(wg);
+    TW_NEED(g_scale);
+    TW_NEED(wu);
+    TW_NEED(u_scale);
+    TW_NEED_M(h);
+    QuantIn in;
+    TW_TRY(check_quant_in(x, x_type, x_stride, x_scale, M, K, max_k, ws, ws_bytes, &in));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    if (in.q_out && gamma)
+        TW_TRY(launched(tw::launch_layernorm_quant(x, x_type, x_stride, nullptr, 0, gamma, beta,
+                                                   eps, M, K, nullptr, in.q_out, in.scale_out, s),
+                        "layer norm launch"));
+    else if (in.q_out)
+        TW_TRY(launched(tw::launch_quant_rows(x, x_type, x_stride, M, K, in.q_out, in.scale_out, s),
+                        "row quantisation launch"));
+    TW_TRY(record(events, 1, s));
+    TW_TRY(launched(tw::launch_quant_gateup(in.q, in.scale, wg, g_scale, wu, u_scale, M, K, N, h,
+                                            h_type, s),
+                    "int8 product launch"));
+    TW_TRY(record(events, 2, s));
+    return TW_OK;
+}
+
+}  // extern "C"

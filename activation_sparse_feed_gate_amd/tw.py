@@ -14,6 +14,13 @@ hybrid training storage ``tw_hybrid_pack``, ``tw_hybrid_up``,
 ``tw_hybrid_bwd_dw``.  ``pack_gate``, ``pack_unfused``, ``sparse_ffn``, ``ffn``,
 ``hybrid_forward`` and ``hybrid_backward`` allocate their outputs and return
 them.
+
+The layer norm in front of the block is ``tw_layernorm_fwd`` and
+``tw_layernorm_bwd`` (allocating: ``layernorm``, ``layernorm_backward``); the
+block's dense projections on 8-bit integers are ``tw_quant_rows``,
+``tw_layernorm_quant``, ``tw_quant_linear`` and ``tw_quant_gateup``
+(allocating: ``quantize_rows``, ``layernorm_quantize``, ``quant_linear``,
+``quant_gateup``).
 """
 from __future__ import annotations
 
@@ -86,7 +93,31 @@ _lib.tw_hybrid_bwd_dw.restype = _i
 _lib.tw_hybrid_bwd_dw.argtypes = [_vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                   _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]
 
+_i64, _f = ctypes.c_int64, ctypes.c_float
+_lib.tw_layernorm_fwd.restype = _i
+_lib.tw_layernorm_fwd.argtypes = [_vp, _i, _i64, _vp, _i, _vp, _vp, _f, _i, _i, _vp, _vp, _i, _vp,
+                                  _vp, _vp, _vp]
+_lib.tw_layernorm_bwd_workspace_bytes.restype = _sz
+_lib.tw_layernorm_bwd_workspace_bytes.argtypes = [_i, _i]
+_lib.tw_layernorm_bwd.restype = _i
+_lib.tw_layernorm_bwd.argtypes = [_vp, _i, _vp, _i, _i64, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp,
+                                  _vp, _vp, _sz, _vp, _vp]
+_lib.tw_quant_rows.restype = _i
+_lib.tw_quant_rows.argtypes = [_vp, _i, _i64, _i, _i, _vp, _vp, _vp, _vp]
+_lib.tw_layernorm_quant.restype = _i
+_lib.tw_layernorm_quant.argtypes = [_vp, _i, _i64, _vp, _i, _vp, _vp, _f, _i, _i, _vp, _vp, _vp,
+                                    _vp, _vp]
+_lib.tw_quant_workspace_bytes.restype = _sz
+_lib.tw_quant_workspace_bytes.argtypes = [_i, _i]
+_lib.tw_quant_linear.restype = _i
+_lib.tw_quant_linear.argtypes = [_vp, _i, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _sz,
+                                 _vp, _vp]
+_lib.tw_quant_gateup.restype = _i
+_lib.tw_quant_gateup.argtypes = [_vp, _i, _i64, _vp, _vp, _vp, _f, _vp, _vp, _vp, _vp, _i, _i, _i,
+                                 _vp, _i, _vp, _sz, _vp, _vp]
+
 TW_OK, TW_EINVAL, TW_EUNSUPPORTED, TW_EHIP = 0, 1, 2, 3
+TW_BF16, TW_F32, TW_INT8 = 0, 1, 2
 
 
 class TwError(RuntimeError):
@@ -111,7 +142,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _rows_ptr(t):
+    """Address of a tensor whose rows ``_Args.rows`` has checked."""
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the library must be device tensors")
+    return t.data_ptr()
+
+
 _F32, _I32, _BF16, _U8T = torch.float32, torch.int32, torch.bfloat16, torch.uint8
+_I8 = torch.int8
+_TYPE = {_BF16: TW_BF16, _F32: TW_F32, _I8: TW_INT8}
+_FLOATS = (_BF16, _F32)
 
 
 class _Args:
@@ -135,6 +176,9 @@ class _Args:
 
     def shape(self, t, name, dtype, shape):
         """t must have exactly this shape (None: t may be None)."""
+        if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape
+                and t.device == self.device):
+            return
         if t is None:
             raise ValueError(f"{self.where}: {name} is required")
         self._common(t, name, dtype)
@@ -162,6 +206,29 @@ class _Args:
         if t.dim() != 1 or t.numel() < n:
             raise ValueError(f"{self.where}: {name} has shape {tuple(t.shape)}, expected "
                              f"one dimension of at least {n} elements")
+
+    def typed(self, t, name, dtypes, shape):
+        """t has this shape and one of these dtypes; its tw_type."""
+        if t is None:
+            raise ValueError(f"{self.where}: {name} is required")
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{self.where}: {name} must be a tensor, got {type(t).__name__}")
+        dtype = t.dtype
+        if dtype not in dtypes:
+            raise TypeError(f"{self.where}: {name} must be one of {dtypes}, got {dtype}")
+        self.shape(t, name, dtype, shape)
+        return _TYPE[dtype]
+
+    def rows(self, t, name, dtypes):
+        """t is [M][K] with contiguous rows, any distance apart (a single
+        row's distance counts as K): its tw_type and the row distance."""
+        M, K = t.shape
+        kind = self.typed(t, name, dtypes, (M, K))
+        if t.is_contiguous():
+            return kind, K
+        if K > 1 and t.stride(1) != 1:
+            raise ValueError(f"{self.where}: {name} must have contiguous rows")
+        return kind, (t.stride(0) if M > 1 else K)
 
     def bytes(self, t, name):
         """A workspace: any dtype, on the inputs' device (its size is checked
@@ -496,6 +563,142 @@ def tw_hybrid_bwd_dw(x, dy, P, hy_h, hy_du, hy_dz, hy_idx, hy_cnt, route, bk_row
     _check(st, "tw_hybrid_bwd_dw")
 
 
+# ------------------------------------------- layer norm and int8 products --
+def _norm_args(a, x, add, gamma, beta, total):
+    M, K = x.shape
+    kind, stride = a.rows(x, "x", _FLOATS)
+    add_kind = 0 if add is None else a.typed(add, "add", _FLOATS, (M, K))
+    a.shape(gamma, "gamma", _F32, (K,))
+    a.opt(beta, "beta", _F32, (K,))
+    a.opt(total, "total", x.dtype, (M, K))
+    return kind, stride, add_kind
+
+
+def tw_layernorm_fwd(x, gamma, beta, eps, y, add=None, total=None, mean=None, rstd=None,
+                     stream=None, events=None) -> None:
+    """y = layer norm of x (+ add); ``total`` receives x + add in x's type,
+    ``mean`` and ``rstd`` what the backward reads."""
+    M, K = _dims2(x, "x", "tw_layernorm_fwd")
+    a = _Args("tw_layernorm_fwd", x)
+    kind, stride, add_kind = _norm_args(a, x, add, gamma, beta, total)
+    y_kind = a.typed(y, "y", _FLOATS, (M, K))
+    a.opt(mean, "mean", _F32, (M,))
+    a.opt(rstd, "rstd", _F32, (M,))
+    ev = _events(events)
+    st = _lib.tw_layernorm_fwd(_rows_ptr(x), kind, stride, _ptr(add), add_kind, _ptr(gamma),
+                               _ptr(beta), eps, M, K, _ptr(total), _ptr(y), y_kind, _ptr(mean),
+                               _ptr(rstd), _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_layernorm_fwd")
+
+
+def tw_layernorm_bwd_workspace_bytes(M, K) -> int:
+    return int(_lib.tw_layernorm_bwd_workspace_bytes(M, K))
+
+
+def tw_layernorm_bwd(dy, x, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, ws=None,
+                     stream=None, events=None) -> None:
+    M, K = _dims2(x, "x", "tw_layernorm_bwd")
+    a = _Args("tw_layernorm_bwd", x)
+    kind, stride = a.rows(x, "x", _FLOATS)
+    dy_kind = a.typed(dy, "dy", _FLOATS, (M, K))
+    a.shape(gamma, "gamma", _F32, (K,))
+    a.shape(mean, "mean", _F32, (M,))
+    a.shape(rstd, "rstd", _F32, (M,))
+    dx_kind = a.typed(dx, "dx", _FLOATS, (M, K))
+    a.opt(dres, "dres", dx.dtype, (M, K))
+    a.opt(dgamma, "dgamma", _F32, (K,))
+    a.opt(dbeta, "dbeta", _F32, (K,))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    st = _lib.tw_layernorm_bwd(_ptr(dy), dy_kind, _rows_ptr(x), kind, stride, _ptr(gamma),
+                               _ptr(mean), _ptr(rstd), _ptr(dres), M, K, _ptr(dx), dx_kind,
+                               _ptr(dgamma), _ptr(dbeta), _ptr(ws), _nbytes(ws), _stream(stream),
+                               ev[0] if ev else None)
+    _check(st, "tw_layernorm_bwd")
+
+
+def tw_quant_rows(x, q, scale, stream=None, events=None) -> None:
+    """q, scale = the rows of x in int8 with one scale each."""
+    M, K = _dims2(x, "x", "tw_quant_rows")
+    a = _Args("tw_quant_rows", x)
+    kind, stride = a.rows(x, "x", _FLOATS)
+    a.shape(q, "q", _I8, (M, K))
+    a.shape(scale, "scale", _F32, (M,))
+    ev = _events(events)
+    st = _lib.tw_quant_rows(_rows_ptr(x), kind, stride, M, K, _ptr(q), _ptr(scale),
+                            _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_quant_rows")
+
+
+def tw_layernorm_quant(x, gamma, beta, eps, q, scale, add=None, total=None, stream=None,
+                       events=None) -> None:
+    """The layer norm of x (+ add) in int8 with one scale per row."""
+    M, K = _dims2(x, "x", "tw_layernorm_quant")
+    a = _Args("tw_layernorm_quant", x)
+    kind, stride, add_kind = _norm_args(a, x, add, gamma, beta, total)
+    a.shape(q, "q", _I8, (M, K))
+    a.shape(scale, "scale", _F32, (M,))
+    ev = _events(events)
+    st = _lib.tw_layernorm_quant(_rows_ptr(x), kind, stride, _ptr(add), add_kind, _ptr(gamma),
+                                 _ptr(beta), eps, M, K, _ptr(total), _ptr(q), _ptr(scale),
+                                 _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_layernorm_quant")
+
+
+def tw_quant_workspace_bytes(M, K) -> int:
+    return int(_lib.tw_quant_workspace_bytes(M, K))
+
+
+def _quant_in(a, x, x_scale):
+    """Rows of float (no x_scale), or int8 rows with their scales."""
+    kind, stride = a.rows(x, "x", (_BF16, _F32, _I8))
+    if kind == TW_INT8:
+        a.shape(x_scale, "x_scale", _F32, (x.shape[0],))
+    elif x_scale is not None:
+        raise ValueError(f"{a.where}: x_scale is given, but x is not int8")
+    return kind, stride
+
+
+def tw_quant_linear(x, w, w_scale, y, bias=None, x_scale=None, ws=None, stream=None,
+                    events=None) -> None:
+    M, K = _dims2(x, "x", "tw_quant_linear")
+    N = _dims2(w, "w", "tw_quant_linear")[0]
+    a = _Args("tw_quant_linear", x)
+    kind, stride = _quant_in(a, x, x_scale)
+    a.shape(w, "w", _I8, (N, K))
+    a.shape(w_scale, "w_scale", _F32, (N,))
+    a.opt(bias, "bias", _F32, (N,))
+    y_kind = a.typed(y, "y", _FLOATS, (M, N))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    st = _lib.tw_quant_linear(_rows_ptr(x), kind, stride, _ptr(x_scale), _ptr(w), _ptr(w_scale),
+                              _ptr(bias), M, K, N, _ptr(y), y_kind, _ptr(ws), _nbytes(ws),
+                              _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_quant_linear")
+
+
+def tw_quant_gateup(x, wg, g_scale, wu, u_scale, h, gamma=None, beta=None, eps=1e-5, x_scale=None,
+                    ws=None, stream=None, events=None) -> None:
+    M, K = _dims2(x, "x", "tw_quant_gateup")
+    N = _dims2(wg, "wg", "tw_quant_gateup")[0]
+    a = _Args("tw_quant_gateup", x)
+    kind, stride = _quant_in(a, x, x_scale)
+    a.shape(wg, "wg", _I8, (N, K))
+    a.shape(g_scale, "g_scale", _F32, (N,))
+    a.shape(wu, "wu", _I8, (N, K))
+    a.shape(u_scale, "u_scale", _F32, (N,))
+    a.opt(gamma, "gamma", _F32, (K,))
+    a.opt(beta, "beta", _F32, (K,))
+    h_kind = a.typed(h, "h", _FLOATS, (M, N))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    st = _lib.tw_quant_gateup(_rows_ptr(x), kind, stride, _ptr(x_scale), _ptr(gamma), _ptr(beta),
+                              eps, _ptr(wg), _ptr(g_scale), _ptr(wu), _ptr(u_scale), M, K, N,
+                              _ptr(h), h_kind, _ptr(ws), _nbytes(ws), _stream(stream),
+                              ev[0] if ev else None)
+    _check(st, "tw_quant_gateup")
+
+
 # ------------------------------------------------------------- allocating --
 def alloc_pack(M, N, T, C, R_max, device="cuda"):
     """Output buffers of tw_pack_gate."""
@@ -655,6 +858,90 @@ def hybrid_backward(x, wg_t, wu_t, wd, dy, hy, l1=0.0):
                      hy["bk_h"], out["bk_du"], out["bk_dz"], out["dwg_t"], out["dwu_t"],
                      out["dwd"], wsw)
     return out
+
+
+def layernorm(x, gamma, beta=None, eps=1e-5, add=None, out_dtype=torch.bfloat16):
+    """Layer norm of the rows of x (+ add).  Returns a dict: y, mean and rstd
+    (fp32, for ``layernorm_backward``), and sum = x + add in x's type (None
+    without add)."""
+    M, K = _dims2(x, "x", "layernorm")
+    dev = x.device
+    out = {
+        "y": torch.empty((M, K), dtype=out_dtype, device=dev),
+        "sum": None if add is None else torch.empty((M, K), dtype=x.dtype, device=dev),
+        "mean": torch.empty((M,), dtype=_F32, device=dev),
+        "rstd": torch.empty((M,), dtype=_F32, device=dev),
+    }
+    tw_layernorm_fwd(x, gamma, beta, eps, out["y"], add=add, total=out["sum"], mean=out["mean"],
+                     rstd=out["rstd"])
+    return out
+
+
+def layernorm_backward(dy, x, gamma, mean, rstd, dres=None, dx_dtype=torch.float32):
+    """Gradient of ``layernorm``: x is its input (``sum`` if there was an
+    add), dres the gradient reaching x past the norm (dx's dtype).  Returns a
+    dict with dx, dgamma, dbeta."""
+    M, K = _dims2(x, "x", "layernorm_backward")
+    dev = x.device
+    out = {
+        "dx": torch.empty((M, K), dtype=dx_dtype, device=dev),
+        "dgamma": torch.empty((K,), dtype=_F32, device=dev),
+        "dbeta": torch.empty((K,), dtype=_F32, device=dev),
+    }
+    ws = torch.empty((tw_layernorm_bwd_workspace_bytes(M, K),), dtype=_U8T, device=dev)
+    tw_layernorm_bwd(dy, x, gamma, mean, rstd, out["dx"], out["dgamma"], out["dbeta"], dres=dres,
+                     ws=ws)
+    return out
+
+
+def quantize_rows(x):
+    """The rows of x in int8: (q [M][K], scale [M]).  For weights, x is the
+    matrix with one row per output channel."""
+    M, K = _dims2(x, "x", "quantize_rows")
+    q = torch.empty((M, K), dtype=_I8, device=x.device)
+    scale = torch.empty((M,), dtype=_F32, device=x.device)
+    tw_quant_rows(x, q, scale)
+    return q, scale
+
+
+def layernorm_quantize(x, gamma, beta=None, eps=1e-5, add=None):
+    """The layer norm of x (+ add) in int8.  Returns a dict: q, scale, and
+    sum = x + add in x's type (None without add)."""
+    M, K = _dims2(x, "x", "layernorm_quantize")
+    out = {
+        "q": torch.empty((M, K), dtype=_I8, device=x.device),
+        "scale": torch.empty((M,), dtype=_F32, device=x.device),
+        "sum": None if add is None else torch.empty((M, K), dtype=x.dtype, device=x.device),
+    }
+    tw_layernorm_quant(x, gamma, beta, eps, out["q"], out["scale"], add=add, total=out["sum"])
+    return out
+
+
+def _quant_ws(x):
+    if x.dtype == _I8:
+        return None
+    return torch.empty((tw_quant_workspace_bytes(*x.shape),), dtype=_U8T, device=x.device)
+
+
+def quant_linear(x, w, w_scale, bias=None, x_scale=None, out_dtype=torch.bfloat16, ws=None):
+    """y = x w^T (+ bias) on int8 operands: x is bf16 or fp32 (quantised by
+    the call) or int8 with x_scale; w [N][K] int8 with w_scale [N]."""
+    M, N = _dims2(x, "x", "quant_linear")[0], _dims2(w, "w", "quant_linear")[0]
+    y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    tw_quant_linear(x, w, w_scale, y, bias=bias, x_scale=x_scale,
+                    ws=_quant_ws(x) if ws is None else ws)
+    return y
+
+
+def quant_gateup(x, wg, g_scale, wu, u_scale, gamma=None, beta=None, eps=1e-5, x_scale=None,
+                 out_dtype=torch.bfloat16, ws=None):
+    """h = ReLU(n wg^T) * (n wu^T) on int8 operands, n the layer norm of x
+    (gamma given) or x itself; x as in ``quant_linear``."""
+    M, N = _dims2(x, "x", "quant_gateup")[0], _dims2(wg, "wg", "quant_gateup")[0]
+    h = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    tw_quant_gateup(x, wg, g_scale, wu, u_scale, h, gamma=gamma, beta=beta, eps=eps,
+                    x_scale=x_scale, ws=_quant_ws(x) if ws is None else ws)
+    return h
 
 
 def library_path() -> str:

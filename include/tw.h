@@ -24,7 +24,10 @@
  * equivalent of tw_pack_gate (dense gate written to memory, then packed).
  * tw_hybrid_pack, tw_hybrid_up and tw_hybrid_down are the training forward
  * over the hybrid storage of sections 3-6 and 3-7, and tw_hybrid_bwd_dh,
- * tw_hybrid_bwd_dx and tw_hybrid_bwd_dw its backward (declared at the end).
+ * tw_hybrid_bwd_dx and tw_hybrid_bwd_dw its backward.  tw_layernorm_fwd and
+ * tw_layernorm_bwd are the layer norm in front of the block, and
+ * tw_quant_gateup and tw_quant_linear its dense projections in 8-bit integers
+ * (declared at the end).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -86,6 +89,9 @@ typedef enum tw_status {
     TW_EUNSUPPORTED = 2,  /* valid but outside the supported shapes above  */
     TW_EHIP = 3           /* a HIP runtime call or kernel launch failed    */
 } tw_status;
+
+/* Element type of a row buffer, where an entry point takes more than one. */
+typedef enum tw_type { TW_BF16 = 0, TW_F32 = 1, TW_INT8 = 2 } tw_type;
 
 /* Static name of a status code. */
 const char *tw_status_str(int status);
@@ -406,6 +412,110 @@ tw_status tw_hybrid_bwd_dw(const uint16_t *x, const uint16_t *dy, int M, int K, 
                            const uint16_t *bk_h, const uint16_t *bk_du, const uint16_t *bk_dz,
                            float *dwg_t, float *dwu_t, float *dwd, void *ws, size_t ws_bytes,
                            void *stream, void *const *events);
+
+/*
+ * Layer norm over the last dimension, forward.  For every row m, in fp32:
+ *     z = x[m] (+ add[m]),  mean = sum(z) / K,
+ *     rstd = 1 / sqrt(sum((z - mean)^2) / K + eps),
+ *     y[m] = (z - mean) * rstd * gamma (+ beta).
+ * add is the block's output joining the residual stream; its sum with x is
+ * stored to `sum` (rounded to x's type; the norm uses the unrounded sum).
+ *
+ *   x       [M] rows of K, x_stride elements apart (x_stride >= K), bf16 or fp32
+ *   add     [M][K]   bf16 or fp32, or NULL
+ *   gamma   [K]      fp32
+ *   beta    [K]      fp32, or NULL
+ *   sum     [M][K]   x's type, or NULL; only with add
+ *   y       [M][K]   bf16 or fp32
+ *   mean, rstd [M]   fp32, or NULL: what tw_layernorm_bwd reads
+ *
+ * sum may be x itself (when x_stride == K) or, of the same type, add.
+ * K from 1 to 16384, any value (odd rows included); eps >= 0.  A row holding
+ * a NaN or an infinity gives NaN.  events: [0] before, [1] after the kernel.
+ */
+tw_status tw_layernorm_fwd(const void *x, int x_type, int64_t x_stride, const void *add,
+                           int add_type, const float *gamma, const float *beta, float eps, int M,
+                           int K, void *sum, void *y, int y_type, float *mean, float *rstd,
+                           void *stream, void *const *events);
+
+/*
+ * Layer norm, backward: with n = (x - mean) rstd (x: the forward's z as
+ * stored, in `sum` if there was an add) and t = dy gamma,
+ *     dx = rstd (t - sum(t) / K - n sum(t n) / K) (+ dres),
+ *     dgamma = sum over rows of dy n,   dbeta = sum over rows of dy.
+ * dres is the gradient that reaches z past the norm (the residual stream's).
+ *
+ *   dy      [M][K]  bf16 or fp32;  x as in the forward;  mean, rstd [M]
+ *   dres    [M][K]  dx's type, or NULL
+ *   dx      [M][K]  bf16 or fp32
+ *   dgamma, dbeta [K] fp32, each may be NULL
+ * The row sums of dgamma and dbeta are taken in a fixed order (bit-identical
+ * run to run).  M = 0 writes zeros to dgamma and dbeta.  ws_bytes >=
+ * tw_layernorm_bwd_workspace_bytes(M, K) (ws may be NULL when dgamma and
+ * dbeta both are).  events: [0] before, [1] after the row kernel, [2] after
+ * the sum of dgamma and dbeta.
+ */
+size_t tw_layernorm_bwd_workspace_bytes(int M, int K);
+tw_status tw_layernorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
+                           int64_t x_stride, const float *gamma, const float *mean,
+                           const float *rstd, const void *dres, int M, int K, void *dx,
+                           int dx_type, float *dgamma, float *dbeta, void *ws, size_t ws_bytes,
+                           void *stream, void *const *events);
+
+/*
+ * 8-bit integer rows.  A row r of K values is held as int8 q and one fp32
+ * scale, with top = max |r|:
+ *     scale = top / 127,   q = round(r * ((1 / top) * 127))
+ * (each operation rounded to fp32; halves go to the even code),
+ * so |q| <= 127 and q * scale approximates r within scale / 2.  A row with
+ * top < 2^-100 gets scale 0 and q = 0; a row holding a NaN or an infinity
+ * gets scale NaN and q = 0 (every product with it is NaN).  Weights take the
+ * same form: row n of w [N][K] holds the weights of output channel n, so
+ * tw_quant_rows over a transposed weight matrix gives one scale per channel.
+ *
+ * tw_quant_rows quantises the rows of x (bf16 or fp32, x_stride elements
+ * apart): q [M][K] int8, scale [M] fp32.  K from 1 to 65536.
+ * tw_layernorm_quant quantises the layer norm of x (+ add) (arguments as in
+ * tw_layernorm_fwd, K up to 16384; the normed row is not rounded in
+ * between).  events: [0] before, [1] after the kernel.
+ */
+tw_status tw_quant_rows(const void *x, int x_type, int64_t x_stride, int M, int K, int8_t *q,
+                        float *scale, void *stream, void *const *events);
+tw_status tw_layernorm_quant(const void *x, int x_type, int64_t x_stride, const void *add,
+                             int add_type, const float *gamma, const float *beta, float eps, int M,
+                             int K, void *sum, int8_t *q, float *scale, void *stream,
+                             void *const *events);
+
+/*
+ * Products of 8-bit integer rows, summed exactly in 32-bit integers:
+ *     p(w)[m][n] = (sum_k q[m][k] w[n][k]) * x_scale[m] * w_scale[n]
+ * tw_quant_linear:  y = p(w) (+ bias)            (y [M][N])
+ * tw_quant_gateup:  h = ReLU(p(wg)) * p(wu)      (h [M][N])
+ * The input x is either rows of int8 (x_type TW_INT8, contiguous, with their
+ * scales in x_scale) or bf16 or fp32 rows x_stride elements apart (x_scale
+ * NULL), which the call quantises first as tw_quant_rows does.  With gamma,
+ * tw_quant_gateup quantises their layer norm instead, as tw_layernorm_quant
+ * does without add (gamma, beta NULL: no norm).
+ *
+ *   w, wg, wu [N][K] int8;  w_scale, g_scale, u_scale [N] fp32
+ *   bias  [N] fp32, or NULL
+ *   y, h  [M][N] bf16 or fp32
+ *   ws    ws_bytes >= tw_quant_workspace_bytes(M, K); may be NULL for int8 x
+ * K a positive multiple of 16, at most 65536 (16384 with gamma); M and N up
+ * to 2^24, and at most 2^37 outputs.  Results are bit-identical run to run.
+ * events: [0] before, [1] after the quantisation, [2] after the product
+ * (events[0] and [1] are recorded together where one kernel does both).
+ */
+size_t tw_quant_workspace_bytes(int M, int K);
+tw_status tw_quant_linear(const void *x, int x_type, int64_t x_stride, const float *x_scale,
+                          const int8_t *w, const float *w_scale, const float *bias, int M, int K,
+                          int N, void *y, int y_type, void *ws, size_t ws_bytes, void *stream,
+                          void *const *events);
+tw_status tw_quant_gateup(const void *x, int x_type, int64_t x_stride, const float *x_scale,
+                          const float *gamma, const float *beta, float eps, const int8_t *wg,
+                          const float *g_scale, const int8_t *wu, const float *u_scale, int M,
+                          int K, int N, void *h, int h_type, void *ws, size_t ws_bytes,
+                          void *stream, void *const *events);
 
 #ifdef __cplusplus
 }
