@@ -3,12 +3,15 @@
 Every HIP source is compiled for gfx950 only, with the packed-fp32 target
 feature switched off (the compiler then never emits packed fp32 add/mul/fma),
 and linked into one shared library exporting the C ABI of ``include/tw.h``.
+``_tw_calls.so``, the native part of the Python binding, is host code compiled
+against the installed torch and linked to that library.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(HERE, "libtw.so")
+CALLS = os.path.join(HERE, "_tw_calls.so")  # native part of the Python binding (csrc/tw_calls.cpp)
 PEAK_PROBE = os.path.join(HERE, "peak_probe")  # achievable-peak program (csrc/peak_probe.hip)
 
 SOURCES = ["gate_twell.hip", "pack_dense.hip", "sparse_updown.hip", "dense_ffn.hip", "hybrid.hip",
@@ -29,16 +33,34 @@ FLAGS = [
 ]
 
 
+def _torch_dir() -> str:
+    import importlib.util
+
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _calls_flags() -> list:
+    inc = os.path.join(_torch_dir(), "include")
+    return ["-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-isystem", inc, "-isystem",
+            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+            sysconfig.get_paths()["include"]]
+
+
 def build(verbose: bool = False) -> str:
-    """Compile all sources (in parallel) and link ``libtw.so``; returns its path."""
+    """Compile all sources (in parallel) and link ``libtw.so`` and, to it,
+    ``_tw_calls.so``; returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     procs = []
     objs = []
-    for src in SOURCES:
+    calls_obj = os.path.join(BUILD_DIR, "tw_calls.cpp.o")
+    for src in ["tw_calls.cpp"] + SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
-        objs.append(obj)
-        lang = ["-x", "hip"] if src.endswith(".cpp") else []
-        cmd = [HIPCC, *FLAGS, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+        if obj == calls_obj:
+            flags = _calls_flags()
+        else:
+            objs.append(obj)
+            flags = FLAGS + (["-x", "hip"] if src.endswith(".cpp") else [])
+        cmd = [HIPCC, *flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
@@ -57,6 +79,14 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIBRARY)
+    tmp = CALLS + ".tmp"
+    cmd = [HIPCC, "-shared", "-fPIC", calls_obj, "-o", tmp, "-L", HERE, "-l:libtw.so", "-L",
+           os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_hip",
+           "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALLS)
     return LIBRARY
 
 

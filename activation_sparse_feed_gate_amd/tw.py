@@ -37,6 +37,11 @@ if not os.path.exists(LIBRARY):
         f"{LIBRARY} is missing: build it with `python -m activation_sparse_feed_gate_amd.build`")
 
 _lib = ctypes.CDLL(LIBRARY)
+# The small allocating calls (layernorm, quant_linear, ...) in native code: it
+# checks, allocates and calls the library, and returns None for any argument
+# that is not as the library needs it; the call is then made through the
+# low-level function here, whose checks raise.
+from . import _tw_calls as _calls  # noqa: E402  (built beside the library)
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -864,6 +869,9 @@ def layernorm(x, gamma, beta=None, eps=1e-5, add=None, out_dtype=torch.bfloat16)
     """Layer norm of the rows of x (+ add).  Returns a dict: y, mean and rstd
     (fp32, for ``layernorm_backward``), and sum = x + add in x's type (None
     without add)."""
+    got = _calls.layernorm(x, gamma, beta, eps, add, out_dtype)
+    if got is not None:
+        return dict(zip(("y", "sum", "mean", "rstd"), got))
     M, K = _dims2(x, "x", "layernorm")
     dev = x.device
     out = {
@@ -881,6 +889,9 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dres=None, dx_dtype=torch.float
     """Gradient of ``layernorm``: x is its input (``sum`` if there was an
     add), dres the gradient reaching x past the norm (dx's dtype).  Returns a
     dict with dx, dgamma, dbeta."""
+    got = _calls.layernorm_backward(dy, x, gamma, mean, rstd, dres, dx_dtype)
+    if got is not None:
+        return dict(zip(("dx", "dgamma", "dbeta"), got))
     M, K = _dims2(x, "x", "layernorm_backward")
     dev = x.device
     out = {
@@ -926,6 +937,9 @@ def _quant_ws(x):
 def quant_linear(x, w, w_scale, bias=None, x_scale=None, out_dtype=torch.bfloat16, ws=None):
     """y = x w^T (+ bias) on int8 operands: x is bf16 or fp32 (quantised by
     the call) or int8 with x_scale; w [N][K] int8 with w_scale [N]."""
+    got = _calls.quant_linear(x, w, w_scale, bias, x_scale, out_dtype, ws)
+    if got is not None:
+        return got[0]
     M, N = _dims2(x, "x", "quant_linear")[0], _dims2(w, "w", "quant_linear")[0]
     y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     tw_quant_linear(x, w, w_scale, y, bias=bias, x_scale=x_scale,
@@ -937,6 +951,10 @@ def quant_gateup(x, wg, g_scale, wu, u_scale, gamma=None, beta=None, eps=1e-5, x
                  out_dtype=torch.bfloat16, ws=None):
     """h = ReLU(n wg^T) * (n wu^T) on int8 operands, n the layer norm of x
     (gamma given) or x itself; x as in ``quant_linear``."""
+    got = _calls.quant_gateup(x, wg, g_scale, wu, u_scale, gamma, beta, eps, x_scale, out_dtype,
+                              ws)
+    if got is not None:
+        return got[0]
     M, N = _dims2(x, "x", "quant_gateup")[0], _dims2(wg, "wg", "quant_gateup")[0]
     h = torch.empty((M, N), dtype=out_dtype, device=x.device)
     tw_quant_gateup(x, wg, g_scale, wu, u_scale, h, gamma=gamma, beta=beta, eps=eps,
