@@ -17,6 +17,8 @@
 // in registers; the workgroups' shares go to the workspace and a second
 // kernel adds them in a fixed order (no atomics: results do not depend on
 // timing).
+#include <type_traits>
+
 #include "tw_rows.hpp"
 
 namespace tw {
@@ -171,13 +173,32 @@ struct NormBwdArgs {
     int M, K;
     char *dx;
     int dx_type;
-    float *part;  // [gridDim.x][2][K] shares of dgamma and dbeta, or null
+    float *part;  // [gridDim.x][2][KP] shares of dgamma and dbeta, or null
 };
 
+// Columns of a share: K rounded up to what the threads of a row hold, so that
+// shares are stored and summed without regard to where K ends.
+// Measured: a wave a row up to K = 1024 (16384 x 1024 bf16: 35 us); at 2048 a
+// workgroup a row takes 103 us for 16384 fp32 rows with dres (5.2 TB/s), a
+// wave a row 150 (its registers hold too little besides the sums).
+constexpr int norm_bwd_tpr(int K) { return K <= 1024 ? 64 : K <= 4096 ? 256 : 512; }
+constexpr int norm_bwd_vpt(int K) {
+    return K <= 512 ? 1 : K <= 1024 ? 2 : K <= 2048 ? 1 : K <= 8192 ? 2 : 4;
+}
+constexpr int norm_bwd_threads(int K) {
+    return norm_bwd_tpr(K) > kNormThreads ? norm_bwd_tpr(K) : kNormThreads;
+}
+constexpr int norm_bwd_cols(int K) { return norm_bwd_tpr(K) * norm_bwd_vpt(K) * 8; }
+
+// While a row is reduced and written the next one's loads are in flight: the
+// column sums leave room for few waves, too few to hide the loads behind each
+// other.
 template <int TD, int TX, int TPR, int VPT>
-__global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(NormBwdArgs a) {
-    constexpr int RPB = kNormThreads / TPR;
-    extern __shared__ __attribute__((aligned(16))) float share[];  // 2 K floats (TPR == 64)
+__global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, 2)
+void norm_bwd_kernel(NormBwdArgs a) {
+    constexpr int RPB = TPR > kNormThreads ? 1 : kNormThreads / TPR;
+    constexpr int KP = TPR * VPT * 8;
+    extern __shared__ __attribute__((aligned(16))) float share[];  // [RPB][2][KP] (TPR == 64)
     __shared__ float red[2 * (TPR / kWave)];
     RowReduce<TPR> rr(red);
     const int t = threadIdx.x % TPR;
@@ -187,31 +208,42 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) dg[v][i] = db[v][i] = 0.0f;
 
-    for (int64_t m = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; m < a.M;
-         m += (int64_t)gridDim.x * RPB) {
+    Vec8<TD> dv[VPT];
+    Vec8<TX> xv[VPT];
+    float mean = 0.0f, rstd = 0.0f;
+    auto fetch = [&](int64_t m) {
         const char *dr = a.dy + m * a.K * type_bytes(TD);
         const char *xr = a.x + m * a.x_stride * type_bytes(TX);
-        Vec8<TD> dv[VPT];
-        Vec8<TX> xv[VPT];
+        mean = a.mean[m];
+        rstd = a.rstd[m];
 #pragma unroll
         for (int v = 0; v < VPT; ++v) dv[v] = load8<TD>(dr, 8 * (v * TPR + t), a.K);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) xv[v] = load8<TX>(xr, 8 * (v * TPR + t), a.K);
-        const float mean = a.mean[m], rstd = a.rstd[m];
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t m = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (m < a.M) fetch(m);
+    for (; m < a.M; m += step) {
+        const float r = rstd;
         float n[VPT][8], g[VPT][8];
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            unpack8<TD>(dv[v], g[v]);
+            unpack8<TX>(xv[v], n[v]);
+            // past the end dy = gamma = 0, and n is finite unless the whole
+            // row's statistics are not
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[v][i] = (n[v][i] - mean) * r;
+        }
+        if (m + step < a.M) fetch(m + step);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int e = 8 * (v * TPR + t);
             float gm[8];
-            unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.gamma, e, a.K), gm);
-            unpack8<TD>(dv[v], g[v]);
-            unpack8<TX>(xv[v], n[v]);
+            unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.gamma, 8 * (v * TPR + t), a.K), gm);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                // past the end dy = gamma = 0: only n has to be cleared (it
-                // may be infinite where mean is)
-                n[v][i] = e + i < a.K ? (n[v][i] - mean) * rstd : 0.0f;
                 dg[v][i] += g[v][i] * n[v][i];
                 db[v][i] += g[v][i];
                 g[v][i] *= gm[i];
@@ -224,85 +256,93 @@ __global__ __launch_bounds__(kNormThreads) void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int e = 8 * (v * TPR + t);
-            float r[8];
+            float d[8];
             if (a.dres) {
                 const char *rrow = a.dres + m * a.K * ds;
-                if (a.dx_type == TW_T_F32) unpack8<TW_T_F32>(load8<TW_T_F32>(rrow, e, a.K), r);
-                else unpack8<TW_T_BF16>(load8<TW_T_BF16>(rrow, e, a.K), r);
+                if (a.dx_type == TW_T_F32) unpack8<TW_T_F32>(load8<TW_T_F32>(rrow, e, a.K), d);
+                else unpack8<TW_T_BF16>(load8<TW_T_BF16>(rrow, e, a.K), d);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                g[v][i] = rstd * (g[v][i] - c1 - n[v][i] * c2) + (a.dres ? r[i] : 0.0f);
+                g[v][i] = r * (g[v][i] - c1 - n[v][i] * c2) + (a.dres ? d[i] : 0.0f);
             store8_as(a.dx_type, a.dx + m * a.K * ds, e, a.K, g[v]);
         }
     }
     if (!a.part) return;
 
-    // the workgroup's share: its waves add theirs in wave order
-    float *pg = a.part + (size_t)blockIdx.x * 2 * a.K, *pb = pg + a.K;
+    // the workgroup's share: its waves' column sums, added in wave order
+    float *pg = a.part + (size_t)blockIdx.x * 2 * KP;
     if constexpr (TPR == kWave) {
-        const int wave = threadIdx.x / kWave;
-        for (int w = 0; w < RPB; ++w) {
-            if (wave == w) {
+        float *mine = share + (threadIdx.x / kWave) * 2 * KP;
 #pragma unroll
-                for (int v = 0; v < VPT; ++v)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int e = 8 * (v * TPR + t) + i;
-                        if (e >= a.K) continue;
-                        share[e] = w ? share[e] + dg[v][i] : dg[v][i];
-                        share[a.K + e] = w ? share[a.K + e] + db[v][i] : db[v][i];
-                    }
-            }
-            __syncthreads();
+        for (int v = 0; v < VPT; ++v) {
+            store8<TW_T_F32>((char *)mine, 8 * (v * TPR + t), KP, dg[v]);
+            store8<TW_T_F32>((char *)(mine + KP), 8 * (v * TPR + t), KP, db[v]);
         }
-        for (int e = threadIdx.x; e < 2 * a.K; e += kNormThreads) pg[e] = share[e];
+        __syncthreads();
+        for (int e = 4 * threadIdx.x; e < 2 * KP; e += 4 * kNormThreads) {
+            f32x4 s = *reinterpret_cast<const f32x4 *>(share + e);
+#pragma unroll
+            for (int w = 1; w < RPB; ++w) s += *reinterpret_cast<const f32x4 *>(share + w * 2 * KP + e);
+            *reinterpret_cast<f32x4 *>(pg + e) = s;
+        }
     } else {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            store8<TW_T_F32>((char *)pg, 8 * (v * TPR + t), a.K, dg[v]);
-            store8<TW_T_F32>((char *)pb, 8 * (v * TPR + t), a.K, db[v]);
+            store8<TW_T_F32>((char *)pg, 8 * (v * TPR + t), KP, dg[v]);
+            store8<TW_T_F32>((char *)(pg + KP), 8 * (v * TPR + t), KP, db[v]);
         }
     }
 }
 
-// dgamma and dbeta from the workgroups' shares: 32 columns a workgroup, 32
-// threads a column, each adding every 32nd share; then their sums in order.
+// dgamma (blockIdx.y 0) and dbeta (1) from the workgroups' shares: 32 columns
+// a workgroup, 32 threads a column, each adding every 32nd share; then their
+// sums in order.
 constexpr int kColsPerBlock = 32, kColThreads = 32;
 __global__ __launch_bounds__(kColsPerBlock *kColThreads) void norm_cols_kernel(
-    const float *__restrict__ part, int G, int K, float *__restrict__ dgamma,
+    const float *__restrict__ part, int G, int K, int KP, float *__restrict__ dgamma,
     float *__restrict__ dbeta) {
+    float *out = blockIdx.y ? dbeta : dgamma;
+    if (!out) return;
     __shared__ float s[kColThreads][kColsPerBlock + 1];
     const int c = threadIdx.x % kColsPerBlock, r = threadIdx.x / kColsPerBlock;
-    const int64_t col = (int64_t)blockIdx.x * kColsPerBlock + c;
+    const int col = blockIdx.x * kColsPerBlock + c;  // below KP, a multiple of 32
+    const float *p = part + (size_t)blockIdx.y * KP + col;
     float v = 0.0f;
-    if (col < 2 * (int64_t)K)
-#pragma unroll 4
-        for (int g = r; g < G; g += kColThreads) v += part[(size_t)g * 2 * K + col];
+#pragma unroll 8
+    for (int g = r; g < G; g += kColThreads) v += p[(size_t)g * 2 * KP];
     s[r][c] = v;
     __syncthreads();
-    if (r == 0 && col < 2 * (int64_t)K) {
+    if (r == 0 && col < K) {
         v = 0.0f;
 #pragma unroll
         for (int i = 0; i < kColThreads; ++i) v += s[i][c];
-        float *out = col < K ? dgamma : dbeta;
-        if (out) out[col < K ? col : col - K] = v;
+        out[col] = v;
     }
+}
+
+template <int TD, int TX, int TPR, int VPT>
+hipError_t launch_bwd(const NormBwdArgs &a, int grid, hipStream_t s) {
+    constexpr auto kernel = &norm_bwd_kernel<TD, TX, TPR, VPT>;
+    constexpr int lds = TPR == kWave ? kNormThreads / TPR * 2 * TPR * VPT * 8 * 4 : 0;
+    const hipError_t e = lds_limit_once<kernel>(lds);
+    if (e != hipSuccess) return e;
+    kernel<<<grid, TPR > kNormThreads ? TPR : kNormThreads, a.part ? lds : 0, s>>>(a);
+    return hipGetLastError();
 }
 
 template <int TD, int TX>
 hipError_t launch_bwd(const NormBwdArgs &a, int grid, hipStream_t s) {
-    const size_t lds = a.part && a.K <= 2048 ? (size_t)a.K * 8 : 0;
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kNormThreads, lds, s>>>(a);
-        return hipGetLastError();
+    auto go = [&](auto k) {
+        constexpr int K = decltype(k)::value;
+        return launch_bwd<TD, TX, norm_bwd_tpr(K), norm_bwd_vpt(K)>(a, grid, s);
     };
-    if (a.K <= 512) return go(norm_bwd_kernel<TD, TX, 64, 1>);
-    if (a.K <= 1024) return go(norm_bwd_kernel<TD, TX, 64, 2>);
-    if (a.K <= 2048) return go(norm_bwd_kernel<TD, TX, 64, 4>);
-    if (a.K <= 4096) return go(norm_bwd_kernel<TD, TX, 256, 2>);
-    if (a.K <= 8192) return go(norm_bwd_kernel<TD, TX, 256, 4>);
-    return go(norm_bwd_kernel<TD, TX, 256, 8>);
+    if (a.K <= 512) return go(std::integral_constant<int, 512>{});
+    if (a.K <= 1024) return go(std::integral_constant<int, 1024>{});
+    if (a.K <= 2048) return go(std::integral_constant<int, 2048>{});
+    if (a.K <= 4096) return go(std::integral_constant<int, 4096>{});
+    if (a.K <= 8192) return go(std::integral_constant<int, 8192>{});
+    return go(std::integral_constant<int, 16384>{});
 }
 
 }  // namespace
@@ -333,10 +373,21 @@ hipError_t launch_quant_rows(const void *x, int x_type, int64_t x_stride, int M,
     return launch_rows<TW_T_BF16, -1, kQuant>(a, s);
 }
 
-int layernorm_bwd_groups(int M, int K) {
-    const int rpb = K <= 2048 ? kNormThreads / kWave : 1;
+// Workgroups of the row kernel.  Each writes a share of 2 KP floats that the
+// column sums read again, so their number is kept to what fills the chip: 2 a
+// CU, 1 of 512 threads, 3 where every one still walks 16 rows or more.
+// Measured (us at 256, 512, 768, 1024): 16384 x 2048 fp32 139, 103, 104, 108;
+// the same bf16 91, 55, 48, 48; 4096 x 2048 25.9, 22.4, 24.5, 26.6; 4096 x 8192
+// bf16 57, 64, 72, 79.
+static int norm_bwd_groups(int M, int K) {
+    const int rpb = norm_bwd_threads(K) / norm_bwd_tpr(K);
     const int64_t need = ((int64_t)M + rpb - 1) / rpb;
-    return (int)(need < 1 ? 1 : need < 512 ? need : 512);
+    const int most = norm_bwd_threads(K) > kNormThreads ? 256 : M >= 16 * 768 ? 768 : 512;
+    return (int)(need < 1 ? 1 : need < most ? need : most);
+}
+
+size_t layernorm_bwd_bytes(int M, int K) {
+    return (size_t)norm_bwd_groups(M, K) * 2 * norm_bwd_cols(K) * 4;
 }
 
 hipError_t launch_layernorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
@@ -344,7 +395,7 @@ hipError_t launch_layernorm_bwd(const void *dy, int dy_type, const void *x, int 
                                 const float *rstd, const void *dres, int M, int K, void *dx,
                                 int dx_type, float *dgamma, float *dbeta, float *part,
                                 hipStream_t s, hipEvent_t ev_rows) {
-    const int grid = layernorm_bwd_groups(M, K);
+    const int grid = norm_bwd_groups(M, K);
     NormBwdArgs a{(const char *)dy, (const char *)x, (const char *)dres, x_stride, gamma, mean,
                   rstd, M, K, (char *)dx, dx_type, dgamma || dbeta ? part : nullptr};
     hipError_t e = hipSuccess;
@@ -356,8 +407,9 @@ hipError_t launch_layernorm_bwd(const void *dy, int dy_type, const void *x, int 
                                       : launch_bwd<TW_T_BF16, TW_T_BF16>(a, grid, s));
     if (e == hipSuccess && ev_rows) e = hipEventRecord(ev_rows, s);
     if (e != hipSuccess || !a.part) return e;
-    const int blocks = (2 * K + kColsPerBlock - 1) / kColsPerBlock;
-    norm_cols_kernel<<<blocks, kColsPerBlock * kColThreads, 0, s>>>(part, grid, K, dgamma, dbeta);
+    const dim3 blocks((K + kColsPerBlock - 1) / kColsPerBlock, 2);
+    norm_cols_kernel<<<blocks, kColsPerBlock * kColThreads, 0, s>>>(part, grid, K,
+                                                                    norm_bwd_cols(K), dgamma, dbeta);
     return hipGetLastError();
 }
 

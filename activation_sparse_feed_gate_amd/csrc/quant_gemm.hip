@@ -64,70 +64,318 @@ __device__ __forceinline__ void put(char *y, int type, size_t o, float v) {
 }
 
 // ------------------------------- a few rows --------------------------------
+// 16 weight rows a workgroup, MB blocks of 16 token rows; wave w of 8 takes
+// the 64-element steps w, w + 8, ... of K, and the waves' sums meet in LDS.
+// The time of such a product is the latency of its loads and then the weight
+// stream, so a wave issues the loads of PF of its steps (weights and token
+// rows) at once, after the few small ones that are waited for first: loads
+// complete in order.
+//
+// The token rows come either as int8, read per fragment from memory (every
+// workgroup reads them, mostly from L2), or, for up to 4 rows, as floats that
+// each workgroup norms and quantises itself into LDS while its weights are on
+// their way: that saves the quantiser's launch and the wait between the two.
 constexpr int kFewWaves = 8;
+constexpr int kFewPad = 16;  // bytes between quantised rows in LDS: shifts banks
 
-// 16 weight rows a workgroup, MB blocks of 16 token rows; wave w takes the
-// 64-element steps w, w + 8, ... of K.
-template <int MB, int NB>
-__global__ __launch_bounds__(kFewWaves *kWave) void quant_few_kernel(QArgs a) {
-    __shared__ __attribute__((aligned(16))) i32x4 part[NB][kFewWaves][MB][kWave];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16;
-    const int l16 = lane & 15, kc = (lane >> 4) * 16;
-    const int8_t *wr[NB];
+struct FewRows {
+    const char *x;
+    int64_t x_stride;
+    const float *gamma, *beta;  // gamma null: no norm
+    float eps;
+};
+
+// Fused rows: WPR waves share a token row, 8 / WPR rows at once; a thread
+// holds up to 2 vectors of 8 elements of its row.
+constexpr int kFusedRows = 4;
+__host__ __device__ constexpr int fused_row_waves(int M) { return M <= 1 ? 8 : M <= 2 ? 4 : 2; }
+constexpr int fused_max_k(int M) { return fused_row_waves(M) * kWave * 16; }
+
+// The norm and quantisation of one row by WPR waves (all 8 waves take part;
+// a group past the last row repeats it).  The loads are issued by the
+// constructor, the rest is done by run().
+template <int TX, int WPR, int VEC>
+struct FusedRow {
+    const FewRows &f;
+    const int K, t;
+    Vec8<TX> raw[VEC];
+    Vec8<TW_T_F32> g[VEC], b[VEC];
+    int slot = 0;
+
+    __device__ __forceinline__ int at(int v) const { return 8 * (v * WPR * kWave + t); }
+    __device__ __forceinline__ FusedRow(const FewRows &f_, int m, int K_)
+        : f(f_), K(K_), t(threadIdx.x & (WPR * kWave - 1)) {
+        const char *row = f.x + (int64_t)m * f.x_stride * type_bytes(TX);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) wr[b] = a.w[b].w + (size_t)min(n0 + l16, a.N - 1) * a.K;
-    const int8_t *xr[MB];
+        for (int v = 0; v < VEC; ++v) raw[v] = load8<TX>(row, at(v), K);
+        if (f.gamma) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) xr[i] = a.q + (size_t)min(i * 16 + l16, a.M - 1) * a.K;
-    i32x4 acc[NB][MB];
+            for (int v = 0; v < VEC; ++v) g[v] = load8<TW_T_F32>((const char *)f.gamma, at(v), K);
+        }
+        if (f.beta) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < MB; ++i) acc[b][i] = i32x4{};
-    const int steps = (a.K + 63) / 64;
-#pragma unroll 2
-    for (int s = wave; s < steps; s += kFewWaves) {
-        const int k = s * 64 + kc;
-        const bool in = k < a.K;  // K is a multiple of 16: a chunk is in or out
-        const int kk = in ? k : 0;
-        u32x4 wf[NB], xf[MB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) wf[b] = ld16(wr[b] + kk);
-#pragma unroll
-        for (int i = 0; i < MB; ++i) xf[i] = ld16(xr[i] + kk);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            if (!in) wf[b] = u32x4{};
-#pragma unroll
-            for (int i = 0; i < MB; ++i) acc[b][i] = mfma16_i8(wf[b], xf[i], acc[b][i]);
+            for (int v = 0; v < VEC; ++v) b[v] = load8<TW_T_F32>((const char *)f.beta, at(v), K);
         }
     }
+    // op over the row's WPR waves of their (uniform) values v; two slots of
+    // red in turn, so one barrier each is enough (see RowReduce)
+    template <typename Op>
+    __device__ __forceinline__ float over_waves(float v, float *red, Op op) {
+        float *r = red + slot * kFewWaves;
+        slot ^= 1;
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) r[wave] = v;
+        __syncthreads();
+        const int first = wave & ~(WPR - 1);
+        float a = r[first];
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) a = op(a, r[first + w]);
+        return a;
+    }
+    __device__ __forceinline__ void run(float *red, int8_t *dst, float *scale) {
+        auto add = [](float a, float b) { return a + b; };
+        float z[VEC][8];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) unpack8<TX>(raw[v], z[v]);
+        if (f.gamma) {
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += z[v][i];
+            const float mean = over_waves(wave_sum(s), red, add) / K;
+            s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    z[v][i] = at(v) < K ? z[v][i] - mean : 0.0f;  // K is a multiple of 8
+                    s += z[v][i] * z[v][i];
+                }
+            const float rstd = 1.0f / sqrtf(over_waves(wave_sum(s), red, add) / K + f.eps);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float gf[8], bf[8];
+                unpack8<TW_T_F32>(g[v], gf);
+                if (f.beta) unpack8<TW_T_F32>(b[v], bf);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    z[v][i] = z[v][i] * rstd * gf[i] + (f.beta ? bf[i] : 0.0f);
+            }
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(z[v][i]) & 0x7fffffffu);
+        // magnitudes compare as unsigned integers, NaN above all (row_scale)
+        top = __float_as_uint(
+            over_waves(__uint_as_float(wave_max(top)), red, [](float a, float b) {
+                return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+            }));
+        const RowScale rs = row_scale(top);
+        if (t == 0) *scale = rs.scale;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+            if (at(v) < K) *reinterpret_cast<u32x2 *>(dst + at(v)) = quant8(z[v], rs.inv);
+    }
+};
+
+// MB x NC blocks of 16 token rows by 16 weight rows a workgroup.  WPR, VEC:
+// of the fused rows (0: int8 rows).
+// Waves a SIMD the registers leave room for: the loads in flight, the sums
+// and a fused row's vectors take most of them (128 registers at 4 waves, 256
+// at 2).
+constexpr int few_waves(int loads, int sums, int vec) {
+    return 4 * (loads + sums + 6 * vec) <= 72 ? 4 : 2;
+}
+
+template <int TX, int WPR, int VEC, int MB, int NC, int NB, int PF>
+__global__ __launch_bounds__(kFewWaves *kWave,
+                             few_waves(PF *(NB * NC + (TX == TW_T_INT8 ? MB : 0)), NB *NC *MB,
+                                       VEC))
+void quant_few_kernel(QArgs a, FewRows f) {
+    constexpr bool kFused = TX != TW_T_INT8;
+    static_assert(!kFused || MB == 1, "fused rows: one block of 16");
+    extern __shared__ __attribute__((aligned(16))) char few_smem[];
+    // [NB][NC][MB][waves][64] sums; then, fused, the rows' bytes
+    i32x4 *part = reinterpret_cast<i32x4 *>(few_smem);
+    int8_t *rows = reinterpret_cast<int8_t *>(part + NB * NC * MB * kFewWaves * kWave);
+    __shared__ float red[2 * kFewWaves], row_scales[kFusedRows];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * (16 * NC), m0 = blockIdx.y * (16 * MB);
+    const int l16 = lane & 15, kc = (lane >> 4) * 16;
+    const int steps = (a.K + 63) / 64;
+
+    const int8_t *wr[NB][NC], *xr[MB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int i = 0; i < MB; ++i) part[b][wave][i][lane] = acc[b][i];
+        for (int c = 0; c < NC; ++c)
+            wr[b][c] = a.w[b].w + (size_t)min(n0 + 16 * c + l16, a.N - 1) * a.K;
+    u32x4 wf[PF][NB][NC], xf[PF][kFused ? 1 : MB];
+    // The wave's steps p0 .. p0 + PF - 1 of K (step p is p * 8 + wave): chunks
+    // past a row's end read its first bytes instead, and the weights' are
+    // then cleared (K is a multiple of 16: a chunk is in or out).
+    auto fetch = [&](int p0) {
+#pragma unroll
+        for (int p = 0; p < PF; ++p) {
+            // no branch around loads that are in flight while the fused rows
+            // are waited for: the wait could not count them
+            if (!kFused && (p0 + p) * kFewWaves + wave >= steps) continue;
+            const int k = ((p0 + p) * kFewWaves + wave) * 64 + kc;
+            const int kk = k < a.K ? k : 0;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) wf[p][b][c] = ld16(wr[b][c] + kk);
+            if constexpr (!kFused) {
+#pragma unroll
+                for (int i = 0; i < MB; ++i) xf[p][i] = ld16(xr[i] + kk);
+            }
+        }
+    };
+    if constexpr (kFused) {
+        const int m = min(wave / WPR, a.M - 1);
+        const int stride = a.K + kFewPad;
+        FusedRow<TX, WPR, VEC> row(f, m, a.K);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(0);
+        __builtin_amdgcn_sched_barrier(0);
+        row.run(red, rows + m * stride, row_scales + m);
+        __syncthreads();
+        xr[0] = rows + min(l16, a.M - 1) * stride;
+    } else {
+#pragma unroll
+        for (int i = 0; i < MB; ++i) xr[i] = a.q + (size_t)min(m0 + i * 16 + l16, a.M - 1) * a.K;
+        fetch(0);
+    }
+    i32x4 acc[NB][NC][MB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < MB; ++i) acc[b][c][i] = i32x4{};
+    for (int p0 = 0; p0 * kFewWaves + wave < steps; p0 += PF) {
+        if (p0) fetch(p0);
+#pragma unroll
+        for (int p = 0; p < PF; ++p) {
+            if ((p0 + p) * kFewWaves + wave >= steps) continue;
+            const int k = ((p0 + p) * kFewWaves + wave) * 64 + kc;
+            const bool in = k < a.K;
+            if constexpr (kFused)
+                xf[p][0] = *reinterpret_cast<const u32x4 *>(xr[0] + (in ? k : 0));
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const u32x4 w = in ? wf[p][b][c] : u32x4{};
+#pragma unroll
+                    for (int i = 0; i < MB; ++i) acc[b][c][i] = mfma16_i8(w, xf[p][i], acc[b][c][i]);
+                }
+        }
+    }
+    // what the outputs need besides the sums: the lane's 4 columns, on their
+    // way while the sums meet (a wave finishes blocks wave, wave + 8, ...)
+    constexpr int kBlocks = MB * NC;
+    auto place = [&](int b, int blk, int w) {
+        return ((b * kBlocks + blk) * kFewWaves + w) * kWave + lane;
+    };
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < MB; ++i) part[place(b, c * MB + i, wave)] = acc[b][c][i];
+    if (wave >= kBlocks) return __syncthreads();
+    float ws[NB][4], bias[4], xs;
+    auto columns = [&](int blk) {
+        const int nl = n0 + 16 * (blk / MB) + 4 * (lane >> 4);
+        const int m = m0 + 16 * (blk % MB) + l16;
+        xs = kFused ? 0.0f : a.x_scale[min(m, a.M - 1)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = min(nl + j, a.N - 1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) ws[b][j] = a.w[b].scale[n];
+            bias[j] = NB == 1 && a.bias ? a.bias[n] : 0.0f;
+        }
+    };
+    columns(wave);
     __syncthreads();
-    // one lane position of one row block per thread: 4 outputs of one row
-    for (int i = wave; i < MB; i += kFewWaves) {
+    for (int blk = wave; blk < kBlocks; blk += kFewWaves) {
+        if (blk != wave) columns(blk);
+        const int nl = n0 + 16 * (blk / MB) + 4 * (lane >> 4);
+        const int m = m0 + 16 * (blk % MB) + l16;
         i32x4 s[2] = {};
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int w = 0; w < kFewWaves; ++w) s[b] += part[b][w][i][lane];
-        const int m = i * 16 + l16;
+            for (int w = 0; w < kFewWaves; ++w) s[b] += part[place(b, blk, w)];
         if (m >= a.M) continue;
-        const float xs = a.x_scale[m];
+        if (kFused) xs = row_scales[m];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + 4 * (lane >> 4) + j;
-            if (n >= a.N) continue;
-            put(a.y, a.y_type, (size_t)m * a.N + n,
-                finish<NB>(s[0][j], s[1][j], xs, a.w[0].scale[n], NB == 2 ? a.w[1].scale[n] : 0.0f,
-                           NB == 1 && a.bias ? a.bias[n] : 0.0f));
-        }
+        for (int j = 0; j < 4; ++j)
+            if (nl + j < a.N)
+                put(a.y, a.y_type, (size_t)m * a.N + nl + j,
+                    finish<NB>(s[0][j], s[1][j], xs, ws[0][j], ws[NB - 1][j], bias[j]));
     }
+}
+
+template <int TX, int WPR, int VEC, int MB, int NC, int NB, int PF>
+hipError_t launch_few(const QArgs &a, const FewRows &f, hipStream_t s) {
+    constexpr auto kernel = &quant_few_kernel<TX, WPR, VEC, MB, NC, NB, PF>;
+    constexpr int sums = NB * NC * MB * kFewWaves * kWave * 16;
+    constexpr int most = TX == TW_T_INT8 ? 0 : kFusedRows * (VEC * WPR * kWave * 8 + kFewPad);
+    const hipError_t e = lds_limit_once<kernel>(sums + most);
+    if (e != hipSuccess) return e;
+    const int lds = sums + (TX != TW_T_INT8 ? a.M * (a.K + kFewPad) : 0);
+    const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), (a.M + 16 * MB - 1) / (16 * MB));
+    kernel<<<grid, kFewWaves * kWave, lds, s>>>(a, f);
+    return hipGetLastError();
+}
+
+// Loads of a wave in flight: its whole share of K where that is short, else
+// as many steps as the registers hold.
+template <int TX, int WPR, int VEC, int MB, int NC, int NB>
+hipError_t launch_few(const QArgs &a, const FewRows &f, hipStream_t s) {
+    constexpr int loads = NB * NC + (TX == TW_T_INT8 ? MB : 0);
+    constexpr int most = 36 / loads < 12 ? 36 / loads : 12;
+    const int share = (a.K + kFewWaves * 64 - 1) / (kFewWaves * 64);
+    if constexpr (most > 2)
+        if (share <= 2) return launch_few<TX, WPR, VEC, MB, NC, NB, 2>(a, f, s);
+    if constexpr (most > 4)
+        if (share <= 4) return launch_few<TX, WPR, VEC, MB, NC, NB, 4>(a, f, s);
+    return launch_few<TX, WPR, VEC, MB, NC, NB, most>(a, f, s);
+}
+
+// A CU runs one workgroup of these well; a second one on the same CU, or a
+// second round, costs about as much as the first.  So the block grows (which
+// also has the token rows read by fewer workgroups) until the grid is at most
+// one workgroup a CU.
+constexpr int kFewGrid = 256;
+inline bool few_fits(int M, int N, int MB, int NC) {
+    return ((int64_t)M + 16 * MB - 1) / (16 * MB) * (((int64_t)N + 16 * NC - 1) / (16 * NC)) <=
+           kFewGrid;
+}
+
+template <int TX, int WPR, int NB>
+hipError_t launch_fused(const QArgs &a, const FewRows &f, hipStream_t s) {
+    const bool one = few_fits(a.M, a.N, 1, 1);
+    if (a.K <= WPR * kWave * 8)
+        return one ? launch_few<TX, WPR, 1, 1, 1, NB>(a, f, s)
+                   : launch_few<TX, WPR, 1, 1, 2, NB>(a, f, s);
+    return one ? launch_few<TX, WPR, 2, 1, 1, NB>(a, f, s)
+               : launch_few<TX, WPR, 2, 1, 2, NB>(a, f, s);
+}
+
+template <int TX, int NB>
+hipError_t launch_fused(const QArgs &a, const FewRows &f, hipStream_t s) {
+    if (a.M == 1) return launch_fused<TX, fused_row_waves(1), NB>(a, f, s);
+    if (a.M == 2) return launch_fused<TX, fused_row_waves(2), NB>(a, f, s);
+    return launch_fused<TX, fused_row_waves(kFusedRows), NB>(a, f, s);
 }
 
 // ------------------------------- many rows ---------------------------------
@@ -271,18 +519,28 @@ hipError_t launch_tiles(const QArgs &a, hipStream_t s) {
 template <int NB>
 hipError_t launch_product(const QArgs &a, hipStream_t s) {
     if (a.M == 0) return hipSuccess;
-    const int few = (a.N + 15) / 16;
-    if (a.M <= 16) {
-        quant_few_kernel<1, NB><<<few, kFewWaves * kWave, 0, s>>>(a);
-        return hipGetLastError();
-    }
-    if (a.M <= 32) {
-        quant_few_kernel<2, NB><<<few, kFewWaves * kWave, 0, s>>>(a);
-        return hipGetLastError();
-    }
     auto tiles = [&](int bm, int bn) {
         return ((int64_t)a.M + bm - 1) / bm * (((int64_t)a.N + bn - 1) / bn);
     };
+    // Up to 64 rows per 128 columns or so: the smallest block whose grid fits.
+    // Measured (us, K = 2048, N = 1001; K = 5632, N = 2048; K = 2048, N = 5632):
+    //   32 rows   16x16 4.0, 7.7, 8.0   32x16 4.9, 10.1, 8.0   32x32 5.9, 13.0, 6.4
+    //   64 rows   16x16 4.3, 12.4, 13.3   32x16 5.0, 10.1, 10.8   64x32 8.1, 18.6, 8.8
+    //   128 rows  32x16 5.3, 18.8, 19.0   32x32 6.0, 13.1, 13.8   tiles 8.8, 16.8, 9.4
+    // Where none fits, 64 x 64 tiles, unless they would leave most CUs idle
+    // and the rows are few (N = 8192, K = 2048, 16 rows: 16x32 5.7, tiles 8.6;
+    // N = 14336, K = 4096: 15.9 against 13.0).
+    const FewRows none{};
+    if (a.M <= 16 && few_fits(a.M, a.N, 1, 1))
+        return launch_few<TW_T_INT8, 0, 0, 1, 1, NB>(a, none, s);
+    if (a.M <= 16 && (few_fits(a.M, a.N, 1, 2) || a.M <= 4 || tiles(64, 64) < 192))
+        return launch_few<TW_T_INT8, 0, 0, 1, 2, NB>(a, none, s);
+    if (few_fits(a.M, a.N, 1, 1)) return launch_few<TW_T_INT8, 0, 0, 1, 1, NB>(a, none, s);
+    if (few_fits(a.M, a.N, 2, 1)) return launch_few<TW_T_INT8, 0, 0, 2, 1, NB>(a, none, s);
+    if (few_fits(a.M, a.N, 2, 2)) return launch_few<TW_T_INT8, 0, 0, 2, 2, NB>(a, none, s);
+    // 64 x 32: up to 64 rows (128 rows: 18.6 against 16.8 at K = 5632)
+    if (a.M <= 64 && few_fits(a.M, a.N, 4, 2))
+        return launch_few<TW_T_INT8, 0, 0, 4, 2, NB>(a, none, s);
     if constexpr (NB == 1) {
         if (tiles(256, 256) >= 192) return launch_tiles<256, 256, 4, 2, 4, 1>(a, s);
         if (tiles(128, 128) >= 192) return launch_tiles<128, 128, 2, 4, 4, 1>(a, s);
@@ -294,20 +552,32 @@ hipError_t launch_product(const QArgs &a, hipStream_t s) {
     }
 }
 
-}  // namespace
-
-hipError_t launch_quant_linear(const int8_t *q, const float *x_scale, const int8_t *w,
-                               const float *w_scale, const float *bias, int M, int K, int N,
-                               void *y, int y_type, hipStream_t s) {
-    return launch_product<1>(
-        QArgs{q, x_scale, {{w, w_scale}, {w, w_scale}}, bias, M, K, N, (char *)y, y_type}, s);
+template <int NB>
+hipError_t launch_fused(const QArgs &a, const QuantRows &r, hipStream_t s) {
+    const FewRows f{(const char *)r.x, r.x_stride, r.gamma, r.beta, r.eps};
+    if (r.x_type == TW_T_F32) return launch_fused<TW_T_F32, NB>(a, f, s);
+    return launch_fused<TW_T_BF16, NB>(a, f, s);
 }
 
-hipError_t launch_quant_gateup(const int8_t *q, const float *x_scale, const int8_t *wg,
-                               const float *g_scale, const int8_t *wu, const float *u_scale, int M,
-                               int K, int N, void *h, int h_type, hipStream_t s) {
-    return launch_product<2>(
-        QArgs{q, x_scale, {{wg, g_scale}, {wu, u_scale}}, nullptr, M, K, N, (char *)h, h_type}, s);
+}  // namespace
+
+bool quant_fused(int M, int K) {
+    return M >= 1 && M <= kFusedRows && K <= fused_max_k(M);
+}
+
+hipError_t launch_quant_linear(const int8_t *q, const float *x_scale, const QuantRows *rows,
+                               const int8_t *w, const float *w_scale, const float *bias, int M,
+                               int K, int N, void *y, int y_type, hipStream_t s) {
+    const QArgs a{q, x_scale, {{w, w_scale}, {w, w_scale}}, bias, M, K, N, (char *)y, y_type};
+    return rows ? launch_fused<1>(a, *rows, s) : launch_product<1>(a, s);
+}
+
+hipError_t launch_quant_gateup(const int8_t *q, const float *x_scale, const QuantRows *rows,
+                               const int8_t *wg, const float *g_scale, const int8_t *wu,
+                               const float *u_scale, int M, int K, int N, void *h, int h_type,
+                               hipStream_t s) {
+    const QArgs a{q, x_scale, {{wg, g_scale}, {wu, u_scale}}, nullptr, M, K, N, (char *)h, h_type};
+    return rows ? launch_fused<2>(a, *rows, s) : launch_product<2>(a, s);
 }
 
 }  // namespace tw

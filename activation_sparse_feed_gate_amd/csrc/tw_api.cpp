@@ -795,7 +795,7 @@ tw_status tw_layernorm_fwd(const void *x, int x_type, int64_t x_stride, const vo
 
 size_t tw_layernorm_bwd_workspace_bytes(int M, int K) {
     if (M < 0 || K <= 0 || K > tw::kNormMaxK) return 0;
-    return (size_t)tw::layernorm_bwd_groups(M, K) * 2 * K * 4;
+    return tw::layernorm_bwd_bytes(M, K);
 }
 
 tw_status tw_layernorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
@@ -881,11 +881,14 @@ tw_status tw_quant_linear(const void *x, int x_type, int64_t x_stride, const flo
     TW_TRY(check_quant_in(x, x_type, x_stride, x_scale, M, K, tw::kQuantMaxK, ws, ws_bytes, &in));
     hipStream_t s = static_cast<hipStream_t>(stream);
     TW_TRY(record(events, 0, s));
-    if (in.q_out)
+    const tw::QuantRows rows{x, x_type, x_stride, nullptr, nullptr, 0.0f};
+    const bool fused = in.q_out && tw::quant_fused(M, K);
+    if (in.q_out && !fused)
         TW_TRY(launched(tw::launch_quant_rows(x, x_type, x_stride, M, K, in.q_out, in.scale_out, s),
                         "row quantisation launch"));
     TW_TRY(record(events, 1, s));
-    TW_TRY(launched(tw::launch_quant_linear(in.q, in.scale, w, w_scale, bias, M, K, N, y, y_type, s),
+    TW_TRY(launched(tw::launch_quant_linear(in.q, in.scale, fused ? &rows : nullptr, w, w_scale,
+                                            bias, M, K, N, y, y_type, s),
                     "int8 product launch"));
     TW_TRY(record(events, 2, s));
     return TW_OK;
@@ -913,16 +916,18 @@ tw_status tw_quant_gateup(const void *x, int x_type, int64_t x_stride, const flo
     TW_TRY(check_quant_in(x, x_type, x_stride, x_scale, M, K, max_k, ws, ws_bytes, &in));
     hipStream_t s = static_cast<hipStream_t>(stream);
     TW_TRY(record(events, 0, s));
-    if (in.q_out && gamma)
+    const tw::QuantRows rows{x, x_type, x_stride, gamma, beta, eps};
+    const bool fused = in.q_out && tw::quant_fused(M, K);
+    if (in.q_out && !fused && gamma)
         TW_TRY(launched(tw::launch_layernorm_quant(x, x_type, x_stride, nullptr, 0, gamma, beta,
                                                    eps, M, K, nullptr, in.q_out, in.scale_out, s),
                         "layer norm launch"));
-    else if (in.q_out)
+    else if (in.q_out && !fused)
         TW_TRY(launched(tw::launch_quant_rows(x, x_type, x_stride, M, K, in.q_out, in.scale_out, s),
                         "row quantisation launch"));
     TW_TRY(record(events, 1, s));
-    TW_TRY(launched(tw::launch_quant_gateup(in.q, in.scale, wg, g_scale, wu, u_scale, M, K, N, h,
-                                            h_type, s),
+    TW_TRY(launched(tw::launch_quant_gateup(in.q, in.scale, fused ? &rows : nullptr, wg, g_scale,
+                                            wu, u_scale, M, K, N, h, h_type, s),
                     "int8 product launch"));
     TW_TRY(record(events, 2, s));
     return TW_OK;

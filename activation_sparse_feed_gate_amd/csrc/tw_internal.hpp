@@ -225,9 +225,9 @@ hipError_t launch_layernorm_quant(const void *x, int x_type, int64_t x_stride, c
                                   hipStream_t s);
 hipError_t launch_quant_rows(const void *x, int x_type, int64_t x_stride, int M, int K, int8_t *q,
                              float *scale, hipStream_t s);
-// Gradient of the layer norm.  part: layernorm_bwd_groups(M, K) * 2 K floats
-// (unused when dgamma and dbeta are both null).
-int layernorm_bwd_groups(int M, int K);
+// Gradient of the layer norm.  part: layernorm_bwd_bytes(M, K) bytes (unused
+// when dgamma and dbeta are both null).
+size_t layernorm_bwd_bytes(int M, int K);
 hipError_t launch_layernorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
                                 int64_t x_stride, const float *gamma, const float *mean,
                                 const float *rstd, const void *dres, int M, int K, void *dx,
@@ -235,12 +235,23 @@ hipError_t launch_layernorm_bwd(const void *dy, int dy_type, const void *x, int 
                                 hipStream_t s, hipEvent_t ev_rows);
 
 // int8 products (quant_gemm.hip): y = (q w^T) x_scale w_scale (+ bias), and
-// h = ReLU(gate) * up of two such products.
-hipError_t launch_quant_linear(const int8_t *q, const float *x_scale, const int8_t *w,
-                               const float *w_scale, const float *bias, int M, int K, int N,
-                               void *y, int y_type, hipStream_t s);
-hipError_t launch_quant_gateup(const int8_t *q, const float *x_scale, const int8_t *wg,
-                               const float *g_scale, const int8_t *wu, const float *u_scale, int M,
-                               int K, int N, void *h, int h_type, hipStream_t s);
+// h = ReLU(gate) * up of two such products.  The input is either int8 rows q
+// with x_scale, or, for a few rows (quant_fused), float rows that the same
+// kernel norms (gamma not null) and quantises; q and x_scale are then unused.
+struct QuantRows {
+    const void *x;
+    int x_type;
+    int64_t x_stride;
+    const float *gamma, *beta;
+    float eps;
+};
+bool quant_fused(int M, int K);
+hipError_t launch_quant_linear(const int8_t *q, const float *x_scale, const QuantRows *rows,
+                               const int8_t *w, const float *w_scale, const float *bias, int M,
+                               int K, int N, void *y, int y_type, hipStream_t s);
+hipError_t launch_quant_gateup(const int8_t *q, const float *x_scale, const QuantRows *rows,
+                               const int8_t *wg, const float *g_scale, const int8_t *wu,
+                               const float *u_scale, int M, int K, int N, void *h, int h_type,
+                               hipStream_t s);
 
 }  // namespace tw

@@ -9,6 +9,7 @@
 namespace tw {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // 16-byte accesses at the alignment of the element type: gfx950 runs them at
