@@ -44,46 +44,72 @@ struct NormArgs {
 enum { kNorm = 0, kNormQuant = 1, kQuant = 2 };
 
 // TPR threads hold a row, VPT vectors of 8 elements each (vector v of thread
-// t starts at element 8 (v TPR + t): every load of a wave is contiguous).
+// t starts at element 8 (v TPR + t): every load of a wave is contiguous).  A
+// workgroup walks rows with gamma and beta in registers (read per row from
+// the L2 they would cost as much as the row) and the next row's loads in
+// flight.  Memory bounds it: 16384 x 2048 fp32 with add takes 88 us (5.3
+// TB/s, the rate of a copy), 16384 x 4096 bf16 with add 105, 8192 x 8192 bf16
+// 51.
 template <int TX, int TA, int MODE, int TPR, int VPT>
 __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_rows_kernel(
     NormArgs a) {
     constexpr int RPB = TPR >= kNormThreads ? 1 : kNormThreads / TPR;  // rows per workgroup
+    constexpr bool kNorms = MODE != kQuant, kAdds = TA >= 0;
+    constexpr bool kAhead = VPT <= 4;  // registers for the next row
     __shared__ float red[2 * (TPR / kWave)];
     RowReduce<TPR> rr(red);
     const int t = threadIdx.x % TPR;
-    // no barrier when a row is one wave, so waves may leave at different rows
-    for (int64_t m = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; m < a.M;
-         m += (int64_t)gridDim.x * RPB) {
+    auto at = [&](int v) { return 8 * (v * TPR + t); };
+    float gamma[kNorms ? VPT : 1][8], beta[kNorms ? VPT : 1][8];
+    if constexpr (kNorms) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.gamma, at(v), a.K), gamma[v]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) beta[v][i] = 0.0f;
+            if (a.beta) unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.beta, at(v), a.K), beta[v]);
+        }
+    }
+    Vec8<TX> xv[VPT];
+    Vec8<kAdds ? TA : TX> av[kAdds ? VPT : 1];
+    auto fetch = [&](int64_t m) {
         const char *xr = a.x + m * a.x_stride * type_bytes(TX);
-        Vec8<TX> xv[VPT];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) xv[v] = load8<TX>(xr, 8 * (v * TPR + t), a.K);
-        float z[VPT][8];
-        if constexpr (TA >= 0) {
+        for (int v = 0; v < VPT; ++v) xv[v] = load8<TX>(xr, at(v), a.K);
+        if constexpr (kAdds) {
             const char *ar = a.add + m * a.K * type_bytes(TA);
-            Vec8<TA> av[VPT];
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) av[v] = load8<TA>(ar, 8 * (v * TPR + t), a.K);
+            for (int v = 0; v < VPT; ++v) av[v] = load8<TA>(ar, at(v), a.K);
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t m = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (kAhead && m < a.M) fetch(m);
+    // no barrier when a row is one wave, so waves may leave at different rows
+    for (; m < a.M; m += step) {
+        if (!kAhead) fetch(m);
+        float z[VPT][8];
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) {
+        for (int v = 0; v < VPT; ++v) {
+            unpack8<TX>(xv[v], z[v]);
+            if constexpr (kAdds) {
                 float f[8];
-                unpack8<TX>(xv[v], z[v]);
                 unpack8<TA>(av[v], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z[v][i] += f[i];
             }
+        }
+        // a stored sum may be x or add itself: every element is read here by
+        // the thread that writes it, and the next row's are other elements
+        if (kAhead && m + step < a.M) fetch(m + step);
+        if constexpr (kAdds) {
             if (a.sum) {
 #pragma unroll
                 for (int v = 0; v < VPT; ++v)
-                    store8<TX>(a.sum + m * a.K * type_bytes(TX), 8 * (v * TPR + t), a.K, z[v]);
+                    store8<TX>(a.sum + m * a.K * type_bytes(TX), at(v), a.K, z[v]);
             }
-        } else {
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) unpack8<TX>(xv[v], z[v]);
         }
-
-        if constexpr (MODE != kQuant) {
+        if constexpr (kNorms) {
             float s = 0.0f;
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
@@ -92,32 +118,32 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
             const float mean = rr.sum(s) / a.K;
             s = 0.0f;
 #pragma unroll
-            for (int v = 0; v < VPT; ++v)
+            for (int v = 0; v < VPT; ++v) {
+                if (at(v) + 8 <= a.K) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    z[v][i] = 8 * (v * TPR + t) + i < a.K ? z[v][i] - mean : 0.0f;
-                    s += z[v][i] * z[v][i];
+                    for (int i = 0; i < 8; ++i) z[v][i] -= mean;
+                } else {  // past the end stays zero
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z[v][i] = at(v) + i < a.K ? z[v][i] - mean : 0.0f;
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += z[v][i] * z[v][i];
+            }
             const float rstd = 1.0f / sqrtf(rr.sum(s) / a.K + a.eps);
             if (t == 0) {
                 if (a.mean) a.mean[m] = mean;
                 if (a.rstd) a.rstd[m] = rstd;
             }
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int e = 8 * (v * TPR + t);
-                float g[8], b[8];
-                unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.gamma, e, a.K), g);
-                if (a.beta) unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.beta, e, a.K), b);
+            for (int v = 0; v < VPT; ++v)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    z[v][i] = z[v][i] * rstd * g[i] + (a.beta ? b[i] : 0.0f);
-            }
+                    z[v][i] = z[v][i] * rstd * gamma[v][i] + beta[v][i];
         }
         if constexpr (MODE == kNorm) {
             char *yr = a.y + m * a.K * (a.y_type == TW_T_F32 ? 4 : 2);
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) store8_as(a.y_type, yr, 8 * (v * TPR + t), a.K, z[v]);
+            for (int v = 0; v < VPT; ++v) store8_as(a.y_type, yr, at(v), a.K, z[v]);
         } else {
             uint32_t top = 0;
 #pragma unroll
@@ -127,30 +153,42 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
             const RowScale rs = row_scale(rr.max_u32(top));
             if (t == 0) a.scale[m] = rs.scale;
 #pragma unroll
-            for (int v = 0; v < VPT; ++v)
-                store_q8(a.q + m * a.K, 8 * (v * TPR + t), a.K, quant8(z[v], rs.inv));
+            for (int v = 0; v < VPT; ++v) store_q8(a.q + m * a.K, at(v), a.K, quant8(z[v], rs.inv));
         }
     }
 }
 
+template <int TX, int TA, int MODE, int TPR, int VPT>
+hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
+    constexpr int threads = TPR > kNormThreads ? TPR : kNormThreads;
+    constexpr int rpb = threads / TPR;
+    const int64_t need = ((int64_t)a.M + rpb - 1) / rpb;
+    // Norms: the workgroups the chip holds at once (2048 threads a CU, 1024
+    // with the registers an add takes), so that gamma is read once per
+    // workgroup; the quantiser has nothing to keep and takes a row each.
+    // Measured (us at 1024, 2048, no limit): 8192 x 8192 bf16 51, 51, 66; 16384 x
+    // 2048 bf16 30, 28, 35, fp32 with add 88, 92, 88; int8 16384 x 8192 71, 75, 70.
+    const int64_t most = MODE == kQuant ? 1 << 20 : 256 * (TA >= 0 ? 1024 : 2048) / threads;
+    norm_rows_kernel<TX, TA, MODE, TPR, VPT>
+        <<<(unsigned)(need < most ? need : most), threads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+// A wave a row up to 1024 elements, then a workgroup a row of as few vectors
+// a thread as its 256 to 1024 threads allow.  Measured (us): 16384 x 2048 fp32
+// with add, a workgroup of 256 a row 88, a wave a row 98; 8 rows of 2048, 2.9
+// and 4.3; 4096 x 1024 bf16, a wave a row 5.6, a workgroup 8.1.
 template <int TX, int TA, int MODE>
 hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
-    // Rows of up to 4096 elements are one wave's (4 rows per workgroup, no
-    // barrier); longer ones a workgroup's.
-    auto go = [&](auto kernel, int tpr) {
-        const int rpb = tpr >= kNormThreads ? 1 : kNormThreads / tpr;
-        const int64_t blocks = ((int64_t)a.M + rpb - 1) / rpb;
-        kernel<<<(unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)),
-                 tpr > kNormThreads ? tpr : kNormThreads, 0, s>>>(a);
-        return hipGetLastError();
-    };
     if (a.M == 0) return hipSuccess;
-    if (a.K <= 512) return go(norm_rows_kernel<TX, TA, MODE, 64, 1>, 64);
-    if (a.K <= 1024) return go(norm_rows_kernel<TX, TA, MODE, 64, 2>, 64);
-    if (a.K <= 2048) return go(norm_rows_kernel<TX, TA, MODE, 64, 4>, 64);
-    if (a.K <= 4096) return go(norm_rows_kernel<TX, TA, MODE, 64, 8>, 64);
-    if (a.K <= 16384) return go(norm_rows_kernel<TX, TA, MODE, 256, 8>, 256);
-    return go(norm_rows_kernel<TX, TA, MODE, 1024, 8>, 1024);
+    if (a.K <= 512) return launch_rows<TX, TA, MODE, 64, 1>(a, s);
+    if (a.K <= 1024) return launch_rows<TX, TA, MODE, 64, 2>(a, s);
+    if (a.K <= 2048) return launch_rows<TX, TA, MODE, 256, 1>(a, s);
+    if (a.K <= 4096) return launch_rows<TX, TA, MODE, 256, 2>(a, s);
+    if (a.K <= 8192) return launch_rows<TX, TA, MODE, 512, 2>(a, s);
+    if constexpr (MODE == kQuant)
+        if (a.K > kNormMaxK) return launch_rows<TX, TA, MODE, 1024, 8>(a, s);
+    return launch_rows<TX, TA, MODE, 1024, 2>(a, s);
 }
 
 template <int MODE>
@@ -192,12 +230,13 @@ constexpr int norm_bwd_cols(int K) { return norm_bwd_tpr(K) * norm_bwd_vpt(K) * 
 
 // While a row is reduced and written the next one's loads are in flight: the
 // column sums leave room for few waves, too few to hide the loads behind each
-// other.
+// other.  (Rows of more than 8192 elements fill the registers without.)
 template <int TD, int TX, int TPR, int VPT>
 __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, 2)
 void norm_bwd_kernel(NormBwdArgs a) {
     constexpr int RPB = TPR > kNormThreads ? 1 : kNormThreads / TPR;
     constexpr int KP = TPR * VPT * 8;
+    constexpr bool kAhead = VPT < 4;
     extern __shared__ __attribute__((aligned(16))) float share[];  // [RPB][2][KP] (TPR == 64)
     __shared__ float red[2 * (TPR / kWave)];
     RowReduce<TPR> rr(red);
@@ -223,8 +262,9 @@ void norm_bwd_kernel(NormBwdArgs a) {
     };
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t m = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-    if (m < a.M) fetch(m);
+    if (kAhead && m < a.M) fetch(m);
     for (; m < a.M; m += step) {
+        if (!kAhead) fetch(m);
         const float r = rstd;
         float n[VPT][8], g[VPT][8];
 #pragma unroll
@@ -236,7 +276,7 @@ void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) n[v][i] = (n[v][i] - mean) * r;
         }
-        if (m + step < a.M) fetch(m + step);
+        if (kAhead && m + step < a.M) fetch(m + step);
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
