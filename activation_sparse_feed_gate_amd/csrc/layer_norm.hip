@@ -67,7 +67,8 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
             unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.gamma, at(v), a.K), gamma[v]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) beta[v][i] = 0.0f;
-            if (a.beta) unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.beta, at(v), a.K), beta[v]);
+            if (a.beta)
+                unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.beta, at(v), a.K), beta[v]);
         }
     }
     Vec8<TX> xv[VPT];
@@ -323,7 +324,8 @@ void norm_bwd_kernel(NormBwdArgs a) {
         for (int e = 4 * threadIdx.x; e < 2 * KP; e += 4 * kNormThreads) {
             f32x4 s = *reinterpret_cast<const f32x4 *>(share + e);
 #pragma unroll
-            for (int w = 1; w < RPB; ++w) s += *reinterpret_cast<const f32x4 *>(share + w * 2 * KP + e);
+            for (int w = 1; w < RPB; ++w)
+                s += *reinterpret_cast<const f32x4 *>(share + w * 2 * KP + e);
             *reinterpret_cast<f32x4 *>(pg + e) = s;
         }
     } else {

@@ -8,11 +8,14 @@
 // |sum| <= 127^2 K stays below 2^31 for K <= 131072, and the integer sum does
 // not depend on its order, so every split of K gives the same bits.
 //
-// Two kernels: a few rows stream the weights (every weight byte is read once
-// and K is split over the waves of a workgroup); more rows are tiled over
-// the direct-to-LDS ring of tw_gemm.hpp, whose 64-byte stage rows hold 64
-// int8 elements: the 16 bytes a lane feeds to v_mfma_i32_32x32x32_i8 lie
-// where v_mfma_f32_32x32x16_bf16 has its 8 bf16.
+// Three kernels.  A few rows: fragments straight into registers, K split over
+// the waves of a workgroup.  Hundreds of rows: tiles over the direct-to-LDS
+// ring of tw_gemm.hpp, whose 64-byte stage rows hold 64 int8 elements (the 16
+// bytes a lane feeds to v_mfma_i32_32x32x32_i8 lie where
+// v_mfma_f32_32x32x16_bf16 has its 8 bf16).  Thousands: 256 x 256 tiles with
+// stages of whole 128-byte lines, refilled in parts.
+#include <type_traits>
+
 #include "tw_gemm.hpp"
 #include "tw_internal.hpp"
 #include "tw_rows.hpp"
@@ -273,7 +276,8 @@ void quant_few_kernel(QArgs a, FewRows f) {
                 for (int c = 0; c < NC; ++c) {
                     const u32x4 w = in ? wf[p][b][c] : u32x4{};
 #pragma unroll
-                    for (int i = 0; i < MB; ++i) acc[b][c][i] = mfma16_i8(w, xf[p][i], acc[b][c][i]);
+                    for (int i = 0; i < MB; ++i)
+                        acc[b][c][i] = mfma16_i8(w, xf[p][i], acc[b][c][i]);
                 }
         }
     }
@@ -440,8 +444,8 @@ __global__ __launch_bounds__(WM * WN * 64) void quant_gemm_kernel(QArgs a) {
             char *dst = st + row0 * kPRow;
             // chunks past a row's end read zeros in x, so what the weights'
             // chunks hold there does not matter
-            if (row0 < BM)
-                dma16(rx, last && kt * kPRow + chunk[j] * 16 >= a.K ? kOutside : voff[j], soff, dst);
+            const bool past = last && kt * kPRow + chunk[j] * 16 >= a.K;
+            if (row0 < BM) dma16(rx, past ? kOutside : voff[j], soff, dst);
             else if (NB == 1 || row0 < BM + BN) dma16(r0, voff[j], soff, dst);
             else dma16(r1, voff[j], soff, dst);
         }
@@ -505,6 +509,328 @@ __global__ __launch_bounds__(WM * WN * 64) void quant_gemm_kernel(QArgs a) {
     }
 }
 
+// ------------------------------ large tiles --------------------------------
+// 256 token rows by 256 weight rows (gateup: 128 of each matrix) a workgroup
+// of 8 waves, 64 x 128 outputs each; a workgroup a CU, walking tiles, the next
+// tile's first stages on their way while a tile is written.  Measured on
+// 8-bit normal values: 16384 x 8192 x 2048 245 us, 2.25 POP/s (the 64-byte ring
+// with 256 x 256 tiles 285), gateup 16384 x 2048 x 8192 513 us (607); on zeros,
+// which draw less power, 183 and 408 us.
+//
+// What bounds this product is the stream of operands from L2 into LDS (loads
+// alone: 150 us of the 248 that the ring above took for 16384 x 8192 x 2048
+// on zeros), and a load instruction that covers whole 128-byte lines moves up
+// to 1.7 times the bytes of one that covers 64-byte pieces.  So a stage is
+// 128 bytes of each row, two stages fill 128 KB of LDS, and the loads of the
+// stage after next enter a stage's slot in two parts, as soon as no wave reads
+// what they replace:
+//
+//   step   matrix instructions   fragments read              loads into this slot
+//   0      A x B0                B1 of this stage
+//   -- X: this stage's B2, B3 have landed; its A, B0, B1 are in registers
+//   1      A x B1                B2                          A, B0, B1
+//   2      A x B2                B3
+//   -- Y: the next stage's A, B0, B1 have landed; all of this one is in registers
+//   3      A x B3                A and B0 of the next stage  B2, B3
+//
+// with A the wave's 64 token rows (two blocks of 32) and B0 .. B3 its blocks of
+// 32 weight rows.  Every load has one and a half stages of arithmetic to land
+// in (one barrier a stage, with the whole slot refilled at Y and waited for at
+// the next Y, left the loads idle for their latency in every stage).  A step
+// is 8 matrix instructions, 512 cycles with those of the SIMD's other wave, so
+// its reads are there when the next step begins; the last step reads each
+// sub-step of the next A as soon as it has used its own.
+constexpr int kWideRow = 128;           // bytes of a row in a stage
+constexpr int kWideStage = 512 * kWideRow;
+constexpr int kWideOut = 32 * kWideRow;  // a wave's outputs on their way to memory
+constexpr int kWideLds = 2 * kWideStage + 8 * kWideOut;
+
+// 16-byte chunk c of row r lives at chunk c ^ ((r >> 1) & 7): rows are half of
+// LDS's 256 bytes of banks, so 16 consecutive rows of one logical chunk fall
+// on 16 different bank groups.
+__device__ __forceinline__ int wide_swz(int r) { return (r >> 1) & 7; }
+
+template <int NB>
+__global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a) {
+    constexpr int BN = 256 / NB;  // weight rows of each matrix
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int l32 = lane & 31;
+    const int KT = (a.K + kWideRow - 1) / kWideRow;
+    const int nbm = (a.M + 255) / 256, nbn = (a.N + BN - 1) / BN;
+    const int tiles = nbm * nbn;
+    settle_scalars(a.x_scale, a.w[0].scale, a.w[1].scale, a.bias, a.y, a.y_type, a.M, a.N);
+
+    // the tile being loaded: its origin and descriptors
+    int m0, n0;
+    rsrc_t rx, r0, r1;
+    auto at_tile = [&](int t) {
+        int rb, cb;
+        xcd_tile(t, nbm, nbn, rb, cb);
+        m0 = rb * 256;
+        n0 = cb * BN;
+        const int mr = min(256, a.M - m0), nr = min(BN, a.N - n0);  // rows in this tile
+        rx = make_rsrc(a.q + (size_t)m0 * a.K, (uint64_t)mr * a.K);
+        r0 = make_rsrc(a.w[0].w + (size_t)n0 * a.K, (uint64_t)nr * a.K);
+        r1 = NB == 2 ? make_rsrc(a.w[1].w + (size_t)n0 * a.K, (uint64_t)nr * a.K) : r0;
+    };
+    // A load of a wave fetches 8 whole lines, rows 64 g + 8 wave ..+7 of group g
+    // of 64: groups 0 .. 3 of x, then of the weights.  Rows past the matrix lie
+    // past the descriptor's end and read zeros.
+    const int lrow = 8 * wave + (lane >> 3);
+    const int chunk = (lane & 7) ^ wide_swz(lrow);
+    const uint32_t v0 = (uint32_t)lrow * a.K + chunk * 16;
+    const uint32_t v64 = 64u * a.K;
+    auto slot = [&](int kt, int g) {
+        return smem + (kt & 1) * kWideStage + (64 * g + 8 * wave) * kWideRow;
+    };
+    // weight group of pair p (0: blocks 0, 1; 1: blocks 2, 3), i = 0, 1.
+    // linear: groups 0, 1 are the first 128 columns' blocks, 2, 3 the others';
+    // gateup: 0, 1 are the gate's rows, 2, 3 the up's
+    auto load_b = [&](int kt, int p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int g = NB == 1 ? 2 * i + p : 2 * p + i;
+            dma16(NB == 2 && p ? r1 : r0, v0 + (NB == 1 ? g : i) * v64, kt * kWideRow,
+                  slot(kt, 4 + g));
+        }
+    };
+    auto load_ab = [&](int kt) {
+        // chunks past a row's end read zeros in x, so what the weights'
+        // chunks hold there does not matter
+        const bool past = kt * kWideRow + chunk * 16 >= a.K;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            dma16(rx, past ? kOutside : v0 + g * v64, kt * kWideRow, slot(kt, g));
+        load_b(kt, 0);
+    };
+    constexpr int kAB = 6, kB = 2;  // loads of a wave in each part
+    // Fragments of 32 rows from `row` on, one 32-byte sub-step of a stage.
+    auto read = [&](int kt, int row, int s) {
+        const int c = (2 * s + (lane >> 5)) ^ wide_swz(l32);
+        return lds_ld16(smem + (kt & 1) * kWideStage, (row + l32) * kWideRow + (c << 4));
+    };
+    // weight rows of block j; gateup: blocks 0, 1 of the gate, 2, 3 of the up
+    auto b_row = [&](int j) {
+        return NB == 1 ? wn * 128 + j * 32 : (j >> 1) * 128 + wn * 64 + (j & 1) * 32;
+    };
+    u32x4 fa[4][2], fb[2][4];  // [sub-step][block], [register set][sub-step]
+    auto read_a = [&](int kt, int s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fa[s][i] = read(kt, wm * 64 + i * 32, s);
+    };
+    auto read_b = [&](int kt, int j) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) fb[j & 1][s] = read(kt, 256 + b_row(j), s);
+    };
+    // [token rows][weight rows]; register r of a block is token row l32,
+    // weight row mfma32_row(r)
+    i32x16 acc[2][4];
+    auto mma = [&](int j, int s) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i][j] = mfma32_i8(fb[j & 1][s], fa[s][i], acc[i][j]);
+    };
+    // The scheduling barriers keep each step's reads ahead of its matrix
+    // instructions.
+    auto step = [&](int kt, int j) {
+        read_b(kt, j + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) mma(j, s);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto last_step = [&](int kt) {
+        read_b(kt + 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            mma(3, s);
+            __builtin_amdgcn_sched_barrier(0);
+            read_a(kt + 1, s);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto load_first = [&] {
+        load_ab(0);
+        load_b(0, 1);
+        if (KT > 1) {
+            load_ab(1);
+            load_b(1, 1);
+        }
+    };
+    // Scales of the tile at (m0, n0): of token row l32 of each block, and of
+    // column l32 of each block (the outputs of a lane are other columns of its
+    // row: it gets theirs from their lanes).
+    struct Scales {
+        float x[2], w[4], bias[4];
+    };
+    auto col = [&](int base, int j) {  // first output column of block j
+        return base + (NB == 1 ? wn * 128 + j * 32 : wn * 64 + (j & 1) * 32);
+    };
+    const float *bp = NB == 1 && a.bias ? a.bias : a.w[0].scale;
+    auto load_scales = [&] {
+        Scales c;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c.x[i] = a.x_scale[min(m0 + wm * 64 + i * 32 + l32, a.M - 1)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = min(col(n0, j) + l32, a.N - 1);
+            c.w[j] = a.w[NB == 2 ? j >> 1 : 0].scale[n];
+            c.bias[j] = NB == 1 ? bp[n] : 0.0f;
+        }
+        return c;
+    };
+    at_tile(blockIdx.x);
+    Scales sc = load_scales();
+    load_first();
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int mt = m0, nt = n0;  // this tile; m0, n0 move on to the next below
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
+        // what may be outstanding besides the loads below is younger (the last
+        // tile's stores)
+        if (KT > 1) wait_vmcnt<kB + kAB + kB>();
+        else wait_vmcnt<kB>();
+        __builtin_amdgcn_s_barrier();
+#pragma unroll
+        for (int s = 0; s < 4; ++s) read_a(0, s);
+        read_b(0, 0);
+        int kt = 0;
+        for (; kt + 2 < KT; ++kt) {
+            step(kt, 0);
+            wait_vmcnt<kAB + kB>();
+            wait_lgkm0();
+            __builtin_amdgcn_s_barrier();  // X
+            load_ab(kt + 2);
+            step(kt, 1);
+            step(kt, 2);
+            wait_vmcnt<kB + kAB>();
+            wait_lgkm0();
+            __builtin_amdgcn_s_barrier();  // Y
+            load_b(kt + 2, 1);
+            last_step(kt);
+        }
+        if (kt + 1 < KT) {
+            step(kt, 0);
+            wait_vmcnt<kAB + kB>();
+            wait_lgkm0();
+            __builtin_amdgcn_s_barrier();
+            step(kt, 1);
+            step(kt, 2);
+            wait_vmcnt<kB>();
+            wait_lgkm0();
+            __builtin_amdgcn_s_barrier();
+            last_step(kt);
+            ++kt;
+        }
+        step(kt, 0);
+        wait_vmcnt<0>();
+        __builtin_amdgcn_s_barrier();
+        step(kt, 1);
+        step(kt, 2);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) mma(3, s);
+
+        // The next tile's scales and first loads (after every wave has read its
+        // last fragments) are on their way while this tile is written.
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        Scales next = sc;
+        if (t + (int)gridDim.x < tiles) {
+            at_tile(t + gridDim.x);
+            next = load_scales();
+            load_first();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        // Outputs go through 4 KB of LDS a wave, 32 token rows of 128 bytes at a
+        // time, so that they are stored in whole lines: a lane holds 4 consecutive
+        // columns of one row.  (The lane's number is read anew: the addresses
+        // below, computed ahead of the tile loop, would fill the registers that
+        // the k-loop needs.)
+        char *out = smem + 2 * kWideStage + wave * kWideOut;
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int lr = ln & 31;
+        auto write_out = [&](auto type) {
+            constexpr bool kF32 = decltype(type)::value == TW_T_F32;
+            constexpr int ES = kF32 ? 4 : 2;
+            constexpr int JP = kF32 ? 1 : 2;  // blocks of 32 columns in 128 bytes
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j0 = 0; j0 < 4 / NB; j0 += JP) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int j = j0; j < j0 + JP; ++j)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int ju = NB == 2 ? 2 + j : j;
+                                const int from = 8 * g + 4 * (ln >> 5) + e;
+                                const float b =
+                                    NB == 1 && a.bias ? __shfl(sc.bias[j], from) : 0.0f;
+                                v[e] = finish<NB>(acc[i][j][4 * g + e], acc[i][ju][4 * g + e],
+                                                  sc.x[i], __shfl(sc.w[j], from),
+                                                  __shfl(sc.w[ju], from), b);
+                            }
+                            const int byte = ((j - j0) * 32 + 8 * g + 4 * (ln >> 5)) * ES;
+                            char *p = out + lr * kWideRow + (((byte >> 4) ^ wide_swz(lr)) << 4) +
+                                      (byte & 15);
+                            if constexpr (kF32)
+                                *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+                            else
+                                *reinterpret_cast<u32x2 *>(p) =
+                                    u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                        }
+                    const int n = col(nt, j0) + (ln & 7) * (16 / ES);
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const int r = it * 8 + (ln >> 3);
+                        const u32x4 v =
+                            lds_ld16(out, r * kWideRow + (((ln & 7) ^ wide_swz(r)) << 4));
+                        const int m = mt + wm * 64 + i * 32 + r;
+                        if (m >= a.M) continue;
+                        char *p = a.y + ((size_t)m * a.N + n) * ES;
+                        if (n + 16 / ES <= a.N) {
+                            *reinterpret_cast<u32x4_any *>(p) = v;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16 / ES; ++e) {
+                                if (n + e >= a.N) continue;
+                                if constexpr (kF32)
+                                    reinterpret_cast<uint32_t *>(p)[e] = v[e];
+                                else
+                                    reinterpret_cast<uint16_t *>(p)[e] =
+                                        (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+                            }
+                        }
+                    }
+                }
+        };
+        if (a.y_type == TW_T_F32) write_out(std::integral_constant<int, TW_T_F32>{});
+        else write_out(std::integral_constant<int, TW_T_BF16>{});
+        sc = next;
+    }
+}
+
+template <int NB>
+hipError_t launch_wide(const QArgs &a, hipStream_t s) {
+    constexpr auto kernel = &quant_wide_kernel<NB>;
+    const hipError_t e = lds_limit_once<kernel>(kWideLds);
+    if (e != hipSuccess) return e;
+    constexpr int BN = 256 / NB;
+    const int64_t tiles = ((int64_t)a.M + 255) / 256 * (((int64_t)a.N + BN - 1) / BN);
+    kernel<<<(unsigned)(tiles < 256 ? tiles : 256), 512, kWideLds, s>>>(a);
+    return hipGetLastError();
+}
+
 template <int BM, int BN, int WM, int WN, int S, int NB>
 hipError_t launch_tiles(const QArgs &a, hipStream_t s) {
     using P = QG<BM, BN, WM, WN, S, NB>;
@@ -541,15 +867,19 @@ hipError_t launch_product(const QArgs &a, hipStream_t s) {
     // 64 x 32: up to 64 rows (128 rows: 18.6 against 16.8 at K = 5632)
     if (a.M <= 64 && few_fits(a.M, a.N, 4, 2))
         return launch_few<TW_T_INT8, 0, 0, 4, 2, NB>(a, none, s);
+    // Larger tiles do more arithmetic per byte loaded, so the largest whose
+    // grid occupies about half the chip or more.  Measured (us, linear; tiles
+    // of 256 x 256, 128 x 128, 64 x 64):
+    //   K = 2048, N = 5632    512 rows 26.9, 15.3, 17.4   1536 rows 29.0, 37.0, 41.4
+    //   K = 5632, N = 2048   1024 rows 57.7, 28.4, 27.1   4096 rows 61.1, 68.2, 101
+    //   K = 1024, N = 4096    512 rows 17.6, 10.4, 8.5    2048 rows 19.5, 19.1, 23.2
+    if (tiles(256, 256 / NB) >= 120) return launch_wide<NB>(a, s);
     if constexpr (NB == 1) {
-        if (tiles(256, 256) >= 192) return launch_tiles<256, 256, 4, 2, 4, 1>(a, s);
-        if (tiles(128, 128) >= 192) return launch_tiles<128, 128, 2, 4, 4, 1>(a, s);
-        return launch_tiles<64, 64, 2, 2, 4, 1>(a, s);
+        if (tiles(128, 128) >= 144) return launch_tiles<128, 128, 2, 4, 4, 1>(a, s);
     } else {
-        if (tiles(256, 128) >= 192) return launch_tiles<256, 128, 4, 2, 4, 2>(a, s);
-        if (tiles(128, 64) >= 192) return launch_tiles<128, 64, 4, 2, 4, 2>(a, s);
-        return launch_tiles<64, 64, 2, 2, 4, 2>(a, s);
+        if (tiles(128, 64) >= 144) return launch_tiles<128, 64, 4, 2, 4, 2>(a, s);
     }
+    return launch_tiles<64, 64, 2, 2, 4, NB>(a, s);
 }
 
 template <int NB>

@@ -57,7 +57,8 @@ def gate_ref(q, xs, wg, gs, wu, us):
 SHAPES = [(1, 16, 1), (1, 2048, 5), (2, 48, 16), (7, 80, 127), (16, 256, 250), (17, 1008, 33),
           (32, 64, 1001), (33, 2048, 128), (64, 96, 63), (65, 4096, 65), (77, 1008, 1001),
           (128, 128, 4096), (129, 160, 2500), (300, 272, 700), (1025, 80, 1300), (2000, 1040, 2100),
-          (4100, 144, 3300), (5000, 64, 4097)]
+          (4100, 144, 3300), (5000, 64, 4097), (2900, 400, 4700), (4200, 656, 5000),
+          (16001, 384, 300)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
