@@ -110,14 +110,16 @@ struct FusedRow {
         : f(f_), K(K_), t(threadIdx.x & (WPR * kWave - 1)) {
         const char *row = f.x + (int64_t)m * f.x_stride * type_bytes(TX);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) raw[v] = load8<TX>(row, at(v), K);
+        for (int v = 0; v < VEC; ++v) raw[v] = load8_whole<TX>(row, at(v), K);
         if (f.gamma) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) g[v] = load8<TW_T_F32>((const char *)f.gamma, at(v), K);
+            for (int v = 0; v < VEC; ++v)
+                g[v] = load8_whole<TW_T_F32>((const char *)f.gamma, at(v), K);
         }
         if (f.beta) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) b[v] = load8<TW_T_F32>((const char *)f.beta, at(v), K);
+            for (int v = 0; v < VEC; ++v)
+                b[v] = load8_whole<TW_T_F32>((const char *)f.beta, at(v), K);
         }
     }
     // op over the row's WPR waves of their (uniform) values v; two slots of
@@ -139,7 +141,13 @@ struct FusedRow {
         auto add = [](float a, float b) { return a + b; };
         float z[VEC][8];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) unpack8<TX>(raw[v], z[v]);
+        for (int v = 0; v < VEC; ++v) {
+            unpack8<TX>(raw[v], z[v]);
+            if (at(v) >= K) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[v][i] = 0.0f;
+            }
+        }
         if (f.gamma) {
             float s = 0.0f;
 #pragma unroll
@@ -163,7 +171,7 @@ struct FusedRow {
                 if (f.beta) unpack8<TW_T_F32>(b[v], bf);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    z[v][i] = z[v][i] * rstd * gf[i] + (f.beta ? bf[i] : 0.0f);
+                    z[v][i] = at(v) < K ? z[v][i] * rstd * gf[i] + (f.beta ? bf[i] : 0.0f) : 0.0f;
             }
         }
         uint32_t top = 0;
@@ -197,7 +205,7 @@ template <int TX, int WPR, int VEC, int MB, int NC, int NB, int PF>
 __global__ __launch_bounds__(kFewWaves *kWave,
                              few_waves(PF *(NB * NC + (TX == TW_T_INT8 ? MB : 0)), NB *NC *MB,
                                        VEC))
-void quant_few_kernel(QArgs a, FewRows f) {
+void quant_few_kernel(QArgs a, FewRows f, int R) {
     constexpr bool kFused = TX != TW_T_INT8;
     static_assert(!kFused || MB == 1, "fused rows: one block of 16");
     extern __shared__ __attribute__((aligned(16))) char few_smem[];
@@ -207,7 +215,7 @@ void quant_few_kernel(QArgs a, FewRows f) {
     __shared__ float red[2 * kFewWaves], row_scales[kFusedRows];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * (16 * NC), m0 = blockIdx.y * (16 * MB);
+    const int n0 = blockIdx.x * R, m0 = blockIdx.y * (16 * MB);
     const int l16 = lane & 15, kc = (lane >> 4) * 16;
     const int steps = (a.K + 63) / 64;
 
@@ -216,7 +224,7 @@ void quant_few_kernel(QArgs a, FewRows f) {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            wr[b][c] = a.w[b].w + (size_t)min(n0 + 16 * c + l16, a.N - 1) * a.K;
+            wr[b][c] = a.w[b].w + (size_t)min(n0 + min(16 * c + l16, R - 1), a.N - 1) * a.K;
     u32x4 wf[PF][NB][NC], xf[PF][kFused ? 1 : MB];
     // The wave's steps p0 .. p0 + PF - 1 of K (step p is p * 8 + wave): chunks
     // past a row's end read its first bytes instead, and the weights' are
@@ -322,10 +330,32 @@ void quant_few_kernel(QArgs a, FewRows f) {
         if (kFused) xs = row_scales[m];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (nl + j < a.N)
+            if (nl + j < min(n0 + R, a.N))
                 put(a.y, a.y_type, (size_t)m * a.N + nl + j,
                     finish<NB>(s[0][j], s[1][j], xs, ws[0][j], ws[NB - 1][j], bias[j]));
     }
+}
+
+// A CU runs one workgroup of these well; a second one on the same CU, or a
+// second round, costs about as much as the first.  So the block grows (which
+// also has the token rows read by fewer workgroups) until the grid is at most
+// one workgroup a CU.
+constexpr int kFewGrid = 256;
+inline bool few_fits(int M, int N, int MB, int NC) {
+    return ((int64_t)M + 16 * MB - 1) / (16 * MB) * (((int64_t)N + 16 * NC - 1) / (16 * NC)) <=
+           kFewGrid;
+}
+
+// Weight rows a workgroup of one row block takes: an even share of N over that
+// many workgroups, so that every CU streams as much (the other rows of its
+// last block of 16 repeat the last one's and are not stored).  At least 8
+// where each workgroup also quantises the rows.  Measured (us, one row, 16 NC
+// against this): linear 5632 x 2048 6.1, 5.3; gateup 5632 x 2048 10.6, 8.9, 2048
+// x 5632 8.0, 7.6.
+inline int few_rows(int N, int NC, bool fused) {
+    const int share = (N + kFewGrid - 1) / kFewGrid, least = fused ? 8 : 4;
+    const int R = share < least ? least : (share + 1) / 2 * 2;
+    return R < 16 * NC ? R : 16 * NC;
 }
 
 template <int TX, int WPR, int VEC, int MB, int NC, int NB, int PF>
@@ -336,8 +366,9 @@ hipError_t launch_few(const QArgs &a, const FewRows &f, hipStream_t s) {
     const hipError_t e = lds_limit_once<kernel>(sums + most);
     if (e != hipSuccess) return e;
     const int lds = sums + (TX != TW_T_INT8 ? a.M * (a.K + kFewPad) : 0);
-    const dim3 grid((a.N + 16 * NC - 1) / (16 * NC), (a.M + 16 * MB - 1) / (16 * MB));
-    kernel<<<grid, kFewWaves * kWave, lds, s>>>(a, f);
+    const int R = MB == 1 ? few_rows(a.N, NC, TX != TW_T_INT8) : 16 * NC;
+    const dim3 grid((a.N + R - 1) / R, (a.M + 16 * MB - 1) / (16 * MB));
+    kernel<<<grid, kFewWaves * kWave, lds, s>>>(a, f, R);
     return hipGetLastError();
 }
 
@@ -353,16 +384,6 @@ hipError_t launch_few(const QArgs &a, const FewRows &f, hipStream_t s) {
     if constexpr (most > 4)
         if (share <= 4) return launch_few<TX, WPR, VEC, MB, NC, NB, 4>(a, f, s);
     return launch_few<TX, WPR, VEC, MB, NC, NB, most>(a, f, s);
-}
-
-// A CU runs one workgroup of these well; a second one on the same CU, or a
-// second round, costs about as much as the first.  So the block grows (which
-// also has the token rows read by fewer workgroups) until the grid is at most
-// one workgroup a CU.
-constexpr int kFewGrid = 256;
-inline bool few_fits(int M, int N, int MB, int NC) {
-    return ((int64_t)M + 16 * MB - 1) / (16 * MB) * (((int64_t)N + 16 * NC - 1) / (16 * NC)) <=
-           kFewGrid;
 }
 
 template <int TX, int WPR, int NB>

@@ -52,6 +52,18 @@ __device__ __forceinline__ Vec8<T> load8(const char *row, int e, int K) {
     return v;
 }
 
+// The same where K is a multiple of 8 (a vector is in or out): vectors past
+// the end read the row's last one instead.  No branch, so nothing waits for a
+// load before it is used.
+template <int T>
+__device__ __forceinline__ Vec8<T> load8_whole(const char *row, int e, int K) {
+    const char *p = row + (size_t)min(e, K - 8) * type_bytes(T);
+    Vec8<T> v;
+    v.w[0] = *reinterpret_cast<const u32x4_any *>(p);
+    if constexpr (T == TW_T_F32) v.w[1] = *reinterpret_cast<const u32x4_any *>(p + 16);
+    return v;
+}
+
 template <int T>
 __device__ __forceinline__ void unpack8(const Vec8<T> &v, float *f) {
 #pragma unroll
