@@ -44,13 +44,15 @@ struct NormArgs {
 enum { kNorm = 0, kNormQuant = 1, kQuant = 2 };
 
 // TPR threads hold a row, VPT vectors of 8 elements each (vector v of thread
-// t starts at element 8 (v TPR + t): every load of a wave is contiguous).  A
+// t starts at element 8 (v TPR + t): every load of a wave is contiguous).
+// WHOLE: K is a multiple of 8, and the loads need no branch (4096 x 1024 bf16
+// 5.1 us against 5.8).  A
 // workgroup walks rows with gamma and beta in registers (read per row from
 // the L2 they would cost as much as the row) and the next row's loads in
 // flight.  Memory bounds it: 16384 x 2048 fp32 with add takes 88 us (5.3
 // TB/s, the rate of a copy), 16384 x 4096 bf16 with add 105, 8192 x 8192 bf16
 // 51.
-template <int TX, int TA, int MODE, int TPR, int VPT>
+template <int TX, int TA, int MODE, int TPR, int VPT, bool WHOLE>
 __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_rows_kernel(
     NormArgs a) {
     constexpr int RPB = TPR >= kNormThreads ? 1 : kNormThreads / TPR;  // rows per workgroup
@@ -64,11 +66,11 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
     if constexpr (kNorms) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.gamma, at(v), a.K), gamma[v]);
+            unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.gamma, at(v), a.K), gamma[v]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) beta[v][i] = 0.0f;
             if (a.beta)
-                unpack8<TW_T_F32>(load8<TW_T_F32>((const char *)a.beta, at(v), a.K), beta[v]);
+                unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.beta, at(v), a.K), beta[v]);
         }
     }
     Vec8<TX> xv[VPT];
@@ -76,11 +78,11 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
     auto fetch = [&](int64_t m) {
         const char *xr = a.x + m * a.x_stride * type_bytes(TX);
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) xv[v] = load8<TX>(xr, at(v), a.K);
+        for (int v = 0; v < VPT; ++v) xv[v] = load8_of<WHOLE, TX>(xr, at(v), a.K);
         if constexpr (kAdds) {
             const char *ar = a.add + m * a.K * type_bytes(TA);
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) av[v] = load8<TA>(ar, at(v), a.K);
+            for (int v = 0; v < VPT; ++v) av[v] = load8_of<WHOLE, TA>(ar, at(v), a.K);
         }
     };
     const int64_t step = (int64_t)gridDim.x * RPB;
@@ -98,6 +100,10 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
                 unpack8<TA>(av[v], f);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) z[v][i] += f[i];
+            }
+            if (WHOLE && at(v) >= a.K) {  // the others read zeros past the end
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[v][i] = 0.0f;
             }
         }
         // a stored sum may be x or add itself: every element is read here by
@@ -170,8 +176,9 @@ hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
     // Measured (us at 1024, 2048, no limit): 8192 x 8192 bf16 51, 51, 66; 16384 x
     // 2048 bf16 30, 28, 35, fp32 with add 88, 92, 88; int8 16384 x 8192 71, 75, 70.
     const int64_t most = MODE == kQuant ? 1 << 20 : 256 * (TA >= 0 ? 1024 : 2048) / threads;
-    norm_rows_kernel<TX, TA, MODE, TPR, VPT>
-        <<<(unsigned)(need < most ? need : most), threads, 0, s>>>(a);
+    const unsigned grid = (unsigned)(need < most ? need : most);
+    if (a.K % 8 == 0) norm_rows_kernel<TX, TA, MODE, TPR, VPT, true><<<grid, threads, 0, s>>>(a);
+    else norm_rows_kernel<TX, TA, MODE, TPR, VPT, false><<<grid, threads, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -365,11 +372,9 @@ __global__ __launch_bounds__(kColsPerBlock *kColThreads) void norm_cols_kernel(
 
 template <int TD, int TX, int TPR, int VPT>
 hipError_t launch_bwd(const NormBwdArgs &a, int grid, hipStream_t s) {
-    constexpr auto kernel = &norm_bwd_kernel<TD, TX, TPR, VPT>;
     constexpr int lds = TPR == kWave ? kNormThreads / TPR * 2 * TPR * VPT * 8 * 4 : 0;
-    const hipError_t e = lds_limit_once<kernel>(lds);
-    if (e != hipSuccess) return e;
-    kernel<<<grid, TPR > kNormThreads ? TPR : kNormThreads, a.part ? lds : 0, s>>>(a);
+    constexpr int threads = TPR > kNormThreads ? TPR : kNormThreads;
+    norm_bwd_kernel<TD, TX, TPR, VPT><<<grid, threads, a.part ? lds : 0, s>>>(a);
     return hipGetLastError();
 }
 

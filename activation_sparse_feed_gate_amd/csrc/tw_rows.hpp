@@ -64,6 +64,12 @@ __device__ __forceinline__ Vec8<T> load8_whole(const char *row, int e, int K) {
     return v;
 }
 
+template <bool WHOLE, int T>
+__device__ __forceinline__ Vec8<T> load8_of(const char *row, int e, int K) {
+    if constexpr (WHOLE) return load8_whole<T>(row, e, K);
+    else return load8<T>(row, e, K);
+}
+
 template <int T>
 __device__ __forceinline__ void unpack8(const Vec8<T> &v, float *f) {
 #pragma unroll
