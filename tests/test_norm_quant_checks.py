@@ -256,3 +256,19 @@ def test_product_reference_by_hand():
     w = np.array([[3, 4, 127], [-1, 0, 2]], dtype=np.int8)
     v, _ = R.product(q, np.array([0.5]), w, np.array([2.0, 0.25]), np.array([1.0, -1.0]))
     assert v.tolist() == [[(3 - 8 + 16129) * 1.0 + 1.0, (-1 + 254) * 0.125 - 1.0]]
+
+
+def test_native_calls_leave_bad_arguments_to_the_checked_path(tw):
+    """On the CPU every argument is unusable: the native functions answer
+    None (no exception, no call) and the binding's own checks raise."""
+    c = tw._calls
+    x, g, w = e(4, 64), e(64), e(8, 64, dtype=I8)
+    assert c.layernorm(x, g, None, 1e-5, None, BF) is None
+    assert c.layernorm(None, "gamma", 3, object(), x, BF) is None
+    assert c.layernorm() is None and c.layernorm(x) is None
+    assert c.layernorm_backward(x, x, g, e(4), e(4), None, F32) is None
+    assert c.quant_linear(x, w, e(8), None, None, BF, None) is None
+    assert c.quant_linear(x, w, e(8), None, None, "bf16", None) is None
+    assert c.quant_gateup(x, w, e(8), w, e(8), None, None, 1e-5, None, BF, None) is None
+    with pytest.raises(ValueError, match="device tensor"):
+        tw.layernorm(x, g)
