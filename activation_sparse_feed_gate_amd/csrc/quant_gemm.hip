@@ -572,7 +572,7 @@ constexpr int kWideLds = 2 * kWideStage + 8 * kWideOut;
 __device__ __forceinline__ int wide_swz(int r) { return (r >> 1) & 7; }
 
 template <int NB>
-__global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a) {
+__global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_regions) {
     constexpr int BN = 256 / NB;  // weight rows of each matrix
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -589,7 +589,9 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a) {
     rsrc_t rx, r0, r1;
     auto at_tile = [&](int t) {
         int rb, cb;
-        xcd_tile(t, nbm, nbn, rb, cb);
+        if (row_regions == 8) xcd_tile<8>(t, nbm, nbn, rb, cb);
+        else if (row_regions == 4) xcd_tile<4>(t, nbm, nbn, rb, cb);
+        else xcd_tile<2>(t, nbm, nbn, rb, cb);
         m0 = rb * 256;
         n0 = cb * BN;
         const int mr = min(256, a.M - m0), nr = min(BN, a.N - n0);  // rows in this tile
@@ -847,8 +849,18 @@ hipError_t launch_wide(const QArgs &a, hipStream_t s) {
     const hipError_t e = lds_limit_once<kernel>(kWideLds);
     if (e != hipSuccess) return e;
     constexpr int BN = 256 / NB;
-    const int64_t tiles = ((int64_t)a.M + 255) / 256 * (((int64_t)a.N + BN - 1) / BN);
-    kernel<<<(unsigned)(tiles < 256 ? tiles : 256), 512, kWideLds, s>>>(a);
+    const int64_t nbm = ((int64_t)a.M + 255) / 256, nbn = ((int64_t)a.N + BN - 1) / BN;
+    const int64_t tiles = nbm * nbn;
+    // Regions of the 8 XCDs: with RX row regions a token row comes into 8 / RX
+    // of their L2s and a weight row into RX.  The fewest such copies, of the
+    // splits that divide the grid (16384 x 8192 x 2048: 8 regions 181 us on zeros,
+    // 2 regions 186; gateup 16384 x 2048 x 8192: 442 and 408).
+    int rx = 2;
+    for (int r = 4; r <= 8; r *= 2)
+        if (nbm % r == 0 && nbn % (8 / r) == 0 &&
+            nbm * (8 / r) + nbn * r < nbm * (8 / rx) + nbn * rx)
+            rx = r;
+    kernel<<<(unsigned)(tiles < 256 ? tiles : 256), 512, kWideLds, s>>>(a, rx);
     return hipGetLastError();
 }
 
