@@ -54,11 +54,16 @@ struct QArgs {
 
 // The value of one output element from its integer sums.
 template <int NB>
-__device__ __forceinline__ float finish(int s0, int s1, float xs, float ws0, float ws1, float b) {
+__device__ __forceinline__ float scaled(int s0, int s1, float xs, float ws0, float ws1) {
     const float v = (float)s0 * xs * ws0;
-    if constexpr (NB == 1) return v + b;
+    if constexpr (NB == 1) return v;
     // a NaN gate stays NaN
     return (v < 0.0f ? 0.0f : v) * ((float)s1 * xs * ws1);
+}
+template <int NB>
+__device__ __forceinline__ float finish(int s0, int s1, float xs, float ws0, float ws1, float b) {
+    const float v = scaled<NB>(s0, s1, xs, ws0, ws1);
+    return NB == 1 ? v + b : v;
 }
 
 __device__ __forceinline__ void put(char *y, int type, size_t o, float v) {
@@ -534,9 +539,9 @@ __global__ __launch_bounds__(WM * WN * 64) void quant_gemm_kernel(QArgs a) {
 // 256 token rows by 256 weight rows (gateup: 128 of each matrix) a workgroup
 // of 8 waves, 64 x 128 outputs each; a workgroup a CU, walking tiles, the next
 // tile's first stages on their way while a tile is written.  Measured on
-// 8-bit normal values: 16384 x 8192 x 2048 245 us, 2.25 POP/s (the 64-byte ring
-// with 256 x 256 tiles 285), gateup 16384 x 2048 x 8192 513 us (607); on zeros,
-// which draw less power, 183 and 408 us.
+// 8-bit normal values: 16384 x 8192 x 2048 237 us, 2.32 POP/s (the 64-byte ring
+// with 256 x 256 tiles 285), gateup 16384 x 2048 x 8192 484 us, 2.27 POP/s (607);
+// on zeros, which draw less power, 175 and 378 us.
 //
 // What bounds this product is the stream of operands from L2 into LDS (loads
 // alone: 150 us of the 248 that the ring above took for 16384 x 8192 x 2048
@@ -603,8 +608,8 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
     // of 64: groups 0 .. 3 of x, then of the weights.  Rows past the matrix lie
     // past the descriptor's end and read zeros.
     const int lrow = 8 * wave + (lane >> 3);
-    const int chunk = (lane & 7) ^ wide_swz(lrow);
-    const uint32_t v0 = (uint32_t)lrow * a.K + chunk * 16;
+    int chunk = (lane & 7) ^ wide_swz(lrow);
+    uint32_t v0 = (uint32_t)lrow * a.K + chunk * 16;
     const uint32_t v64 = 64u * a.K;
     auto slot = [&](int kt, int g) {
         return smem + (kt & 1) * kWideStage + (64 * g + 8 * wave) * kWideRow;
@@ -685,14 +690,13 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
     };
     // Scales of the tile at (m0, n0): of token row l32 of each block, and of
     // column l32 of each block (the outputs of a lane are other columns of its
-    // row: it gets theirs from their lanes).
+    // row).
     struct Scales {
-        float x[2], w[4], bias[4];
+        float x[2], w[4];
     };
     auto col = [&](int base, int j) {  // first output column of block j
         return base + (NB == 1 ? wn * 128 + j * 32 : wn * 64 + (j & 1) * 32);
     };
-    const float *bp = NB == 1 && a.bias ? a.bias : a.w[0].scale;
     auto load_scales = [&] {
         Scales c;
 #pragma unroll
@@ -701,7 +705,6 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         for (int j = 0; j < 4; ++j) {
             const int n = min(col(n0, j) + l32, a.N - 1);
             c.w[j] = a.w[NB == 2 ? j >> 1 : 0].scale[n];
-            c.bias[j] = NB == 1 ? bp[n] : 0.0f;
         }
         return c;
     };
@@ -710,6 +713,9 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
     load_first();
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int mt = m0, nt = n0;  // this tile; m0, n0 move on to the next below
+        // (Opaque copies: what the loads below need of these is then computed
+        // where it is used, not kept in registers through the k-loop.)
+        asm volatile("" : "+v"(chunk), "+v"(v0));
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -779,31 +785,43 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         int ln = lane;
         asm volatile("" : "+v"(ln));
         const int lr = ln & 31;
+        // The columns' scales go through it first, from the lanes that hold
+        // them to every lane's 4 columns of each register group.
+        f32x4 w[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) reinterpret_cast<float *>(out)[j * 32 + lr] = sc.w[j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                w[j][g] = *reinterpret_cast<const f32x4 *>(
+                    out + (j * 32 + 8 * g + 4 * (ln >> 5)) * 4);
         auto write_out = [&](auto type) {
             constexpr bool kF32 = decltype(type)::value == TW_T_F32;
             constexpr int ES = kF32 ? 4 : 2;
             constexpr int JP = kF32 ? 1 : 2;  // blocks of 32 columns in 128 bytes
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int j0 = 0; j0 < 4 / NB; j0 += JP)
 #pragma unroll
-                for (int j0 = 0; j0 < 4 / NB; j0 += JP) {
+                for (int i = 0; i < 2; ++i) {
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int j = j0; j < j0 + JP; ++j)
+                    for (int jj = 0; jj < JP; ++jj)
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
+                            const int j = j0 + jj, ju = NB == 2 ? 2 + j : j;
                             float v[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int ju = NB == 2 ? 2 + j : j;
-                                const int from = 8 * g + 4 * (ln >> 5) + e;
-                                const float b =
-                                    NB == 1 && a.bias ? __shfl(sc.bias[j], from) : 0.0f;
-                                v[e] = finish<NB>(acc[i][j][4 * g + e], acc[i][ju][4 * g + e],
-                                                  sc.x[i], __shfl(sc.w[j], from),
-                                                  __shfl(sc.w[ju], from), b);
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = scaled<NB>(acc[i][j][4 * g + e], acc[i][ju][4 * g + e],
+                                                  sc.x[i], w[j][g][e], w[ju][g][e]);
+                            if (NB == 1 && a.bias) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    v[e] += a.bias[min(col(nt, j) + 8 * g + 4 * (ln >> 5) + e,
+                                                       a.N - 1)];
                             }
-                            const int byte = ((j - j0) * 32 + 8 * g + 4 * (ln >> 5)) * ES;
+                            const int byte = (jj * 32 + 8 * g + 4 * (ln >> 5)) * ES;
                             char *p = out + lr * kWideRow + (((byte >> 4) ^ wide_swz(lr)) << 4) +
                                       (byte & 15);
                             if constexpr (kF32)
