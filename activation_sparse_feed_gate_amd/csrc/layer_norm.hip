@@ -66,11 +66,13 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
     if constexpr (kNorms) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.gamma, at(v), a.K), gamma[v]);
+            unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.gamma, at(v), a.K),
+                              gamma[v]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) beta[v][i] = 0.0f;
             if (a.beta)
-                unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.beta, at(v), a.K), beta[v]);
+                unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.beta, at(v), a.K),
+                                  beta[v]);
         }
     }
     Vec8<TX> xv[VPT];

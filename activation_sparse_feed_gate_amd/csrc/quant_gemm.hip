@@ -17,7 +17,7 @@
 #include <type_traits>
 
 #include "tw_gemm.hpp"
-#include "tw_internal.hpp"
+#include "tw_norm_quant.hpp"
 #include "tw_rows.hpp"
 
 namespace tw {

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "tw_internal.hpp"
+#include "tw_norm_quant.hpp"
 
 namespace {
 

@@ -4,7 +4,7 @@
 #pragma once
 
 #include "tw_device.hpp"
-#include "tw_internal.hpp"
+#include "tw_norm_quant.hpp"
 
 namespace tw {
 
@@ -24,7 +24,9 @@ struct Vec8 {
     u32x4 w[T == TW_T_F32 ? 2 : 1];
 };
 
-__host__ __device__ constexpr int type_bytes(int t) { return t == TW_T_F32 ? 4 : t == TW_T_BF16 ? 2 : 1; }
+__host__ __device__ constexpr int type_bytes(int t) {
+    return t == TW_T_F32 ? 4 : t == TW_T_BF16 ? 2 : 1;
+}
 
 // Elements e .. e+7 of a row of K; those past the end read zero.
 template <int T>
