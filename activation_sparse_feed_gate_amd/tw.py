@@ -871,7 +871,7 @@ def layernorm(x, gamma, beta=None, eps=1e-5, add=None, out_dtype=torch.bfloat16)
     without add)."""
     got = _calls.layernorm(x, gamma, beta, eps, add, out_dtype)
     if got is not None:
-        return dict(zip(("y", "sum", "mean", "rstd"), got))
+        return got
     M, K = _dims2(x, "x", "layernorm")
     dev = x.device
     out = {
@@ -891,7 +891,7 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dres=None, dx_dtype=torch.float
     dict with dx, dgamma, dbeta."""
     got = _calls.layernorm_backward(dy, x, gamma, mean, rstd, dres, dx_dtype)
     if got is not None:
-        return dict(zip(("dx", "dgamma", "dbeta"), got))
+        return got
     M, K = _dims2(x, "x", "layernorm_backward")
     dev = x.device
     out = {
@@ -939,7 +939,7 @@ def quant_linear(x, w, w_scale, bias=None, x_scale=None, out_dtype=torch.bfloat1
     the call) or int8 with x_scale; w [N][K] int8 with w_scale [N]."""
     got = _calls.quant_linear(x, w, w_scale, bias, x_scale, out_dtype, ws)
     if got is not None:
-        return got[0]
+        return got
     M, N = _dims2(x, "x", "quant_linear")[0], _dims2(w, "w", "quant_linear")[0]
     y = torch.empty((M, N), dtype=out_dtype, device=x.device)
     tw_quant_linear(x, w, w_scale, y, bias=bias, x_scale=x_scale,
@@ -954,7 +954,7 @@ def quant_gateup(x, wg, g_scale, wu, u_scale, gamma=None, beta=None, eps=1e-5, x
     got = _calls.quant_gateup(x, wg, g_scale, wu, u_scale, gamma, beta, eps, x_scale, out_dtype,
                               ws)
     if got is not None:
-        return got[0]
+        return got
     M, N = _dims2(x, "x", "quant_gateup")[0], _dims2(wg, "wg", "quant_gateup")[0]
     h = torch.empty((M, N), dtype=out_dtype, device=x.device)
     tw_quant_gateup(x, wg, g_scale, wu, u_scale, h, gamma=gamma, beta=beta, eps=eps,
