@@ -539,9 +539,9 @@ __global__ __launch_bounds__(WM * WN * 64) void quant_gemm_kernel(QArgs a) {
 // 256 token rows by 256 weight rows (gateup: 128 of each matrix) a workgroup
 // of 8 waves, 64 x 128 outputs each; a workgroup a CU, walking tiles, the next
 // tile's first stages on their way while a tile is written.  Measured on
-// 8-bit normal values: 16384 x 8192 x 2048 237 us, 2.32 POP/s (the 64-byte ring
-// with 256 x 256 tiles 285), gateup 16384 x 2048 x 8192 484 us, 2.27 POP/s (607);
-// on zeros, which draw less power, 175 and 378 us.
+// 8-bit normal values: 16384 x 8192 x 2048 218 us, 2.52 POP/s (the 64-byte ring
+// with 256 x 256 tiles 285), gateup 16384 x 2048 x 8192 445 us, 2.47 POP/s (607);
+// on zeros, which draw less power, 173 and 380 us.
 //
 // What bounds this product is the stream of operands from L2 into LDS (loads
 // alone: 150 us of the 248 that the ring above took for 16384 x 8192 x 2048
@@ -559,13 +559,18 @@ __global__ __launch_bounds__(WM * WN * 64) void quant_gemm_kernel(QArgs a) {
 //   -- Y: the next stage's A, B0, B1 have landed; all of this one is in registers
 //   3      A x B3                A and B0 of the next stage  B2, B3
 //
-// with A the wave's 64 token rows (two blocks of 32) and B0 .. B3 its blocks of
-// 32 weight rows.  Every load has one and a half stages of arithmetic to land
+// with A the wave's 64 token rows and B0 .. B3 its blocks of 32 weight rows.
+// Every load has one and a half stages of arithmetic to land
 // in (one barrier a stage, with the whole slot refilled at Y and waited for at
 // the next Y, left the loads idle for their latency in every stage).  A step
-// is 8 matrix instructions, 512 cycles with those of the SIMD's other wave, so
+// is 16 matrix instructions, 512 cycles with those of the SIMD's other wave, so
 // its reads are there when the next step begins; the last step reads each
-// sub-step of the next A as soon as it has used its own.
+// fragment of the next A as soon as it has used its own.
+//
+// 16 x 16 x 64 instructions, because power sets the pace on real operands: out
+// of registers, on 8-bit normal values, they sustain 4.16 POP/s and 32 x 32 x 32
+// ones 3.46 (4.8 both on zeros); in this kernel 218 and 236 us.  Both halves of a block of
+// weight rows run on a token fragment before the next one's: 1% over the other way.
 constexpr int kWideRow = 128;           // bytes of a row in a stage
 constexpr int kWideStage = 512 * kWideRow;
 constexpr int kWideOut = 32 * kWideRow;  // a wave's outputs on their way to memory
@@ -583,7 +588,7 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int l32 = lane & 31;
+    const int l16 = lane & 15;
     const int KT = (a.K + kWideRow - 1) / kWideRow;
     const int nbm = (a.M + 255) / 256, nbn = (a.N + BN - 1) / BN;
     const int tiles = nbm * nbn;
@@ -635,30 +640,28 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         load_b(kt, 0);
     };
     constexpr int kAB = 6, kB = 2;  // loads of a wave in each part
-    // Fragments of 32 rows from `row` on, one 32-byte sub-step of a stage.
+    // Fragment of 16 rows from `row` on, one 64-byte sub-step of a stage: lane
+    // l holds row l % 16, 16 bytes from 64 s + 16 (l / 16) on.
     auto read = [&](int kt, int row, int s) {
-        const int c = (2 * s + (lane >> 5)) ^ wide_swz(l32);
-        return lds_ld16(smem + (kt & 1) * kWideStage, (row + l32) * kWideRow + (c << 4));
+        const int c = (4 * s + (lane >> 4)) ^ wide_swz(l16);
+        return lds_ld16(smem + (kt & 1) * kWideStage, (row + l16) * kWideRow + (c << 4));
     };
     // weight rows of block j; gateup: blocks 0, 1 of the gate, 2, 3 of the up
     auto b_row = [&](int j) {
         return NB == 1 ? wn * 128 + j * 32 : (j >> 1) * 128 + wn * 64 + (j & 1) * 32;
     };
-    u32x4 fa[4][2], fb[2][4];  // [sub-step][block], [register set][sub-step]
-    auto read_a = [&](int kt, int s) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) fa[s][i] = read(kt, wm * 64 + i * 32, s);
-    };
+    u32x4 fa[2][4], fb[2][2][2];  // [sub-step][16 rows], [register set][sub-step][16 rows]
     auto read_b = [&](int kt, int j) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) fb[j & 1][s] = read(kt, 256 + b_row(j), s);
-    };
-    // [token rows][weight rows]; register r of a block is token row l32,
-    // weight row mfma32_row(r)
-    i32x16 acc[2][4];
-    auto mma = [&](int j, int s) {
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) acc[i][j] = mfma32_i8(fb[j & 1][s], fa[s][i], acc[i][j]);
+            for (int h = 0; h < 2; ++h) fb[j & 1][s][h] = read(kt, 256 + b_row(j) + 16 * h, s);
+    };
+    // [16 token rows][16 weight rows]: register r of a block is token row l16,
+    // weight row 4 (lane / 16) + r
+    i32x4 acc[4][8];
+    auto mma = [&](int j, int s, int i, int h) {
+        acc[i][2 * j + h] = mfma16_i8(fb[j & 1][s][h], fa[s][i], acc[i][2 * j + h]);
     };
     // The scheduling barriers keep each step's reads ahead of its matrix
     // instructions.
@@ -666,19 +669,26 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         read_b(kt, j + 1);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) mma(j, s);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) mma(j, s, i, h);
         __builtin_amdgcn_sched_barrier(0);
     };
     auto last_step = [&](int kt) {
         read_b(kt + 1, 0);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            mma(3, s);
-            __builtin_amdgcn_sched_barrier(0);
-            read_a(kt + 1, s);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mma(3, s, i, 0);
+                mma(3, s, i, 1);
+                __builtin_amdgcn_sched_barrier(0);
+                fa[s][i] = read(kt + 1, wm * 64 + i * 16, s);
+                __builtin_amdgcn_sched_barrier(0);
+            }
     };
     auto load_first = [&] {
         load_ab(0);
@@ -688,24 +698,23 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
             load_b(1, 1);
         }
     };
-    // Scales of the tile at (m0, n0): of token row l32 of each block, and of
-    // column l32 of each block (the outputs of a lane are other columns of its
-    // row).
+    // Scales of the tile at (m0, n0): of the lane's token rows (l16 of each
+    // block), and of two of the wave's 128 weight rows, lane and 64 + lane (the
+    // outputs of a lane are of other weight rows).
     struct Scales {
-        float x[2], w[4];
+        float x[4], w[2];
     };
-    auto col = [&](int base, int j) {  // first output column of block j
-        return base + (NB == 1 ? wn * 128 + j * 32 : wn * 64 + (j & 1) * 32);
+    // output column of the wave's weight row 64 p + c
+    auto col = [&](int base, int p, int c) {
+        return base + (NB == 1 ? wn * 128 + 64 * p : wn * 64) + c;
     };
     auto load_scales = [&] {
         Scales c;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) c.x[i] = a.x_scale[min(m0 + wm * 64 + i * 32 + l32, a.M - 1)];
+        for (int i = 0; i < 4; ++i) c.x[i] = a.x_scale[min(m0 + wm * 64 + i * 16 + l16, a.M - 1)];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = min(col(n0, j) + l32, a.N - 1);
-            c.w[j] = a.w[NB == 2 ? j >> 1 : 0].scale[n];
-        }
+        for (int p = 0; p < 2; ++p)
+            c.w[p] = a.w[NB == 2 ? p : 0].scale[min(col(n0, p, lane), a.N - 1)];
         return c;
     };
     at_tile(blockIdx.x);
@@ -717,16 +726,18 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         // where it is used, not kept in registers through the k-loop.)
         asm volatile("" : "+v"(chunk), "+v"(v0));
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
+            for (int j = 0; j < 8; ++j) acc[i][j] = i32x4{};
         // what may be outstanding besides the loads below is younger (the last
         // tile's stores)
         if (KT > 1) wait_vmcnt<kB + kAB + kB>();
         else wait_vmcnt<kB>();
         __builtin_amdgcn_s_barrier();
 #pragma unroll
-        for (int s = 0; s < 4; ++s) read_a(0, s);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fa[s][i] = read(0, wm * 64 + i * 16, s);
         read_b(0, 0);
         int kt = 0;
         for (; kt + 2 < KT; ++kt) {
@@ -762,7 +773,11 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         step(kt, 1);
         step(kt, 2);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) mma(3, s);
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) mma(3, s, i, h);
 
         // The next tile's scales and first loads (after every wave has read its
         // last fragments) are on their way while this tile is written.
@@ -784,45 +799,42 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         char *out = smem + 2 * kWideStage + wave * kWideOut;
         int ln = lane;
         asm volatile("" : "+v"(ln));
-        const int lr = ln & 31;
+        const int lr = ln & 15, lc = 4 * (ln >> 4);
         // The columns' scales go through it first, from the lanes that hold
-        // them to every lane's 4 columns of each register group.
-        f32x4 w[4][4];
+        // them to every lane's 4 columns of each block.
+        f32x4 w[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) reinterpret_cast<float *>(out)[j * 32 + lr] = sc.w[j];
+        for (int p = 0; p < 2; ++p) reinterpret_cast<float *>(out)[64 * p + ln] = sc.w[p];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                w[j][g] = *reinterpret_cast<const f32x4 *>(
-                    out + (j * 32 + 8 * g + 4 * (ln >> 5)) * 4);
+        for (int j = 0; j < 8; ++j)
+            w[j] = *reinterpret_cast<const f32x4 *>(out + (16 * j + lc) * 4);
         auto write_out = [&](auto type) {
             constexpr bool kF32 = decltype(type)::value == TW_T_F32;
             constexpr int ES = kF32 ? 4 : 2;
-            constexpr int JP = kF32 ? 1 : 2;  // blocks of 32 columns in 128 bytes
+            constexpr int JP = kF32 ? 2 : 4;  // blocks of 16 columns in 128 bytes
 #pragma unroll
-            for (int j0 = 0; j0 < 4 / NB; j0 += JP)
+            for (int j0 = 0; j0 < 8 / NB; j0 += JP)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i0 = 0; i0 < 4; i0 += 2) {
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int jj = 0; jj < JP; ++jj)
+                    for (int i = i0; i < i0 + 2; ++i)
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int j = j0 + jj, ju = NB == 2 ? 2 + j : j;
+                        for (int j = j0; j < j0 + JP; ++j) {
+                            const int ju = NB == 2 ? 4 + j : j;
                             float v[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                v[e] = scaled<NB>(acc[i][j][4 * g + e], acc[i][ju][4 * g + e],
-                                                  sc.x[i], w[j][g][e], w[ju][g][e]);
+                                v[e] = scaled<NB>(acc[i][j][e], acc[i][ju][e], sc.x[i], w[j][e],
+                                                  w[ju][e]);
                             if (NB == 1 && a.bias) {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    v[e] += a.bias[min(col(nt, j) + 8 * g + 4 * (ln >> 5) + e,
-                                                       a.N - 1)];
+                                    v[e] += a.bias[min(col(nt, 0, 16 * j + lc + e), a.N - 1)];
                             }
-                            const int byte = (jj * 32 + 8 * g + 4 * (ln >> 5)) * ES;
-                            char *p = out + lr * kWideRow + (((byte >> 4) ^ wide_swz(lr)) << 4) +
+                            const int r = 16 * (i - i0) + lr;
+                            const int byte = (16 * (j - j0) + lc) * ES;
+                            char *p = out + r * kWideRow + (((byte >> 4) ^ wide_swz(r)) << 4) +
                                       (byte & 15);
                             if constexpr (kF32)
                                 *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
@@ -830,13 +842,13 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
                                 *reinterpret_cast<u32x2 *>(p) =
                                     u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
                         }
-                    const int n = col(nt, j0) + (ln & 7) * (16 / ES);
+                    const int n = col(nt, 0, 16 * j0 + (ln & 7) * (16 / ES));
 #pragma unroll
                     for (int it = 0; it < 4; ++it) {
                         const int r = it * 8 + (ln >> 3);
                         const u32x4 v =
                             lds_ld16(out, r * kWideRow + (((ln & 7) ^ wide_swz(r)) << 4));
-                        const int m = mt + wm * 64 + i * 32 + r;
+                        const int m = mt + wm * 64 + i0 * 16 + r;
                         if (m >= a.M) continue;
                         char *p = a.y + ((size_t)m * a.N + n) * ES;
                         if (n + 16 / ES <= a.N) {
