@@ -883,8 +883,8 @@ hipError_t launch_wide(const QArgs &a, hipStream_t s) {
     const int64_t tiles = nbm * nbn;
     // Regions of the 8 XCDs: with RX row regions a token row comes into 8 / RX
     // of their L2s and a weight row into RX.  The fewest such copies, of the
-    // splits that divide the grid (16384 x 8192 x 2048: 8 regions 181 us on zeros,
-    // 2 regions 186; gateup 16384 x 2048 x 8192: 442 and 408).
+    // splits that divide the grid (on zeros, 16384 x 8192 x 2048: 8 row regions
+    // 172 us, 2 regions 178; gateup 16384 x 2048 x 8192: 411 and 380).
     int rx = 2;
     for (int r = 4; r <= 8; r *= 2)
         if (nbm % r == 0 && nbn % (8 / r) == 0 &&
@@ -933,9 +933,9 @@ hipError_t launch_product(const QArgs &a, hipStream_t s) {
     // Larger tiles do more arithmetic per byte loaded, so the largest whose
     // grid occupies about half the chip or more.  Measured (us, linear; tiles
     // of 256 x 256, 128 x 128, 64 x 64):
-    //   K = 2048, N = 5632    512 rows 26.9, 15.3, 17.4   1536 rows 29.0, 37.0, 41.4
-    //   K = 5632, N = 2048   1024 rows 57.7, 28.4, 27.1   4096 rows 61.1, 68.2, 101
-    //   K = 1024, N = 4096    512 rows 17.6, 10.4, 8.5    2048 rows 19.5, 19.1, 23.2
+    //   K = 2048, N = 5632    512 rows 25.1, 15.5, 17.6   1536 rows 27.0, 35.8, 40.4
+    //   K = 5632, N = 2048   1024 rows 56.8, 29.2, 28.3   4096 rows 58.9, 66.4, 99.1
+    //   K = 1024, N = 4096    512 rows 15.7, 10.9, 8.7    2048 rows 17.7, 18.2, 22.2
     if (tiles(256, 256 / NB) >= 120) return launch_wide<NB>(a, s);
     if constexpr (NB == 1) {
         if (tiles(128, 128) >= 144) return launch_tiles<128, 128, 2, 4, 4, 1>(a, s);
