@@ -70,7 +70,9 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
                               gamma[v]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) beta[v][i] = 0.0f;
-            if (a.beta)
+            // none past the end, where z stays 0 and the row's maximum must not
+            // see another vector's
+            if (a.beta && (!WHOLE || at(v) < a.K))
                 unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.beta, at(v), a.K),
                                   beta[v]);
         }
