@@ -55,10 +55,24 @@ def serve(x, layers, gamma_out, beta_out=None, eps=1e-5):
 
 def train_forward(x, gamma, beta, wg_t, wu_t, wd, T=128, C=128, P=128, R_max=None, eps=1e-5):
     """y = x + FFN(norm(x)) for training (fp32 [M][K]); x fp32 or bf16, weights
-    bf16.  Returns (y, what ``train_backward`` needs)."""
+    bf16.  Returns (y, what ``train_backward`` needs).
+
+    A row with more than P active neurons, or more than C in one tile of T (at
+    random initialisation about half of N are active), lives in the dense
+    backup of R_max rows: by default there is one for every row.  For a smaller
+    backup the call waits for the number of rows that need it and raises where
+    they do not fit, since such a row would have no output."""
+    M, N = x.shape[0], wg_t.shape[0]
+    # the backup's own limit is 2^31 elements
+    R_max = min(M, (2 ** 31 - 1) // N if R_max is None else R_max)
     n = tw.layernorm(x, gamma, beta, eps)
     packed = tw.pack_gate(n["y"], wg_t, T, C, 0)
     f, hy = tw.hybrid_forward(n["y"], wg_t, wu_t, wd, packed, P=P, R_max=R_max)
+    if R_max < M:
+        need = int(hy["bk_count"])
+        if need > R_max:
+            raise RuntimeError(f"train_forward: {need} rows have more active neurons than a "
+                               f"sparse row holds, the dense backup has room for {R_max}")
     return x.float() + f, dict(x=x, n=n, hy=hy, gamma=gamma, weights=(wg_t, wu_t, wd))
 
 
