@@ -283,10 +283,14 @@ void norm_bwd_kernel(NormBwdArgs a) {
         for (int v = 0; v < VPT; ++v) {
             unpack8<TD>(dv[v], g[v]);
             unpack8<TX>(xv[v], n[v]);
-            // past the end dy = gamma = 0, and n is finite unless the whole
-            // row's statistics are not
+            const int left = a.K - 8 * (v * TPR + t);
+            if (left >= 8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) n[v][i] = (n[v][i] - mean) * r;
+                for (int i = 0; i < 8; ++i) n[v][i] = (n[v][i] - mean) * r;
+            } else {  // past the end zero: -mean r may be infinite, and 0 inf is NaN
+#pragma unroll
+                for (int i = 0; i < 8; ++i) n[v][i] = i < left ? (n[v][i] - mean) * r : 0.0f;
+            }
         }
         if (kAhead && m + step < a.M) fetch(m + step);
         float s1 = 0.0f, s2 = 0.0f;
