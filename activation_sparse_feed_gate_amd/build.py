@@ -48,7 +48,8 @@ def _calls_flags() -> list:
 
 def build(verbose: bool = False) -> str:
     """Compile all sources (in parallel) and link ``libtw.so`` and, to it,
-    ``_tw_calls.so``; returns the library's path."""
+    ``_tw_calls.so``; returns the library's path.  A failure of the latter alone
+    raises with the library built and no older ``_tw_calls.so`` beside it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     procs = []
     objs = []
@@ -71,14 +72,18 @@ def build(verbose: bool = False) -> str:
             sys.stderr.write(out.decode(errors="replace"))
         if p.returncode:
             failed.append(src)
-    if failed:
+    if any(src in SOURCES for src in failed):
         raise RuntimeError(f"hipcc failed for {failed}")
+    if os.path.exists(CALLS):  # never an older one beside a newer library
+        os.remove(CALLS)
     tmp = LIBRARY + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIBRARY)
+    if failed:
+        raise RuntimeError(f"hipcc failed for {failed}")
     tmp = CALLS + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", calls_obj, "-o", tmp, "-L", HERE, "-l:libtw.so", "-L",
            os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_hip",

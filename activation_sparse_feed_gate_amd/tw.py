@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch  # loads the HIP runtime the library links against
 
@@ -40,8 +41,19 @@ _lib = ctypes.CDLL(LIBRARY)
 # The small allocating calls (layernorm, quant_linear, ...) in native code: it
 # checks, allocates and calls the library, and returns None for any argument
 # that is not as the library needs it; the call is then made through the
-# low-level function here, whose checks raise.
-from . import _tw_calls as _calls  # noqa: E402  (built beside the library)
+# low-level function here, whose checks raise.  It is bound to one build of
+# torch: where it does not load, every call takes the second way (the same
+# kernels, with more host time a call).
+try:
+    from . import _tw_calls as _calls  # built beside the library
+except ImportError as _e:
+    warnings.warn(f"the native part of the binding does not load ({_e}): the layer norm and int8 "
+                  "calls take more host time each; build it with "
+                  "`python -m activation_sparse_feed_gate_amd.build`", RuntimeWarning, stacklevel=2)
+
+    class _calls:  # noqa: N801
+        layernorm = layernorm_backward = quant_linear = quant_gateup = staticmethod(lambda *a: None)
+
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
