@@ -18,6 +18,7 @@
 
 #include "tw_gemm.hpp"
 #include "tw_norm_quant.hpp"
+#include "tw_quant_rules.hpp"
 #include "tw_rows.hpp"
 
 namespace tw {
@@ -341,28 +342,6 @@ void quant_few_kernel(QArgs a, FewRows f, int R) {
     }
 }
 
-// A CU runs one workgroup of these well; a second one on the same CU, or a
-// second round, costs about as much as the first.  So the block grows (which
-// also has the token rows read by fewer workgroups) until the grid is at most
-// one workgroup a CU.
-constexpr int kFewGrid = 256;
-inline bool few_fits(int M, int N, int MB, int NC) {
-    return ((int64_t)M + 16 * MB - 1) / (16 * MB) * (((int64_t)N + 16 * NC - 1) / (16 * NC)) <=
-           kFewGrid;
-}
-
-// Weight rows a workgroup of one row block takes: an even share of N over that
-// many workgroups, so that every CU streams as much (the other rows of its
-// last block of 16 repeat the last one's and are not stored).  At least 8
-// where each workgroup also quantises the rows.  Measured (us, one row, 16 NC
-// against this): linear 5632 x 2048 6.1, 5.3; gateup 5632 x 2048 10.6, 8.9, 2048
-// x 5632 8.0, 7.6.
-inline int few_rows(int N, int NC, bool fused) {
-    const int share = (N + kFewGrid - 1) / kFewGrid, least = fused ? 8 : 4;
-    const int R = share < least ? least : (share + 1) / 2 * 2;
-    return R < 16 * NC ? R : 16 * NC;
-}
-
 template <int TX, int WPR, int VEC, int MB, int NC, int NB, int PF>
 hipError_t launch_few(const QArgs &a, const FewRows &f, hipStream_t s) {
     constexpr auto kernel = &quant_few_kernel<TX, WPR, VEC, MB, NC, NB, PF>;
@@ -371,7 +350,7 @@ hipError_t launch_few(const QArgs &a, const FewRows &f, hipStream_t s) {
     const hipError_t e = lds_limit_once<kernel>(sums + most);
     if (e != hipSuccess) return e;
     const int lds = sums + (TX != TW_T_INT8 ? a.M * (a.K + kFewPad) : 0);
-    const int R = MB == 1 ? few_rows(a.N, NC, TX != TW_T_INT8) : 16 * NC;
+    const int R = MB == 1 ? few_rows(a.M, a.N, NC, TX != TW_T_INT8) : 16 * NC;
     const dim3 grid((a.N + R - 1) / R, (a.M + 16 * MB - 1) / (16 * MB));
     kernel<<<grid, kFewWaves * kWave, lds, s>>>(a, f, R);
     return hipGetLastError();
@@ -913,9 +892,9 @@ hipError_t launch_product(const QArgs &a, hipStream_t s) {
     };
     // Up to 64 rows per 128 columns or so: the smallest block whose grid fits.
     // Measured (us, K = 2048, N = 1001; K = 5632, N = 2048; K = 2048, N = 5632):
-    //   32 rows   16x16 4.0, 7.7, 8.0   32x16 4.9, 10.1, 8.0   32x32 5.9, 13.0, 6.4
-    //   64 rows   16x16 4.3, 12.4, 13.3   32x16 5.0, 10.1, 10.8   64x32 8.1, 18.6, 8.8
-    //   128 rows  32x16 5.3, 18.8, 19.0   32x32 6.0, 13.1, 13.8   tiles 8.8, 16.8, 9.4
+    //   32 rows   16x16 3.9, 7.7, 8.1   32x16 4.9, 10.1, 8.1   32x32 5.9, 13.1, 6.5
+    //   64 rows   16x16 4.3, 12.4, 13.4   32x16 5.0, 10.2, 10.8   64x32 8.2, 18.6, 9.1
+    //   128 rows  32x16 5.3, 18.9, 19.6   32x32 6.0, 13.1, 14.0   tiles 8.3, 17.2, 9.3
     // Where none fits, 64 x 64 tiles, unless they would leave most CUs idle
     // and the rows are few (N = 8192, K = 2048, 16 rows: 16x32 5.7, tiles 8.6;
     // N = 14336, K = 4096: 15.9 against 13.0).
@@ -927,7 +906,7 @@ hipError_t launch_product(const QArgs &a, hipStream_t s) {
     if (few_fits(a.M, a.N, 1, 1)) return launch_few<TW_T_INT8, 0, 0, 1, 1, NB>(a, none, s);
     if (few_fits(a.M, a.N, 2, 1)) return launch_few<TW_T_INT8, 0, 0, 2, 1, NB>(a, none, s);
     if (few_fits(a.M, a.N, 2, 2)) return launch_few<TW_T_INT8, 0, 0, 2, 2, NB>(a, none, s);
-    // 64 x 32: up to 64 rows (128 rows: 18.6 against 16.8 at K = 5632)
+    // 64 x 32: up to 64 rows (128 rows: 18.6 against 17.2 at K = 5632)
     if (a.M <= 64 && few_fits(a.M, a.N, 4, 2))
         return launch_few<TW_T_INT8, 0, 0, 4, 2, NB>(a, none, s);
     // Larger tiles do more arithmetic per byte loaded, so the largest whose
