@@ -860,16 +860,8 @@ hipError_t launch_wide(const QArgs &a, hipStream_t s) {
     constexpr int BN = 256 / NB;
     const int64_t nbm = ((int64_t)a.M + 255) / 256, nbn = ((int64_t)a.N + BN - 1) / BN;
     const int64_t tiles = nbm * nbn;
-    // Regions of the 8 XCDs: with RX row regions a token row comes into 8 / RX
-    // of their L2s and a weight row into RX.  The fewest such copies, of the
-    // splits that divide the grid (on zeros, 16384 x 8192 x 2048: 8 row regions
-    // 172 us, 2 regions 178; gateup 16384 x 2048 x 8192: 411 and 380).
-    int rx = 2;
-    for (int r = 4; r <= 8; r *= 2)
-        if (nbm % r == 0 && nbn % (8 / r) == 0 &&
-            nbm * (8 / r) + nbn * r < nbm * (8 / rx) + nbn * rx)
-            rx = r;
-    kernel<<<(unsigned)(tiles < 256 ? tiles : 256), 512, kWideLds, s>>>(a, rx);
+    kernel<<<(unsigned)(tiles < 256 ? tiles : 256), 512, kWideLds, s>>>(
+        a, wide_row_regions(nbm, nbn));
     return hipGetLastError();
 }
 

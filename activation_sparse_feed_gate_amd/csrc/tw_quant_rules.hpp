@@ -33,4 +33,25 @@ constexpr int few_rows(int M, int N, int NC, bool fused) {
     return (int)(R < 16 * NC ? R : 16 * NC);
 }
 
+// ---- large tiles: row regions of the 8 XCDs ---------------------------------
+// With r row regions (and 8 / r column regions) a token row comes into 8 / r of
+// the L2s and a weight row into r: the fewest such copies of the splits into 2,
+// 4 and 8 row regions that divide the grid of nbm x nbn tiles.  2 where none
+// does: the grid is then walked without regions.  Measured (us): on zeros,
+// 16384 x 8192 x 2048, 8 regions 172, 2 regions 178, gateup 16384 x 2048 x 8192
+// 411 and 380; on normal values, 4 regions against the undivided walk, gateup 4096
+// x 1024 x 4352 43.2, 46.2, linear 2048 x 5632 x 5632 59.3, 60.9.
+constexpr int wide_row_regions(int64_t nbm, int64_t nbn) {
+    int best = 0;
+    int64_t copies = 0;
+    for (int r = 2; r <= 8; r *= 2) {
+        if (nbm % r || nbn % (8 / r)) continue;
+        const int64_t c = nbm * (8 / r) + nbn * r;
+        if (best && c >= copies) continue;
+        best = r;
+        copies = c;
+    }
+    return best ? best : 2;
+}
+
 }  // namespace tw

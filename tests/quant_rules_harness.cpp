@@ -1,6 +1,7 @@
 // Host checks of the rules that spread the int8 products over the chip
 // (tw_quant_rules.hpp), over many sizes; prints RULES_OK.
 #include <cstdio>
+#include <initializer_list>
 
 #include "tw_quant_rules.hpp"
 
@@ -33,10 +34,32 @@ void few() {
     expect(few_rows(1, 1 << 24, 2, false) == 32 && few_rows(1 << 24, 5, 1, false) == 5 + 1, "extremes", 0, 0);
 }
 
+// Row regions of the large tiles: 2, 4 or 8; a split that divides the grid
+// wherever one does, and no other such split with fewer operand copies.
+void regions() {
+    using namespace tw;
+    auto divides = [](int m, int n, int r) { return m % r == 0 && n % (8 / r) == 0; };
+    auto copies = [](int m, int n, int r) { return m * (8 / r) + n * r; };
+    for (int m = 1; m <= 200; ++m)
+        for (int n = 1; n <= 200; ++n) {
+            const int got = wide_row_regions(m, n);
+            expect(got == 2 || got == 4 || got == 8, "regions", m, n);
+            for (int r : {2, 4, 8}) {
+                if (!divides(m, n, r)) continue;
+                expect(divides(m, n, got), "a split that divides", m, n);
+                expect(copies(m, n, got) <= copies(m, n, r), "fewest copies", m, n);
+            }
+        }
+    expect(wide_row_regions(64, 8) == 8 && wide_row_regions(64, 16) == 4 && wide_row_regions(16, 16) == 2 &&
+               wide_row_regions(8, 7) == 8 && wide_row_regions(8, 34) == 4 && wide_row_regions(20, 17) == 2,
+           "regions by hand", 0, 0);
+}
+
 }  // namespace
 
 int main() {
     few();
+    regions();
     if (g_fail) return 1;
     std::printf("RULES_OK\n");
     return 0;
