@@ -261,6 +261,8 @@ class _Args:
 def _dims2(t, name, where):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{where}: {name} must be a two-dimensional tensor")
+    if max(t.shape) >= 2 ** 31:  # the library's sizes are 32-bit: it would see the rest of it
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, sizes must be below 2^31")
     return t.shape
 
 
