@@ -13,8 +13,11 @@
 //     ring; no epilogue) at the 0.5B and 2B block shapes on all-zero,
 //     constant and pseudo-random operands.  The part lowers its clock under
 //     the power that toggling multiplier inputs draw, so the same
-//     instructions run at different rates on different data.
-// Each of the first four figures is the best of a few repetitions (the first
+//     instructions run at different rates on different data;
+//   - the int8 rate of both instruction shapes out of registers, a wave tile
+//     of 64 x 128 outputs as the int8 large tiles have it, on zeros and on
+//     normal 8-bit values (standard deviation 30).
+// Each of the register and stream figures is the best of a few repetitions (the first
 // launches run while the clocks ramp up); the main-loop figures are the
 // median of ten launches after four warm-up ones.
 #include <hip/hip_runtime.h>
@@ -98,6 +101,79 @@ __global__ __launch_bounds__(WAVES * 64) void mfma_loop_rand(float *out, int ite
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += acc[i][e];
     out[(size_t)blockIdx.x * blockDim.x + threadIdx.x] = s;
+}
+
+// Four 8-bit codes, normal with a standard deviation of 30 (twelve uniform
+// values, added), from a hash of (seed, index).
+__device__ inline uint32_t normal_codes(uint32_t seed, uint32_t i) {
+    uint32_t w = 0, r = hash32(seed * 0x9e3779b9u + i);
+    for (int b = 0; b < 4; ++b) {
+        float u = -6.0f;
+        for (int j = 0; j < 12; ++j) {
+            r = hash32(r + 1);
+            u += (float)(r >> 8) * 0x1p-24f;
+        }
+        const float c = fminf(fmaxf(rintf(30.0f * u), -127.0f), 127.0f);
+        w |= ((uint32_t)(int)c & 0xffu) << (8 * b);
+    }
+    return w;
+}
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+// 64 x 128 outputs a wave, 64 of K an iteration: 32 instructions of 16 x 16 x 64
+// (S16) or 16 of 32 x 32 x 32.
+template <bool S16>
+__global__ __launch_bounds__(512) void int8_loop(int *out, int iters, int normal) {
+    const uint32_t g = blockIdx.x * blockDim.x + threadIdx.x;
+    i32x4 f[12];
+#pragma unroll
+    for (int j = 0; j < 12; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[j][e] = normal ? (int)normal_codes(g, 4 * j + e) : 0;
+    int v = 0;
+    if constexpr (S16) {
+        i32x4 acc[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = i32x4{};
+        for (int it = 0; it < iters; ++it)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f[4 + j], f[i], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v ^= acc[i][j][e];
+    } else {
+        i32x16 acc[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = i32x16{};
+        for (int it = 0; it < iters; ++it)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[4 + 2 * j + h], f[2 * i + h],
+                                                                          acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v ^= acc[i][j][e];
+    }
+    out[g] = v;  // keeps the products live
 }
 
 // The gate GEMM's main loop alone: A [M][K] and B [N][K] bf16, 256 x 256
@@ -284,6 +360,21 @@ int main() {
     tf = (double)kGrid * 8 * kIters * 8 * mfma_flop / ms / 1e9;
     std::printf("bf16 MFMA, 2 waves per SIMD, pseudo-random operands: %.1f TFLOP/s (%.1f%% of %.1f)\n",
                 tf, 100 * tf / kPeakBf16, kPeakBf16);
+
+    constexpr double kPeakI8 = 2 * kPeakBf16;
+    const double loop_ops = 256.0 * 8 * kIters * 64 * 128 * 64 * 2;  // 256 workgroups of 8 waves
+    int *iout = reinterpret_cast<int *>(out);
+    for (int normal = 0; normal < 2; ++normal)
+        for (int s16 = 0; s16 < 2; ++s16) {
+            CHECK(timed([&] {
+                      if (s16) hipLaunchKernelGGL(int8_loop<true>, dim3(256), dim3(512), 0, 0, iout, kIters, normal);
+                      else hipLaunchKernelGGL(int8_loop<false>, dim3(256), dim3(512), 0, 0, iout, kIters, normal);
+                  }, ms));
+            tf = loop_ops / ms / 1e9;
+            std::printf("int8 MFMA %s, 2 waves per SIMD, %s: %.1f TOP/s (%.1f%% of %.1f)\n",
+                        s16 ? "16x16x64" : "32x32x32", normal ? "normal values" : "zeros", tf,
+                        100 * tf / kPeakI8, kPeakI8);
+        }
     CHECK(hipFree(out));
 
     // the gate's main loop at the 0.5B and 2B block shapes, by operand values
