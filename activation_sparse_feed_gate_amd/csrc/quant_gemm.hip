@@ -95,7 +95,13 @@ struct FewRows {
 };
 
 // Fused rows: WPR waves share a token row, 8 / WPR rows at once; a thread
-// holds up to 2 vectors of 8 elements of its row.
+// holds up to 2 vectors of 8 elements of its row, so 1, 2 and 4 rows may be of
+// 8192, 4096 and 2048 elements (8 rows, a wave each, of 1024 only).  Measured (us,
+// K x N, fused against a quantiser's launch of its own): one row, linear 5632 x
+// 2048 5.3, 7.5, gateup 8.9, 10.5; two, 2048 x 5632 4.4, 6.6, gateup 7.3, 9.4, 4096 x
+// 4096 6.7, 7.8, gateup 11.8, 11.5; four, 2048 x 5632 4.7, 6.8, gateup 8.3, 9.7.  The
+// two sum a norm in different orders, so a code half way between two may
+// differ between a call of few rows and one of many.
 constexpr int kFusedRows = 4;
 __host__ __device__ constexpr int fused_row_waves(int M) { return M <= 1 ? 8 : M <= 2 ? 4 : 2; }
 constexpr int fused_max_k(int M) { return fused_row_waves(M) * kWave * 16; }
@@ -518,9 +524,10 @@ __global__ __launch_bounds__(WM * WN * 64) void quant_gemm_kernel(QArgs a) {
 // 256 token rows by 256 weight rows (gateup: 128 of each matrix) a workgroup
 // of 8 waves, 64 x 128 outputs each; a workgroup a CU, walking tiles, the next
 // tile's first stages on their way while a tile is written.  Measured on
-// 8-bit normal values: 16384 x 8192 x 2048 218 us, 2.52 POP/s (the 64-byte ring
-// with 256 x 256 tiles 285), gateup 16384 x 2048 x 8192 445 us, 2.47 POP/s (607);
-// on zeros, which draw less power, 173 and 380 us.
+// 8-bit normal values, from session to session: 16384 x 8192 x 2048 207 to 238 us, 2.3
+// to 2.65 POP/s (the 64-byte ring with 256 x 256 tiles 285), gateup 16384 x 2048 x
+// 8192 445 to 489 us, 2.25 to 2.47 POP/s (607); on zeros, which draw less power,
+// 173 and 380 us in all of them.
 //
 // What bounds this product is the stream of operands from L2 into LDS (loads
 // alone: 150 us of the 248 that the ring above took for 16384 x 8192 x 2048
@@ -547,9 +554,10 @@ __global__ __launch_bounds__(WM * WN * 64) void quant_gemm_kernel(QArgs a) {
 // fragment of the next A as soon as it has used its own.
 //
 // 16 x 16 x 64 instructions, because power sets the pace on real operands: out
-// of registers, on 8-bit normal values, they sustain 4.16 POP/s and 32 x 32 x 32
-// ones 3.46 (4.8 both on zeros); in this kernel 218 and 236 us.  Both halves of a block of
-// weight rows run on a token fragment before the next one's: 1% over the other way.
+// of registers, on 8-bit normal values, they sustain 3.7 POP/s and 32 x 32 x 32 ones
+// 3.3 (4.9 and 4.8 on zeros; peak_probe.hip); in this kernel, in one session, 218 and
+// 236 us.  Both halves of a block of weight rows run on a token fragment before
+// the next one's: 1% over the other way.
 constexpr int kWideRow = 128;           // bytes of a row in a stage
 constexpr int kWideStage = 512 * kWideRow;
 constexpr int kWideOut = 32 * kWideRow;  // a wave's outputs on their way to memory
@@ -708,8 +716,10 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] = i32x4{};
-        // what may be outstanding besides the loads below is younger (the last
-        // tile's stores)
+        // What may be outstanding besides the loads below is younger: the last
+        // tile's stores, 8 to 32 of them.  They are among the operations that the
+        // counts below leave outstanding, so from the second tile on these waits
+        // hold for more of the loads than stage 0's first six.
         if (KT > 1) wait_vmcnt<kB + kAB + kB>();
         else wait_vmcnt<kB>();
         __builtin_amdgcn_s_barrier();
@@ -806,6 +816,9 @@ __global__ __launch_bounds__(512) void quant_wide_kernel(QArgs a, int row_region
                             for (int e = 0; e < 4; ++e)
                                 v[e] = scaled<NB>(acc[i][j][e], acc[i][ju][e], sc.x[i], w[j][e],
                                                   w[ju][e]);
+                            // (read behind the next tile's first loads, which each
+                            // wait here includes: 16384 x 1024 x 4096 110 us with a
+                            // bias, 80 without; 16384 x 8192 x 2048 237 and 227)
                             if (NB == 1 && a.bias) {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)

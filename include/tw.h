@@ -503,6 +503,10 @@ tw_status tw_layernorm_quant(const void *x, int x_type, int64_t x_stride, const 
  *   ws    ws_bytes >= tw_quant_workspace_bytes(M, K); may be NULL for int8 x
  * K a positive multiple of 16, at most 65536 (16384 with gamma); M and N up
  * to 2^24, and at most 2^37 outputs.  Results are bit-identical run to run.
+ * Calls of up to 4 float rows norm and quantise them in the product's kernel,
+ * which sums a norm in another order than tw_layernorm_quant: with gamma, a
+ * code whose value lies half way between two (within fp32 rounding) may
+ * differ between a row in a call of few rows and the same row among many.
  * events: [0] before, [1] after the quantisation, [2] after the product
  * (events[0] and [1] are recorded together where one kernel does both).
  */
