@@ -23,7 +23,8 @@ CALLS = os.path.join(HERE, "_tw_calls.so")  # native part of the Python binding 
 PEAK_PROBE = os.path.join(HERE, "peak_probe")  # achievable-peak program (csrc/peak_probe.hip)
 
 SOURCES = ["gate_twell.hip", "pack_dense.hip", "sparse_updown.hip", "dense_ffn.hip", "hybrid.hip",
-           "layer_norm.hip", "quant_gemm.hip", "tw_api.cpp"]
+           "layer_norm.hip", "quant_gemm.hip", "gated_ffn.hip", "linear_ce.hip", "grad_clip.hip",
+           "tw_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

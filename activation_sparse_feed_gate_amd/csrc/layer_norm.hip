@@ -17,9 +17,14 @@
 // in registers; the workgroups' shares go to the workspace and a second
 // kernel adds them in a fixed order (no atomics: results do not depend on
 // timing).
+//
+// The RMS norm is the same without the mean and beta (kRms): rstd =
+// 1 / sqrt(sum(z^2) / K + eps), y = z rstd gamma, and its gradient without the
+// mean's term, dx = rstd (t - n sum(t n) / K) (+ dres) with n = z rstd.
 #include <type_traits>
 
 #include "tw_rows.hpp"
+#include "tw_train.hpp"
 
 namespace tw {
 namespace {
@@ -40,8 +45,8 @@ struct NormArgs {
 };
 
 // What becomes of a row: its norm, the norm quantised to int8, or the row
-// itself quantised.
-enum { kNorm = 0, kNormQuant = 1, kQuant = 2 };
+// itself quantised; its RMS norm, that quantised.
+enum { kNorm = 0, kNormQuant = 1, kQuant = 2, kRms = 3, kRmsQuant = 4 };
 
 // TPR threads hold a row, VPT vectors of 8 elements each (vector v of thread
 // t starts at element 8 (v TPR + t): every load of a wave is contiguous).
@@ -57,17 +62,19 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
     NormArgs a) {
     constexpr int RPB = TPR >= kNormThreads ? 1 : kNormThreads / TPR;  // rows per workgroup
     constexpr bool kNorms = MODE != kQuant, kAdds = TA >= 0;
+    constexpr bool kCentres = MODE == kNorm || MODE == kNormQuant;
     constexpr bool kAhead = VPT <= 4;  // registers for the next row
     __shared__ float red[2 * (TPR / kWave)];
     RowReduce<TPR> rr(red);
     const int t = threadIdx.x % TPR;
     auto at = [&](int v) { return 8 * (v * TPR + t); };
-    float gamma[kNorms ? VPT : 1][8], beta[kNorms ? VPT : 1][8];
+    float gamma[kNorms ? VPT : 1][8], beta[kCentres ? VPT : 1][8];
     if constexpr (kNorms) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             unpack8<TW_T_F32>(load8_of<WHOLE, TW_T_F32>((const char *)a.gamma, at(v), a.K),
                               gamma[v]);
+            if constexpr (!kCentres) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i) beta[v][i] = 0.0f;
             // none past the end, where z stays 0 and the row's maximum must not
@@ -120,7 +127,25 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
                     store8<TX>(a.sum + m * a.K * type_bytes(TX), at(v), a.K, z[v]);
             }
         }
-        if constexpr (kNorms) {
+        if constexpr (kNorms && !kCentres) {
+            float s = 0.0f;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += z[v][i] * z[v][i];  // zeros past the end
+            const float rstd = 1.0f / sqrtf(rr.sum(s) / a.K + a.eps);
+            if (t == 0 && a.rstd) a.rstd[m] = rstd;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                // (an infinite rstd, of a row of zeros without eps, must not
+                // make NaNs of the zeros past the end)
+                if (at(v) >= a.K) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (WHOLE || at(v) + i < a.K) z[v][i] = z[v][i] * rstd * gamma[v][i];
+            }
+        }
+        if constexpr (kCentres) {
             float s = 0.0f;
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
@@ -151,7 +176,7 @@ __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads) void norm_
                 for (int i = 0; i < 8; ++i)
                     z[v][i] = z[v][i] * rstd * gamma[v][i] + beta[v][i];
         }
-        if constexpr (MODE == kNorm) {
+        if constexpr (MODE == kNorm || MODE == kRms) {
             char *yr = a.y + m * a.K * (a.y_type == TW_T_F32 ? 4 : 2);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) store8_as(a.y_type, yr, at(v), a.K, z[v]);
@@ -247,7 +272,7 @@ constexpr int norm_bwd_cols(int K) { return norm_bwd_tpr(K) * norm_bwd_vpt(K) * 
 // them, waits for them too, as loads complete in order.  Up to K = 1024, where a
 // wave walks few rows, that latency bounds the kernel (4096 x 1024, fp32 dy: 12
 // us for 42 MB); from 2048 on it runs at the rate of a copy.
-template <int TD, int TX, int TPR, int VPT>
+template <int TD, int TX, int TPR, int VPT, bool RMS>
 __global__ __launch_bounds__(TPR > kNormThreads ? TPR : kNormThreads, 2)
 void norm_bwd_kernel(NormBwdArgs a) {
     constexpr int RPB = TPR > kNormThreads ? 1 : kNormThreads / TPR;
@@ -257,11 +282,11 @@ void norm_bwd_kernel(NormBwdArgs a) {
     __shared__ float red[2 * (TPR / kWave)];
     RowReduce<TPR> rr(red);
     const int t = threadIdx.x % TPR;
-    float dg[VPT][8], db[VPT][8];
+    float dg[VPT][8], db[RMS ? 1 : VPT][8];
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dg[v][i] = db[v][i] = 0.0f;
+        for (int i = 0; i < 8; ++i) dg[v][i] = db[RMS ? 0 : v][i] = 0.0f;
 
     Vec8<TD> dv[VPT];
     Vec8<TX> xv[VPT];
@@ -269,7 +294,7 @@ void norm_bwd_kernel(NormBwdArgs a) {
     auto fetch = [&](int64_t m) {
         const char *dr = a.dy + m * a.K * type_bytes(TD);
         const char *xr = a.x + m * a.x_stride * type_bytes(TX);
-        mean = a.mean[m];
+        if constexpr (!RMS) mean = a.mean[m];
         rstd = a.rstd[m];
 #pragma unroll
         for (int v = 0; v < VPT; ++v) dv[v] = load8<TD>(dr, 8 * (v * TPR + t), a.K);
@@ -290,10 +315,11 @@ void norm_bwd_kernel(NormBwdArgs a) {
             const int left = a.K - 8 * (v * TPR + t);
             if (left >= 8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n[v][i] = (n[v][i] - mean) * r;
+                for (int i = 0; i < 8; ++i) n[v][i] = RMS ? n[v][i] * r : (n[v][i] - mean) * r;
             } else {  // past the end zero: -mean r may be infinite, and 0 inf is NaN
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n[v][i] = i < left ? (n[v][i] - mean) * r : 0.0f;
+                for (int i = 0; i < 8; ++i)
+                    n[v][i] = i < left ? (RMS ? n[v][i] * r : (n[v][i] - mean) * r) : 0.0f;
             }
         }
         if (kAhead && m + step < a.M) fetch(m + step);
@@ -305,13 +331,13 @@ void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dg[v][i] += g[v][i] * n[v][i];
-                db[v][i] += g[v][i];
+                if constexpr (!RMS) db[v][i] += g[v][i];
                 g[v][i] *= gm[i];
-                s1 += g[v][i];
+                if constexpr (!RMS) s1 += g[v][i];
                 s2 += g[v][i] * n[v][i];
             }
         }
-        const float c1 = rr.sum(s1) / a.K, c2 = rr.sum(s2) / a.K;
+        const float c1 = RMS ? 0.0f : rr.sum(s1) / a.K, c2 = rr.sum(s2) / a.K;
         const int ds = a.dx_type == TW_T_F32 ? 4 : 2;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
@@ -324,7 +350,8 @@ void norm_bwd_kernel(NormBwdArgs a) {
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                g[v][i] = r * (g[v][i] - c1 - n[v][i] * c2) + (a.dres ? d[i] : 0.0f);
+                g[v][i] = r * ((RMS ? g[v][i] : g[v][i] - c1) - n[v][i] * c2) +
+                          (a.dres ? d[i] : 0.0f);
             store8_as(a.dx_type, a.dx + m * a.K * ds, e, a.K, g[v]);
         }
     }
@@ -337,10 +364,11 @@ void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             store8<TW_T_F32>((char *)mine, 8 * (v * TPR + t), KP, dg[v]);
-            store8<TW_T_F32>((char *)(mine + KP), 8 * (v * TPR + t), KP, db[v]);
+            if constexpr (!RMS)
+                store8<TW_T_F32>((char *)(mine + KP), 8 * (v * TPR + t), KP, db[v]);
         }
         __syncthreads();
-        for (int e = 4 * threadIdx.x; e < 2 * KP; e += 4 * kNormThreads) {
+        for (int e = 4 * threadIdx.x; e < (RMS ? 1 : 2) * KP; e += 4 * kNormThreads) {
             f32x4 s = *reinterpret_cast<const f32x4 *>(share + e);
 #pragma unroll
             for (int w = 1; w < RPB; ++w)
@@ -351,7 +379,8 @@ void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             store8<TW_T_F32>((char *)pg, 8 * (v * TPR + t), KP, dg[v]);
-            store8<TW_T_F32>((char *)(pg + KP), 8 * (v * TPR + t), KP, db[v]);
+            if constexpr (!RMS)
+                store8<TW_T_F32>((char *)(pg + KP), 8 * (v * TPR + t), KP, db[v]);
         }
     }
 }
@@ -382,19 +411,19 @@ __global__ __launch_bounds__(kColsPerBlock *kColThreads) void norm_cols_kernel(
     }
 }
 
-template <int TD, int TX, int TPR, int VPT>
+template <int TD, int TX, int TPR, int VPT, bool RMS>
 hipError_t launch_bwd(const NormBwdArgs &a, int grid, hipStream_t s) {
     constexpr int lds = TPR == kWave ? kNormThreads / TPR * 2 * TPR * VPT * 8 * 4 : 0;
     constexpr int threads = TPR > kNormThreads ? TPR : kNormThreads;
-    norm_bwd_kernel<TD, TX, TPR, VPT><<<grid, threads, a.part ? lds : 0, s>>>(a);
+    norm_bwd_kernel<TD, TX, TPR, VPT, RMS><<<grid, threads, a.part ? lds : 0, s>>>(a);
     return hipGetLastError();
 }
 
-template <int TD, int TX>
+template <int TD, int TX, bool RMS>
 hipError_t launch_bwd(const NormBwdArgs &a, int grid, hipStream_t s) {
     auto go = [&](auto k) {
         constexpr int K = decltype(k)::value;
-        return launch_bwd<TD, TX, norm_bwd_tpr(K), norm_bwd_vpt(K)>(a, grid, s);
+        return launch_bwd<TD, TX, norm_bwd_tpr(K), norm_bwd_vpt(K), RMS>(a, grid, s);
     };
     if (a.K <= 512) return go(std::integral_constant<int, 512>{});
     if (a.K <= 1024) return go(std::integral_constant<int, 1024>{});
@@ -449,27 +478,58 @@ size_t layernorm_bwd_bytes(int M, int K) {
     return (size_t)norm_bwd_groups(M, K) * 2 * norm_bwd_cols(K) * 4;
 }
 
+template <bool RMS>
+static hipError_t launch_norm_bwd(const NormBwdArgs &a, int dy_type, int x_type, float *dgamma,
+                                  float *dbeta, hipStream_t s, hipEvent_t ev_rows) {
+    const int grid = norm_bwd_groups(a.M, a.K);
+    hipError_t e = hipSuccess;
+    if (a.M > 0 || a.part)
+        e = dy_type == TW_T_F32
+                ? (x_type == TW_T_F32 ? launch_bwd<TW_T_F32, TW_T_F32, RMS>(a, grid, s)
+                                      : launch_bwd<TW_T_F32, TW_T_BF16, RMS>(a, grid, s))
+                : (x_type == TW_T_F32 ? launch_bwd<TW_T_BF16, TW_T_F32, RMS>(a, grid, s)
+                                      : launch_bwd<TW_T_BF16, TW_T_BF16, RMS>(a, grid, s));
+    if (e == hipSuccess && ev_rows) e = hipEventRecord(ev_rows, s);
+    if (e != hipSuccess || !a.part) return e;
+    const dim3 blocks((a.K + kColsPerBlock - 1) / kColsPerBlock, RMS ? 1 : 2);
+    norm_cols_kernel<<<blocks, kColsPerBlock * kColThreads, 0, s>>>(
+        a.part, grid, a.K, norm_bwd_cols(a.K), dgamma, dbeta);
+    return hipGetLastError();
+}
+
 hipError_t launch_layernorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
                                 int64_t x_stride, const float *gamma, const float *mean,
                                 const float *rstd, const void *dres, int M, int K, void *dx,
                                 int dx_type, float *dgamma, float *dbeta, float *part,
                                 hipStream_t s, hipEvent_t ev_rows) {
-    const int grid = norm_bwd_groups(M, K);
-    NormBwdArgs a{(const char *)dy, (const char *)x, (const char *)dres, x_stride, gamma, mean,
-                  rstd, M, K, (char *)dx, dx_type, dgamma || dbeta ? part : nullptr};
-    hipError_t e = hipSuccess;
-    if (M > 0 || a.part)
-        e = dy_type == TW_T_F32
-                ? (x_type == TW_T_F32 ? launch_bwd<TW_T_F32, TW_T_F32>(a, grid, s)
-                                      : launch_bwd<TW_T_F32, TW_T_BF16>(a, grid, s))
-                : (x_type == TW_T_F32 ? launch_bwd<TW_T_BF16, TW_T_F32>(a, grid, s)
-                                      : launch_bwd<TW_T_BF16, TW_T_BF16>(a, grid, s));
-    if (e == hipSuccess && ev_rows) e = hipEventRecord(ev_rows, s);
-    if (e != hipSuccess || !a.part) return e;
-    const dim3 blocks((K + kColsPerBlock - 1) / kColsPerBlock, 2);
-    norm_cols_kernel<<<blocks, kColsPerBlock * kColThreads, 0, s>>>(part, grid, K,
-                                                                    norm_bwd_cols(K), dgamma, dbeta);
-    return hipGetLastError();
+    const NormBwdArgs a{(const char *)dy, (const char *)x, (const char *)dres, x_stride, gamma,
+                        mean, rstd, M, K, (char *)dx, dx_type, dgamma || dbeta ? part : nullptr};
+    return launch_norm_bwd<false>(a, dy_type, x_type, dgamma, dbeta, s, ev_rows);
+}
+
+hipError_t launch_rmsnorm(const void *x, int x_type, int64_t x_stride, const void *add,
+                          int add_type, const float *gamma, float eps, int M, int K, void *sum,
+                          void *y, int y_type, float *rstd, hipStream_t s) {
+    NormArgs a{(const char *)x, (const char *)add, x_stride, gamma, nullptr, eps, M, K,
+               (char *)sum, (char *)y, y_type, nullptr, rstd, nullptr, nullptr};
+    return launch_norm<kRms>(a, x_type, add_type, s);
+}
+
+hipError_t launch_rmsnorm_quant(const void *x, int x_type, int64_t x_stride, const void *add,
+                                int add_type, const float *gamma, float eps, int M, int K,
+                                void *sum, int8_t *q, float *scale, hipStream_t s) {
+    NormArgs a{(const char *)x, (const char *)add, x_stride, gamma, nullptr, eps, M, K,
+               (char *)sum, nullptr, 0, nullptr, nullptr, q, scale};
+    return launch_norm<kRmsQuant>(a, x_type, add_type, s);
+}
+
+hipError_t launch_rmsnorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
+                              int64_t x_stride, const float *gamma, const float *rstd,
+                              const void *dres, int M, int K, void *dx, int dx_type, float *dgamma,
+                              float *part, hipStream_t s, hipEvent_t ev_rows) {
+    const NormBwdArgs a{(const char *)dy, (const char *)x, (const char *)dres, x_stride, gamma,
+                        nullptr, rstd, M, K, (char *)dx, dx_type, dgamma ? part : nullptr};
+    return launch_norm_bwd<true>(a, dy_type, x_type, dgamma, nullptr, s, ev_rows);
 }
 
 }  // namespace tw

@@ -1,0 +1,232 @@
+// linear_ce.hip -- softmax cross entropy of an output projection over a large
+// vocabulary, without the logits in memory, and its gradient.
+//
+// With l = x w^T (one row a token, V columns) and a row's target t:
+//   lse = log sum_v exp(l_v),  loss = lse - l_t,
+//   D_v = dloss (exp(l_v - lse) - [v = t]),  dx = D w,  dw = D^T x.
+// Forward: the product's tiles stay in registers; each leaves, for every row
+// of it, the largest logit and the sum of the exponentials below it, and a
+// second kernel joins a row's column blocks and takes the target's logit as
+// one more dot product.  Backward: the logits are computed again, a piece of the
+// vocabulary at a time; a piece's D (bf16: it feeds the matrix cores) is the
+// operand of both products.
+//
+// A row whose target is outside [0, V) is left out: its loss and its row of D
+// are 0.
+#include "tw_tiles.hpp"
+#include "tw_train.hpp"
+
+namespace tw {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// A row's target if it lies in [first, first + count), relative to first, else -1.
+__device__ __forceinline__ int target_of(Targets t, int m, int64_t first, int64_t count) {
+    const int64_t v = (t.wide ? static_cast<const int64_t *>(t.p)[m]
+                              : (int64_t) static_cast<const int32_t *>(t.p)[m]);
+    // (v - first may overflow for a target far outside)
+    return v >= first && v < first + count ? (int)(v - first) : -1;
+}
+
+// Largest logit and sum of exponentials of a set of columns, in units of
+// log 2: the sum is of 2^(l log2e - top).  The rounding of `top` does not
+// matter, as the same number is added back.
+struct Soft {
+    float top, sum;
+};
+__device__ __forceinline__ Soft join_soft(Soft a, Soft b) {
+    const float top = fmaxf(a.top, b.top);
+    const float at = top == -INFINITY ? 0.0f : top;  // nothing yet: sums stay 0
+    return {top, a.sum * __builtin_amdgcn_exp2f(a.top - at) +
+                     b.sum * __builtin_amdgcn_exp2f(b.top - at)};
+}
+
+struct EpiSoft {
+    static constexpr bool kStats = true;
+    Soft *part;  // [column blocks][M]
+    int M, N;
+    struct Row {
+        float most, top, sum;
+    };
+    __device__ Row row(int) const { return {-INFINITY, 0.0f, 0.0f}; }
+    __device__ __forceinline__ void most(Row &r, int n, f32x4 v) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < N) r.most = fmaxf(r.most, v[e]);
+    }
+    __device__ __forceinline__ void add(Row &r, int n, f32x4 v) const {
+        r.top = r.most == -INFINITY ? 0.0f : r.most * kLog2e;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < N) r.sum += __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
+    }
+    template <int L>
+    __device__ __forceinline__ void join(Row &r) const {
+        const Soft a{r.most == -INFINITY ? -INFINITY : r.top, r.sum};
+        const Soft b{__shfl_xor(a.top, L), __shfl_xor(a.sum, L)};
+        const Soft j = join_soft(a, b);
+        r.most = r.top = j.top;
+        r.sum = j.sum;
+    }
+    __device__ __forceinline__ void put(const Row &r, char *lds, int w, int i) const {
+        reinterpret_cast<Soft *>(lds)[w * 256 + i] = {r.top, r.sum};
+    }
+    template <int W>
+    __device__ __forceinline__ void finish(const char *lds, int i, int m, int cb) const {
+        const Soft *s = reinterpret_cast<const Soft *>(lds) + i;
+        Soft j = s[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) j = join_soft(j, s[w * 256]);
+        part[(int64_t)cb * M + m] = j;
+    }
+};
+
+// Joins the column blocks of a row and takes the target's logit: 16 threads a
+// row.
+__global__ __launch_bounds__(256) void ce_rows_kernel(const Soft *__restrict__ part, int blocks,
+                                                      const uint16_t *__restrict__ x,
+                                                      int64_t x_stride,
+                                                      const uint16_t *__restrict__ w, Targets t,
+                                                      int M, int K, int V,
+                                                      float *__restrict__ loss,
+                                                      float *__restrict__ lse) {
+    const int r = threadIdx.x & 15, i = threadIdx.x >> 4;  // row and thread of it
+    const int m = blockIdx.x * 16 + r;
+    const bool in = m < M;
+    Soft s{-INFINITY, 0.0f};
+    if (in)
+        for (int b = i; b < blocks; b += 16) s = join_soft(s, part[(int64_t)b * M + m]);
+    __shared__ Soft all[16][17];
+    __shared__ float dots[16];
+    all[i][r] = s;
+    // the dot products have 16 neighbouring threads a row
+    const int dr = threadIdx.x >> 4, di = threadIdx.x & 15;
+    const int dm = blockIdx.x * 16 + dr;
+    const int tgt = dm < M ? target_of(t, dm, 0, V) : -1;
+    float d = 0.0f;
+    if (tgt >= 0) {
+        const uint16_t *xr = x + dm * x_stride, *wr = w + (int64_t)tgt * K;
+        for (int k = 8 * di; k < K; k += 128) {
+            const u32x4 a = ld16(xr + k), b = ld16(wr + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                d += bf_lo(a[e]) * bf_lo(b[e]) + bf_hi(a[e]) * bf_hi(b[e]);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) d += __shfl_xor(d, o);
+    if (di == 0) dots[dr] = d;
+    __syncthreads();
+    if (threadIdx.x >= 16 || !in) return;
+    s = all[0][r];
+    for (int j = 1; j < 16; ++j) s = join_soft(s, all[j][r]);
+    const float l = kLn2 * (s.top + __builtin_amdgcn_logf(s.sum));
+    lse[m] = l;
+    // a loss is never negative; the two sums may cross by a rounding
+    const float v = l - dots[r];
+    loss[m] = target_of(t, m, 0, V) < 0 ? 0.0f : v < 0.0f ? 0.0f : v;
+}
+
+// D of a piece of the vocabulary, columns first .. first + N - 1 of V.
+struct EpiD {
+    static constexpr bool kStats = false;
+    const float *lse, *dloss;
+    Targets t;
+    uint16_t *d;
+    int64_t ldd;  // N rounded up to 8; the columns past N are written as zeros
+    int M, N, first, V;
+    struct Row {
+        float top, scale;
+        int t;
+        bool live;
+    };
+    __device__ __forceinline__ Row row(int m) const {
+        return {lse[m] * kLog2e, dloss[m], target_of(t, m, first, N), target_of(t, m, 0, V) >= 0};
+    }
+    __device__ __forceinline__ void quad(int, int, Row &r, int m, int n, f32x4 v, f32x4) const {
+        if (n >= ldd) return;
+        f32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float p = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
+            if (n + e == r.t) p -= 1.0f;
+            o[e] = r.live && n + e < N ? p * r.scale : 0.0f;
+        }
+        store4(d, TW_T_BF16, m * ldd + n, o);
+    }
+};
+
+constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// The backward pass's pieces of the vocabulary: columns of D in at most 256 MB.
+struct Pieces {
+    int width;
+    size_t d_bytes, part_bytes;
+    int splits;
+};
+Pieces pieces_of(int M, int K, int V) {
+    Pieces p;
+    const int64_t most = (int64_t)(256 << 20) / 2 / (M > 0 ? M : 1) / 256 * 256;
+    p.width = (int)(most < 256 ? 256 : most < V ? most : V);
+    p.d_bytes = up256((size_t)M * ((p.width + 7) / 8 * 8) * 2);
+    p.splits = 1;
+    p.part_bytes = p.width < V ? up256((size_t)M * K * 4) : 0;
+    return p;
+}
+
+}  // namespace
+
+size_t ce_fwd_bytes(int M, int, int V) {
+    return up256((size_t)M * (((size_t)V + kRingBN - 1) / kRingBN) * sizeof(Soft));
+}
+
+hipError_t launch_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w, Targets t, int M,
+                         int K, int V, float *loss, float *lse, void *ws, hipStream_t s) {
+    if (M == 0) return hipSuccess;
+    const TileArgs p{{x}, {w}, x_stride, K, M, V, K, 1};
+    Soft *part = static_cast<Soft *>(ws);
+    hipError_t e = launch_ring<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, 1, s);
+    if (e != hipSuccess) return e;
+    ce_rows_kernel<<<(M + 15) / 16, 256, 0, s>>>(part, (V + kRingBN - 1) / kRingBN, x, x_stride, w,
+                                                 t, M, K, V, loss, lse);
+    return hipGetLastError();
+}
+
+size_t ce_bwd_bytes(int M, int K, int V) {
+    const Pieces p = pieces_of(M, K, V);
+    return p.d_bytes + p.part_bytes;
+}
+
+hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride,
+                         const uint16_t *w, Targets t, const float *lse, int M, int K, int V,
+                         void *dx, int dx_type, void *dw, int dw_type, void *ws, hipStream_t s) {
+    const Pieces pc = pieces_of(M, K, V);
+    uint16_t *d = static_cast<uint16_t *>(ws);
+    float *part = pc.part_bytes ? reinterpret_cast<float *>((char *)ws + pc.d_bytes) : nullptr;
+    hipError_t e = hipSuccess;
+    for (int first = 0; first < V && e == hipSuccess; first += pc.width) {
+        const int N = V - first < pc.width ? V - first : pc.width;
+        const int64_t ldd = (N + 7) / 8 * 8;
+        const uint16_t *wp = w + (int64_t)first * K;
+        if (M > 0)
+            e = launch_ring<kRows, kRows, 1, 1>(
+                TileArgs{{x}, {wp}, x_stride, K, M, N, K, 1},
+                EpiD{lse, dloss, t, d, ldd, M, N, first, V}, 1, s);
+        if (e == hipSuccess && dx)
+            e = launch_ring<kRows, kCols, 1, 1>(
+                TileArgs{{d}, {wp}, ldd, K, M, K, N, 1},
+                EpiStore{{dx}, dx_type, part, first > 0, M, K}, 1, s);
+        if (e == hipSuccess && dw) {
+            char *out = static_cast<char *>(dw) + (int64_t)first * K * (dw_type == TW_T_F32 ? 4 : 2);
+            e = launch_ring<kCols, kCols, 1, 1>(
+                TileArgs{{d}, {x}, ldd, x_stride, N, K, M, 1},
+                EpiStore{{out}, dw_type, nullptr, 0, N, K}, 1, s);
+        }
+    }
+    if (e == hipSuccess && dx && part) e = launch_sum_parts(part, 1, (int64_t)M * K, dx, dx_type, s);
+    return e;
+}
+
+}  // namespace tw

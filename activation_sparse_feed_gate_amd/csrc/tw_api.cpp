@@ -4,12 +4,16 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "tw_internal.hpp"
 #include "tw_norm_quant.hpp"
+#include "tw_train.hpp"
 
 namespace {
 
@@ -932,6 +936,398 @@ tw_status tw_quant_gateup(const void *x, int x_type, int64_t x_stride, const flo
                     "int8 product launch"));
     TW_TRY(record(events, 2, s));
     return TW_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- the dense training step -------------------------------------------------
+
+// Rows of bf16 that the tile kernels read in 16-byte pieces.
+constexpr int kTileMost = 1 << 20;  // elements of a row, and between rows
+tw_status check_tile_rows(int K, int64_t x_stride) {
+    if (x_stride < K)
+        return fail(TW_EINVAL, "x_stride=%lld is below K=%d", (long long)x_stride, K);
+    if (x_stride % 8 || x_stride > kTileMost)
+        return fail(TW_EUNSUPPORTED, "x_stride=%lld: must be a multiple of 8, at most 2^20",
+                    (long long)x_stride);
+    return TW_OK;
+}
+tw_status check_tile_sizes(int M, int K) {
+    if (M < 0 || K <= 0) return fail(TW_EINVAL, "M=%d K=%d: need M >= 0, K > 0", M, K);
+    if (K % 8 || K > kTileMost)
+        return fail(TW_EUNSUPPORTED, "K=%d: must be a multiple of 8, at most 2^20", K);
+    if (M > (1 << 24)) return fail(TW_EUNSUPPORTED, "M=%d: at most 2^24", M);
+    return TW_OK;
+}
+// Output tiles of 128 x 128 that one launch can number.
+tw_status check_tile_grid(int64_t a, int64_t b) {
+    if ((a + 127) / 128 * ((b + 127) / 128) >= (int64_t(1) << 31))
+        return fail(TW_EUNSUPPORTED, "%lld x %lld outputs: at most 2^45", (long long)a,
+                    (long long)b);
+    return TW_OK;
+}
+
+tw_status check_gated(int M, int K, int N) {
+    TW_TRY(check_tile_sizes(M, K));
+    if (N <= 0) return fail(TW_EINVAL, "N=%d: need N > 0", N);
+    if (N % 8 || N > kTileMost)
+        return fail(TW_EUNSUPPORTED, "N=%d: must be a multiple of 8, at most 2^20", N);
+    TW_TRY(check_tile_grid(M, N));
+    TW_TRY(check_tile_grid(M, K));
+    return check_tile_grid(N, K);
+}
+
+tw_status check_ce(int M, int K, int V) {
+    TW_TRY(check_tile_sizes(M, K));
+    if (V <= 0) return fail(TW_EINVAL, "V=%d: need V > 0", V);
+    if (V > (1 << 24)) return fail(TW_EUNSUPPORTED, "V=%d: at most 2^24", V);
+    TW_TRY(check_tile_grid(M, V));
+    TW_TRY(check_tile_grid(M, K));
+    return check_tile_grid(V, K);
+}
+
+tw_status check_act(int act) {
+    if (act < TW_RELU || act > TW_GELU)
+        return fail(TW_EINVAL, "act=%d: TW_RELU, TW_SILU or TW_GELU", act);
+    return TW_OK;
+}
+
+tw_status check_target(const void *target, int target_type, int M) {
+    if (target_type != TW_INT32 && target_type != TW_INT64)
+        return fail(TW_EINVAL, "target_type=%d: TW_INT32 or TW_INT64", target_type);
+    TW_NEED_M(target);
+    return TW_OK;
+}
+
+tw_status check_ws(const void *ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return TW_OK;
+    TW_NEED(ws);
+    if (ws_bytes < need) return fail(TW_EINVAL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+    return TW_OK;
+}
+
+// Runs a shape check without leaving its message behind (the workspace
+// queries return 0 and no error).
+template <typename F>
+bool shape_ok(F check) {
+    char saved[sizeof g_err];
+    std::snprintf(saved, sizeof saved, "%s", g_err);
+    const tw_status st = check();
+    std::snprintf(g_err, sizeof g_err, "%s", saved);
+    return st == TW_OK;
+}
+
+size_t act_bytes(int M, int N) { return round_up((size_t)M * N * 2, 256); }
+
+// The buffers of a clipping call: types, addresses, sizes.
+constexpr int kMostBuffers = 1 << 20;
+tw_status check_buffers(int count, const void *const *g, const int64_t *n, const int *types,
+                        const char *what) {
+    for (int i = 0; i < count; ++i) {
+        if (!float_type(types[i]))
+            return fail(TW_EINVAL, "%s[%d]: type %d, TW_BF16 or TW_F32", what, i, types[i]);
+        if (n[i] < 0) return fail(TW_EINVAL, "n[%d]=%lld: need n >= 0", i, (long long)n[i]);
+        if (n[i] > (int64_t(1) << 34))
+            return fail(TW_EUNSUPPORTED, "n[%d]=%lld: at most 2^34", i, (long long)n[i]);
+        if (n[i] == 0) continue;
+        if (!g[i]) return fail(TW_EINVAL, "%s[%d] is NULL", what, i);
+        if (reinterpret_cast<uintptr_t>(g[i]) % (types[i] == TW_F32 ? 4 : 2))
+            return fail(TW_EINVAL, "%s[%d] is not aligned to its type", what, i);
+    }
+    return TW_OK;
+}
+
+tw_status check_grad_norm(int count, const void *const *g, const int64_t *n, const int *g_type,
+                          const float *norm, const void *ws, size_t ws_bytes) {
+    if (count < 0) return fail(TW_EINVAL, "count=%d: need count >= 0", count);
+    if (count > kMostBuffers) return fail(TW_EUNSUPPORTED, "count=%d: at most 2^20", count);
+    if (count && (!g || !n || !g_type)) return fail(TW_EINVAL, "g, n or g_type is NULL");
+    TW_TRY(check_buffers(count, g, n, g_type, "g"));
+    if (!norm) return fail(TW_EINVAL, "norm is NULL");
+    if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(TW_EINVAL, "norm is not aligned to 4");
+    return check_ws(ws, ws_bytes, tw_grad_norm_workspace_bytes(count, n));
+}
+
+// No output may overlap another output, or a gradient other than its own in
+// place.
+tw_status check_overlaps(int count, const void *const *g, const int64_t *n, const int *g_type,
+                         void *const *out, const int *out_type) {
+    struct Span {
+        uintptr_t begin, end;
+        int i;
+    };
+    std::vector<Span> spans;
+    spans.reserve(count);
+    auto bytes = [](int type, int64_t k) { return (uintptr_t)k * (type == TW_F32 ? 4 : 2); };
+    for (int i = 0; i < count; ++i) {
+        if (!n[i]) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
+        spans.push_back({at, at + bytes(out_type[i], n[i]), i});
+    }
+    std::sort(spans.begin(), spans.end(),
+              [](const Span &a, const Span &b) { return a.begin < b.begin; });
+    for (size_t k = 1; k < spans.size(); ++k)
+        if (spans[k].begin < spans[k - 1].end)
+            return fail(TW_EINVAL, "out[%d] and out[%d] overlap", spans[k - 1].i, spans[k].i);
+    for (int i = 0; i < count; ++i) {
+        if (!n[i]) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(g[i]);
+        const uintptr_t end = at + bytes(g_type[i], n[i]);
+        // the first output that ends after g[i] begins (they are disjoint, so
+        // their ends ascend too)
+        auto k = std::upper_bound(spans.begin(), spans.end(), at,
+                                  [](uintptr_t v, const Span &b) { return v < b.end; });
+        for (; k != spans.end() && k->begin < end; ++k)
+            if (k->i != i || g[i] != out[i] || g_type[i] != out_type[i])
+                return fail(TW_EINVAL, "g[%d] and out[%d] overlap", i, k->i);
+    }
+    return TW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tw_status tw_rmsnorm_fwd(const void *x, int x_type, int64_t x_stride, const void *add,
+                         int add_type, const float *gamma, float eps, int M, int K, void *sum,
+                         void *y, int y_type, float *rstd, void *stream, void *const *events) {
+    TW_TRY(check_norm(x, x_type, x_stride, add, add_type, gamma, nullptr, eps, M, K, sum));
+    if (!float_type(y_type)) return fail(TW_EINVAL, "y_type=%d: TW_BF16 or TW_F32", y_type);
+    TW_NEED_M(y);
+    if (rstd) TW_NEED(rstd);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_rmsnorm(x, x_type, x_stride, add, add_type, gamma, eps, M, K, sum,
+                                       y, y_type, rstd, s),
+                    "RMS norm launch"));
+    TW_TRY(record(events, 1, s));
+    return TW_OK;
+}
+
+tw_status tw_rmsnorm_quant(const void *x, int x_type, int64_t x_stride, const void *add,
+                           int add_type, const float *gamma, float eps, int M, int K, void *sum,
+                           int8_t *q, float *scale, void *stream, void *const *events) {
+    TW_TRY(check_norm(x, x_type, x_stride, add, add_type, gamma, nullptr, eps, M, K, sum));
+    TW_NEED_M(q);
+    TW_NEED_M(scale);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_rmsnorm_quant(x, x_type, x_stride, add, add_type, gamma, eps, M, K,
+                                             sum, q, scale, s),
+                    "RMS norm launch"));
+    TW_TRY(record(events, 1, s));
+    return TW_OK;
+}
+
+size_t tw_rmsnorm_bwd_workspace_bytes(int M, int K) {
+    return tw_layernorm_bwd_workspace_bytes(M, K);
+}
+
+tw_status tw_rmsnorm_bwd(const void *dy, int dy_type, const void *x, int x_type, int64_t x_stride,
+                         const float *gamma, const float *rstd, const void *dres, int M, int K,
+                         void *dx, int dx_type, float *dgamma, void *ws, size_t ws_bytes,
+                         void *stream, void *const *events) {
+    TW_TRY(check_rows(M, K, tw::kNormMaxK, x_type, x_stride));
+    if (!float_type(dy_type)) return fail(TW_EINVAL, "dy_type=%d: TW_BF16 or TW_F32", dy_type);
+    if (!float_type(dx_type)) return fail(TW_EINVAL, "dx_type=%d: TW_BF16 or TW_F32", dx_type);
+    TW_NEED_M(dy);
+    TW_NEED_M(x);
+    TW_NEED(gamma);
+    TW_NEED_M(rstd);
+    TW_NEED_M(dx);
+    if (dres) TW_NEED(dres);
+    if (dgamma) {
+        TW_NEED(dgamma);
+        TW_TRY(check_ws(ws, ws_bytes, tw_rmsnorm_bwd_workspace_bytes(M, K)));
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_rmsnorm_bwd(dy, dy_type, x, x_type, x_stride, gamma, rstd, dres, M,
+                                           K, dx, dx_type, dgamma, static_cast<float *>(ws), s,
+                                           events ? static_cast<hipEvent_t>(events[1]) : nullptr),
+                    "RMS norm gradient launch"));
+    TW_TRY(record(events, 2, s));
+    return TW_OK;
+}
+
+size_t tw_gated_ffn_workspace_bytes(int M, int K, int N) {
+    if (!shape_ok([&] { return check_gated(M, K, N); })) return 0;
+    return act_bytes(M, N) + round_up(tw::ffn_fwd_part_bytes(M, K, N), 256) + 256;
+}
+
+tw_status tw_gated_ffn_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
+                           const uint16_t *wu_t, const uint16_t *wd, int act, int M, int K, int N,
+                           uint16_t *g, uint16_t *u, void *y, int y_type, void *ws,
+                           size_t ws_bytes, void *stream, void *const *events) {
+    TW_TRY(check_gated(M, K, N));
+    TW_TRY(check_tile_rows(K, x_stride));
+    TW_TRY(check_act(act));
+    if (!float_type(y_type)) return fail(TW_EINVAL, "y_type=%d: TW_BF16 or TW_F32", y_type);
+    TW_NEED_M(x);
+    TW_NEED(wg_t);
+    TW_NEED(wu_t);
+    TW_NEED(wd);
+    TW_NEED_M(y);
+    if (g) TW_NEED(g);
+    if (u) TW_NEED(u);
+    if (M > 0) TW_TRY(check_ws(ws, ws_bytes, tw_gated_ffn_workspace_bytes(M, K, N)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    if (M == 0) {
+        TW_TRY(record(events, 1, s));
+        return record(events, 2, s);
+    }
+    uint16_t *h = static_cast<uint16_t *>(ws);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + act_bytes(M, N));
+    TW_TRY(launched(tw::launch_ffn_up(x, x_stride, wg_t, wu_t, act, M, K, N, g, u, h, part, s),
+                    "gate and up launch"));
+    TW_TRY(record(events, 1, s));
+    TW_TRY(launched(tw::launch_ffn_down(h, wd, M, K, N, y, y_type, part, s), "down launch"));
+    return record(events, 2, s);
+}
+
+size_t tw_gated_ffn_bwd_workspace_bytes(int M, int K, int N) {
+    if (!shape_ok([&] { return check_gated(M, K, N); })) return 0;
+    return 3 * act_bytes(M, N) + round_up(tw::ffn_bwd_part_bytes(M, K, N), 256) + 256;
+}
+
+tw_status tw_gated_ffn_bwd(const uint16_t *dy, const uint16_t *x, int64_t x_stride,
+                           const uint16_t *wg_t, const uint16_t *wu_t, const uint16_t *wd, int act,
+                           const uint16_t *g, const uint16_t *u, int M, int K, int N, void *dx,
+                           int dx_type, void *dwg_t, void *dwu_t, void *dwd, int dw_type, void *ws,
+                           size_t ws_bytes, void *stream, void *const *events) {
+    TW_TRY(check_gated(M, K, N));
+    TW_TRY(check_tile_rows(K, x_stride));
+    TW_TRY(check_act(act));
+    if (!float_type(dx_type)) return fail(TW_EINVAL, "dx_type=%d: TW_BF16 or TW_F32", dx_type);
+    if (!float_type(dw_type)) return fail(TW_EINVAL, "dw_type=%d: TW_BF16 or TW_F32", dw_type);
+    TW_NEED_M(dy);
+    TW_NEED_M(x);
+    TW_NEED(wg_t);
+    TW_NEED(wu_t);
+    TW_NEED(wd);
+    TW_NEED_M(g);
+    TW_NEED_M(u);
+    if (dx) TW_NEED(dx);
+    if (!dwg_t != !dwu_t || !dwg_t != !dwd)
+        return fail(TW_EINVAL, "dwg_t, dwu_t and dwd must all be given or all be NULL");
+    if (dwg_t) {
+        TW_NEED(dwg_t);
+        TW_NEED(dwu_t);
+        TW_NEED(dwd);
+    }
+    TW_TRY(check_ws(ws, ws_bytes, tw_gated_ffn_bwd_workspace_bytes(M, K, N)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    uint16_t *dz = static_cast<uint16_t *>(ws);
+    uint16_t *du = dz + act_bytes(M, N) / 2, *h = du + act_bytes(M, N) / 2;
+    float *part = reinterpret_cast<float *>(h + act_bytes(M, N) / 2);
+    TW_TRY(record(events, 0, s));
+    if (M > 0)
+        TW_TRY(launched(tw::launch_ffn_dh(dy, wd, act, g, u, M, K, N, dz, du, h, s), "dh launch"));
+    TW_TRY(record(events, 1, s));
+    if (M > 0 && dx)
+        TW_TRY(launched(tw::launch_ffn_dx(dz, du, wg_t, wu_t, M, K, N, dx, dx_type, part, s),
+                        "dx launch"));
+    TW_TRY(record(events, 2, s));
+    if (dwg_t)
+        TW_TRY(launched(tw::launch_ffn_dw(dz, du, h, x, x_stride, dy, M, K, N, dwg_t, dwu_t, dwd,
+                                          dw_type, part, s),
+                        "weight-gradient launch"));
+    return record(events, 3, s);
+}
+
+size_t tw_linear_ce_workspace_bytes(int M, int K, int V) {
+    if (!shape_ok([&] { return check_ce(M, K, V); })) return 0;
+    return tw::ce_fwd_bytes(M, K, V) + 256;
+}
+
+tw_status tw_linear_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w,
+                           const void *target, int target_type, int M, int K, int V, float *loss,
+                           float *lse, void *ws, size_t ws_bytes, void *stream,
+                           void *const *events) {
+    TW_TRY(check_ce(M, K, V));
+    TW_TRY(check_tile_rows(K, x_stride));
+    TW_TRY(check_target(target, target_type, M));
+    TW_NEED_M(x);
+    TW_NEED(w);
+    TW_NEED_M(loss);
+    TW_NEED_M(lse);
+    if (M > 0) TW_TRY(check_ws(ws, ws_bytes, tw_linear_ce_workspace_bytes(M, K, V)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_ce_fwd(x, x_stride, w, {target, target_type == TW_INT64}, M, K, V,
+                                      loss, lse, ws, s),
+                    "cross entropy launch"));
+    return record(events, 1, s);
+}
+
+size_t tw_linear_ce_bwd_workspace_bytes(int M, int K, int V) {
+    if (!shape_ok([&] { return check_ce(M, K, V); })) return 0;
+    return tw::ce_bwd_bytes(M, K, V) + 256;
+}
+
+tw_status tw_linear_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride,
+                           const uint16_t *w, const void *target, int target_type,
+                           const float *lse, int M, int K, int V, void *dx, int dx_type, void *dw,
+                           int dw_type, void *ws, size_t ws_bytes, void *stream,
+                           void *const *events) {
+    TW_TRY(check_ce(M, K, V));
+    TW_TRY(check_tile_rows(K, x_stride));
+    TW_TRY(check_target(target, target_type, M));
+    if (!float_type(dx_type)) return fail(TW_EINVAL, "dx_type=%d: TW_BF16 or TW_F32", dx_type);
+    if (!float_type(dw_type)) return fail(TW_EINVAL, "dw_type=%d: TW_BF16 or TW_F32", dw_type);
+    TW_NEED_M(dloss);
+    TW_NEED_M(x);
+    TW_NEED(w);
+    TW_NEED_M(lse);
+    if (dx) TW_NEED(dx);
+    if (dw) TW_NEED(dw);
+    TW_TRY(check_ws(ws, ws_bytes, tw_linear_ce_bwd_workspace_bytes(M, K, V)));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_ce_bwd(dloss, x, x_stride, w, {target, target_type == TW_INT64},
+                                      lse, M, K, V, dx, dx_type, dw, dw_type, ws, s),
+                    "cross entropy gradient launch"));
+    return record(events, 1, s);
+}
+
+size_t tw_grad_norm_workspace_bytes(int count, const int64_t *n) {
+    if (count < 0 || count > kMostBuffers || (count && !n)) return 0;
+    return tw::grad_norm_bytes(count, n);
+}
+
+tw_status tw_grad_norm(int count, const void *const *g, const int64_t *n, const int *g_type,
+                       float *norm, void *ws, size_t ws_bytes, void *stream, void *const *events) {
+    TW_TRY(check_grad_norm(count, g, n, g_type, norm, ws, ws_bytes));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_grad_norm(count, g, n, g_type, norm, static_cast<float *>(ws), s),
+                    "gradient norm launch"));
+    return record(events, 1, s);
+}
+
+tw_status tw_grad_clip(int count, const void *const *g, const int64_t *n, const int *g_type,
+                       void *const *out, const int *out_type, float max_norm, float eps,
+                       float *norm, void *ws, size_t ws_bytes, void *stream, void *const *events) {
+    TW_TRY(check_grad_norm(count, g, n, g_type, norm, ws, ws_bytes));
+    if (!(max_norm >= 0.0f)) return fail(TW_EINVAL, "max_norm=%g: need max_norm >= 0", (double)max_norm);
+    if (!(eps >= 0.0f)) return fail(TW_EINVAL, "eps=%g: need eps >= 0", (double)eps);
+    if (count && (!out || !out_type)) return fail(TW_EINVAL, "out or out_type is NULL");
+    TW_TRY(check_buffers(count, out, n, out_type, "out"));
+    try {
+        TW_TRY(check_overlaps(count, g, n, g_type, out, out_type));
+    } catch (const std::bad_alloc &) {
+        return fail(TW_EINVAL, "out of host memory for %d buffers", count);
+    }
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    TW_TRY(record(events, 0, s));
+    TW_TRY(launched(tw::launch_grad_clip(count, g, n, g_type, out, out_type, max_norm, eps, norm,
+                                         static_cast<float *>(ws), s,
+                                         events ? static_cast<hipEvent_t>(events[1]) : nullptr),
+                    "gradient clipping launch"));
+    return record(events, 2, s);
 }
 
 }  // extern "C"

@@ -21,9 +21,18 @@ block's dense projections on 8-bit integers are ``tw_quant_rows``,
 ``tw_layernorm_quant``, ``tw_quant_linear`` and ``tw_quant_gateup``
 (allocating: ``quantize_rows``, ``layernorm_quantize``, ``quant_linear``,
 ``quant_gateup``).
+
+The dense training step is the RMS norm (``tw_rmsnorm_fwd``, ``tw_rmsnorm_quant``,
+``tw_rmsnorm_bwd``; allocating: ``rmsnorm``, ``rmsnorm_quantize``,
+``rmsnorm_backward``), the gated FFN (``tw_gated_ffn_fwd``, ``tw_gated_ffn_bwd``;
+``gated_ffn``, ``gated_ffn_backward``), the cross entropy of the output projection
+(``tw_linear_ce_fwd``, ``tw_linear_ce_bwd``; ``linear_ce``, ``linear_ce_backward``)
+and gradient clipping (``tw_grad_norm``, ``tw_grad_clip``; ``grad_norm``,
+``clip_grads``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import warnings
@@ -133,8 +142,46 @@ _lib.tw_quant_gateup.restype = _i
 _lib.tw_quant_gateup.argtypes = [_vp, _i, _i64, _vp, _vp, _vp, _f, _vp, _vp, _vp, _vp, _i, _i, _i,
                                  _vp, _i, _vp, _sz, _vp, _vp]
 
+_lib.tw_rmsnorm_fwd.restype = _i
+_lib.tw_rmsnorm_fwd.argtypes = [_vp, _i, _i64, _vp, _i, _vp, _f, _i, _i, _vp, _vp, _i, _vp, _vp,
+                                _vp]
+_lib.tw_rmsnorm_quant.restype = _i
+_lib.tw_rmsnorm_quant.argtypes = [_vp, _i, _i64, _vp, _i, _vp, _f, _i, _i, _vp, _vp, _vp, _vp, _vp]
+_lib.tw_rmsnorm_bwd_workspace_bytes.restype = _sz
+_lib.tw_rmsnorm_bwd_workspace_bytes.argtypes = [_i, _i]
+_lib.tw_rmsnorm_bwd.restype = _i
+_lib.tw_rmsnorm_bwd.argtypes = [_vp, _i, _vp, _i, _i64, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp,
+                                _sz, _vp, _vp]
+_lib.tw_gated_ffn_workspace_bytes.restype = _sz
+_lib.tw_gated_ffn_workspace_bytes.argtypes = [_i] * 3
+_lib.tw_gated_ffn_fwd.restype = _i
+_lib.tw_gated_ffn_fwd.argtypes = [_vp, _i64, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _vp,
+                                  _sz, _vp, _vp]
+_lib.tw_gated_ffn_bwd_workspace_bytes.restype = _sz
+_lib.tw_gated_ffn_bwd_workspace_bytes.argtypes = [_i] * 3
+_lib.tw_gated_ffn_bwd.restype = _i
+_lib.tw_gated_ffn_bwd.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _i,
+                                  _vp, _vp, _vp, _i, _vp, _sz, _vp, _vp]
+_lib.tw_linear_ce_workspace_bytes.restype = _sz
+_lib.tw_linear_ce_workspace_bytes.argtypes = [_i] * 3
+_lib.tw_linear_ce_fwd.restype = _i
+_lib.tw_linear_ce_fwd.argtypes = [_vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp, _vp]
+_lib.tw_linear_ce_bwd_workspace_bytes.restype = _sz
+_lib.tw_linear_ce_bwd_workspace_bytes.argtypes = [_i] * 3
+_lib.tw_linear_ce_bwd.restype = _i
+_lib.tw_linear_ce_bwd.argtypes = [_vp, _vp, _i64, _vp, _vp, _i, _vp, _i, _i, _i, _vp, _i, _vp, _i,
+                                  _vp, _sz, _vp, _vp]
+_lib.tw_grad_norm_workspace_bytes.restype = _sz
+_lib.tw_grad_norm_workspace_bytes.argtypes = [_i, _vp]
+_lib.tw_grad_norm.restype = _i
+_lib.tw_grad_norm.argtypes = [_i, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]
+_lib.tw_grad_clip.restype = _i
+_lib.tw_grad_clip.argtypes = [_i, _vp, _vp, _vp, _vp, _vp, _f, _f, _vp, _vp, _sz, _vp, _vp]
+
 TW_OK, TW_EINVAL, TW_EUNSUPPORTED, TW_EHIP = 0, 1, 2, 3
-TW_BF16, TW_F32, TW_INT8 = 0, 1, 2
+TW_BF16, TW_F32, TW_INT8, TW_INT32, TW_INT64 = 0, 1, 2, 3, 4
+TW_RELU, TW_SILU, TW_GELU = 0, 1, 2
+_ACT = {"relu": TW_RELU, "silu": TW_SILU, "gelu": TW_GELU}
 
 
 class TwError(RuntimeError):
@@ -168,7 +215,8 @@ def _rows_ptr(t):
 
 _F32, _I32, _BF16, _U8T = torch.float32, torch.int32, torch.bfloat16, torch.uint8
 _I8 = torch.int8
-_TYPE = {_BF16: TW_BF16, _F32: TW_F32, _I8: TW_INT8}
+_I64 = torch.int64
+_TYPE = {_BF16: TW_BF16, _F32: TW_F32, _I8: TW_INT8, _I32: TW_INT32, _I64: TW_INT64}
 _FLOATS = (_BF16, _F32)
 
 
@@ -275,6 +323,14 @@ def _tiles(N, T, where):
 def _stream(stream):
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _on(t):
+    """The device of a call's tensors made the current one, for the stream and
+    the launches of the call."""
+    if not t.is_cuda or t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
 
 
 def _events(events):
@@ -718,6 +774,229 @@ def tw_quant_gateup(x, wg, g_scale, wu, u_scale, h, gamma=None, beta=None, eps=1
     _check(st, "tw_quant_gateup")
 
 
+# ------------------------------------------------- dense training step --
+def _act(act, where):
+    if act not in _ACT:
+        raise ValueError(f"{where}: act must be one of {sorted(_ACT)}, got {act!r}")
+    return _ACT[act]
+
+
+def tw_rmsnorm_fwd(x, gamma, eps, y, add=None, total=None, rstd=None, stream=None,
+                   events=None) -> None:
+    """y = RMS norm of x (+ add); ``total`` receives x + add in x's type,
+    ``rstd`` what the backward reads."""
+    M, K = _dims2(x, "x", "tw_rmsnorm_fwd")
+    a = _Args("tw_rmsnorm_fwd", x)
+    kind, stride, add_kind = _norm_args(a, x, add, gamma, None, total)
+    y_kind = a.typed(y, "y", _FLOATS, (M, K))
+    a.opt(rstd, "rstd", _F32, (M,))
+    ev = _events(events)
+    with _on(x):
+        st = _lib.tw_rmsnorm_fwd(_rows_ptr(x), kind, stride, _ptr(add), add_kind, _ptr(gamma), eps,
+                                 M, K, _ptr(total), _ptr(y), y_kind, _ptr(rstd), _stream(stream),
+                                 ev[0] if ev else None)
+    _check(st, "tw_rmsnorm_fwd")
+
+
+def tw_rmsnorm_quant(x, gamma, eps, q, scale, add=None, total=None, stream=None,
+                     events=None) -> None:
+    """The RMS norm of x (+ add) in int8 with one scale per row."""
+    M, K = _dims2(x, "x", "tw_rmsnorm_quant")
+    a = _Args("tw_rmsnorm_quant", x)
+    kind, stride, add_kind = _norm_args(a, x, add, gamma, None, total)
+    a.shape(q, "q", _I8, (M, K))
+    a.shape(scale, "scale", _F32, (M,))
+    ev = _events(events)
+    with _on(x):
+        st = _lib.tw_rmsnorm_quant(_rows_ptr(x), kind, stride, _ptr(add), add_kind, _ptr(gamma),
+                                   eps, M, K, _ptr(total), _ptr(q), _ptr(scale), _stream(stream),
+                                   ev[0] if ev else None)
+    _check(st, "tw_rmsnorm_quant")
+
+
+def tw_rmsnorm_bwd_workspace_bytes(M, K) -> int:
+    return int(_lib.tw_rmsnorm_bwd_workspace_bytes(M, K))
+
+
+def tw_rmsnorm_bwd(dy, x, gamma, rstd, dx, dgamma=None, dres=None, ws=None, stream=None,
+                   events=None) -> None:
+    M, K = _dims2(x, "x", "tw_rmsnorm_bwd")
+    a = _Args("tw_rmsnorm_bwd", x)
+    kind, stride = a.rows(x, "x", _FLOATS)
+    dy_kind = a.typed(dy, "dy", _FLOATS, (M, K))
+    a.shape(gamma, "gamma", _F32, (K,))
+    a.shape(rstd, "rstd", _F32, (M,))
+    dx_kind = a.typed(dx, "dx", _FLOATS, (M, K))
+    a.opt(dres, "dres", dx.dtype, (M, K))
+    a.opt(dgamma, "dgamma", _F32, (K,))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    with _on(x):
+        st = _lib.tw_rmsnorm_bwd(_ptr(dy), dy_kind, _rows_ptr(x), kind, stride, _ptr(gamma),
+                                 _ptr(rstd), _ptr(dres), M, K, _ptr(dx), dx_kind, _ptr(dgamma),
+                                 _ptr(ws), _nbytes(ws), _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_rmsnorm_bwd")
+
+
+def tw_gated_ffn_workspace_bytes(M, K, N) -> int:
+    return int(_lib.tw_gated_ffn_workspace_bytes(M, K, N))
+
+
+def tw_gated_ffn_fwd(x, wg_t, wu_t, wd, y, ws, act="silu", g=None, u=None, stream=None,
+                     events=None) -> None:
+    """y = (act(x W_g) * (x W_u)) W_d; g and u receive the projections before
+    the activation."""
+    M, K = _dims2(x, "x", "tw_gated_ffn_fwd")
+    N = _dims2(wg_t, "wg_t", "tw_gated_ffn_fwd")[0]
+    a = _Args("tw_gated_ffn_fwd", x)
+    kind = _act(act, a.where)
+    _, stride = a.rows(x, "x", (_BF16,))
+    for t, name in ((wg_t, "wg_t"), (wu_t, "wu_t"), (wd, "wd")):
+        a.shape(t, name, _BF16, (N, K))
+    a.opt(g, "g", _BF16, (M, N))
+    a.opt(u, "u", _BF16, (M, N))
+    y_kind = a.typed(y, "y", _FLOATS, (M, K))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    with _on(x):
+        st = _lib.tw_gated_ffn_fwd(_rows_ptr(x), stride, _ptr(wg_t), _ptr(wu_t), _ptr(wd), kind, M,
+                                   K, N, _ptr(g), _ptr(u), _ptr(y), y_kind, _ptr(ws), _nbytes(ws),
+                                   _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_gated_ffn_fwd")
+
+
+def tw_gated_ffn_bwd_workspace_bytes(M, K, N) -> int:
+    return int(_lib.tw_gated_ffn_bwd_workspace_bytes(M, K, N))
+
+
+def tw_gated_ffn_bwd(dy, x, wg_t, wu_t, wd, g, u, ws, act="silu", dx=None, dwg_t=None, dwu_t=None,
+                     dwd=None, stream=None, events=None) -> None:
+    """Gradient of ``tw_gated_ffn_fwd`` from its g and u; the weight gradients
+    are of one type."""
+    M, K = _dims2(x, "x", "tw_gated_ffn_bwd")
+    N = _dims2(wg_t, "wg_t", "tw_gated_ffn_bwd")[0]
+    a = _Args("tw_gated_ffn_bwd", x)
+    kind = _act(act, a.where)
+    _, stride = a.rows(x, "x", (_BF16,))
+    a.shape(dy, "dy", _BF16, (M, K))
+    for t, name in ((wg_t, "wg_t"), (wu_t, "wu_t"), (wd, "wd")):
+        a.shape(t, name, _BF16, (N, K))
+    a.shape(g, "g", _BF16, (M, N))
+    a.shape(u, "u", _BF16, (M, N))
+    dx_kind = TW_BF16 if dx is None else a.typed(dx, "dx", _FLOATS, (M, K))
+    dw_kind = TW_BF16 if dwg_t is None else a.typed(dwg_t, "dwg_t", _FLOATS, (N, K))
+    for t, name in ((dwu_t, "dwu_t"), (dwd, "dwd")):
+        a.opt(t, name, _BF16 if dw_kind == TW_BF16 else _F32, (N, K))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    with _on(x):
+        st = _lib.tw_gated_ffn_bwd(_ptr(dy), _rows_ptr(x), stride, _ptr(wg_t), _ptr(wu_t),
+                                   _ptr(wd), kind, _ptr(g), _ptr(u), M, K, N, _ptr(dx), dx_kind,
+                                   _ptr(dwg_t), _ptr(dwu_t), _ptr(dwd), dw_kind, _ptr(ws),
+                                   _nbytes(ws), _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_gated_ffn_bwd")
+
+
+def tw_linear_ce_workspace_bytes(M, K, V) -> int:
+    return int(_lib.tw_linear_ce_workspace_bytes(M, K, V))
+
+
+def _ce_args(a, x, w, target):
+    M, K = x.shape
+    V = _dims2(w, "w", a.where)[0]
+    _, stride = a.rows(x, "x", (_BF16,))
+    a.shape(w, "w", _BF16, (V, K))
+    return V, stride, a.typed(target, "target", (_I32, _I64), (M,))
+
+
+def tw_linear_ce_fwd(x, w, target, loss, lse, ws, stream=None, events=None) -> None:
+    """loss and log-sum-exp of every row of x w^T; a row whose target is
+    outside [0, V) gets loss 0."""
+    M, K = _dims2(x, "x", "tw_linear_ce_fwd")
+    a = _Args("tw_linear_ce_fwd", x)
+    V, stride, t_kind = _ce_args(a, x, w, target)
+    a.shape(loss, "loss", _F32, (M,))
+    a.shape(lse, "lse", _F32, (M,))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    with _on(x):
+        st = _lib.tw_linear_ce_fwd(_rows_ptr(x), stride, _ptr(w), _ptr(target), t_kind, M, K, V,
+                                   _ptr(loss), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream),
+                                   ev[0] if ev else None)
+    _check(st, "tw_linear_ce_fwd")
+
+
+def tw_linear_ce_bwd_workspace_bytes(M, K, V) -> int:
+    return int(_lib.tw_linear_ce_bwd_workspace_bytes(M, K, V))
+
+
+def tw_linear_ce_bwd(dloss, x, w, target, lse, ws, dx=None, dw=None, stream=None,
+                     events=None) -> None:
+    """Gradient of ``tw_linear_ce_fwd`` from the gradient of every row's loss."""
+    M, K = _dims2(x, "x", "tw_linear_ce_bwd")
+    a = _Args("tw_linear_ce_bwd", x)
+    V, stride, t_kind = _ce_args(a, x, w, target)
+    a.shape(dloss, "dloss", _F32, (M,))
+    a.shape(lse, "lse", _F32, (M,))
+    dx_kind = TW_BF16 if dx is None else a.typed(dx, "dx", _FLOATS, (M, K))
+    dw_kind = TW_BF16 if dw is None else a.typed(dw, "dw", _FLOATS, (V, K))
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    with _on(x):
+        st = _lib.tw_linear_ce_bwd(_ptr(dloss), _rows_ptr(x), stride, _ptr(w), _ptr(target),
+                                   t_kind, _ptr(lse), M, K, V, _ptr(dx), dx_kind, _ptr(dw),
+                                   dw_kind, _ptr(ws), _nbytes(ws), _stream(stream),
+                                   ev[0] if ev else None)
+    _check(st, "tw_linear_ce_bwd")
+
+
+class _Buffers:
+    """The arrays of a call over many tensors: addresses, sizes, types."""
+
+    def __init__(self, a, tensors, name):
+        for t in tensors:
+            if not isinstance(t, torch.Tensor) or t.dtype not in _FLOATS:
+                raise TypeError(f"{a.where}: {name} must be tensors of {_FLOATS}")
+            if t.device != a.device:
+                raise ValueError(f"{a.where}: {name} are on {t.device} and {a.device}")
+        self.count = len(tensors)
+        self.p = (ctypes.c_void_p * self.count)(*[_ptr(t) for t in tensors])
+        self.n = (ctypes.c_int64 * self.count)(*[t.numel() for t in tensors])
+        self.type = (ctypes.c_int * self.count)(*[_TYPE[t.dtype] for t in tensors])
+
+
+def tw_grad_norm_workspace_bytes(sizes) -> int:
+    return int(_lib.tw_grad_norm_workspace_bytes(len(sizes), (ctypes.c_int64 * len(sizes))(*sizes)))
+
+
+def tw_grad_norm(grads, norm, ws, stream=None, events=None) -> None:
+    """norm (one fp32) = sqrt(sum of the squares of all elements)."""
+    a = _Args("tw_grad_norm", norm)
+    g = _Buffers(a, grads, "grads")
+    a.shape(norm, "norm", _F32, ())
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    with _on(norm):
+        st = _lib.tw_grad_norm(g.count, g.p, g.n, g.type, _ptr(norm), _ptr(ws), _nbytes(ws),
+                               _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_grad_norm")
+
+
+def tw_grad_clip(grads, out, max_norm, eps, norm, ws, stream=None, events=None) -> None:
+    """out[i] = grads[i] min(1, max_norm / (norm + eps)); out may be grads."""
+    a = _Args("tw_grad_clip", norm)
+    g, o = _Buffers(a, grads, "grads"), _Buffers(a, out, "out")
+    if [t.shape for t in out] != [t.shape for t in grads]:
+        raise ValueError(f"{a.where}: out and grads have different shapes")
+    a.shape(norm, "norm", _F32, ())
+    a.bytes(ws, "ws")
+    ev = _events(events)
+    with _on(norm):
+        st = _lib.tw_grad_clip(g.count, g.p, g.n, g.type, o.p, o.type, max_norm, eps, _ptr(norm),
+                               _ptr(ws), _nbytes(ws), _stream(stream), ev[0] if ev else None)
+    _check(st, "tw_grad_clip")
+
+
 # ------------------------------------------------------------- allocating --
 def alloc_pack(M, N, T, C, R_max, device="cuda"):
     """Output buffers of tw_pack_gate."""
@@ -974,6 +1253,140 @@ def quant_gateup(x, wg, g_scale, wu, u_scale, gamma=None, beta=None, eps=1e-5, x
     tw_quant_gateup(x, wg, g_scale, wu, u_scale, h, gamma=gamma, beta=beta, eps=eps,
                     x_scale=x_scale, ws=_quant_ws(x) if ws is None else ws)
     return h
+
+
+def rmsnorm(x, gamma, eps=1e-5, add=None, out_dtype=torch.bfloat16):
+    """RMS norm of the rows of x (+ add).  Returns a dict: y, rstd (fp32, for
+    ``rmsnorm_backward``), and sum = x + add in x's type (None without add)."""
+    M, K = _dims2(x, "x", "rmsnorm")
+    dev = x.device
+    out = {
+        "y": torch.empty((M, K), dtype=out_dtype, device=dev),
+        "sum": None if add is None else torch.empty((M, K), dtype=x.dtype, device=dev),
+        "rstd": torch.empty((M,), dtype=_F32, device=dev),
+    }
+    tw_rmsnorm_fwd(x, gamma, eps, out["y"], add=add, total=out["sum"], rstd=out["rstd"])
+    return out
+
+
+def rmsnorm_backward(dy, x, gamma, rstd, dres=None, dx_dtype=torch.float32):
+    """Gradient of ``rmsnorm``: x is its input (``sum`` if there was an add),
+    dres the gradient reaching x past the norm (dx's dtype).  Returns a dict
+    with dx, dgamma."""
+    M, K = _dims2(x, "x", "rmsnorm_backward")
+    dev = x.device
+    out = {
+        "dx": torch.empty((M, K), dtype=dx_dtype, device=dev),
+        "dgamma": torch.empty((K,), dtype=_F32, device=dev),
+    }
+    ws = torch.empty((tw_rmsnorm_bwd_workspace_bytes(M, K),), dtype=_U8T, device=dev)
+    tw_rmsnorm_bwd(dy, x, gamma, rstd, out["dx"], out["dgamma"], dres=dres, ws=ws)
+    return out
+
+
+def rmsnorm_quantize(x, gamma, eps=1e-5, add=None):
+    """The RMS norm of x (+ add) in int8.  Returns a dict: q, scale, and
+    sum = x + add in x's type (None without add)."""
+    M, K = _dims2(x, "x", "rmsnorm_quantize")
+    out = {
+        "q": torch.empty((M, K), dtype=_I8, device=x.device),
+        "scale": torch.empty((M,), dtype=_F32, device=x.device),
+        "sum": None if add is None else torch.empty((M, K), dtype=x.dtype, device=x.device),
+    }
+    tw_rmsnorm_quant(x, gamma, eps, out["q"], out["scale"], add=add, total=out["sum"])
+    return out
+
+
+def _scratch(n, device):
+    return torch.empty((n,), dtype=_U8T, device=device) if n else None
+
+
+def gated_ffn(x, wg_t, wu_t, wd, act="silu", keep=False, out_dtype=torch.bfloat16, ws=None):
+    """The dense gated FFN (act(x W_g) * (x W_u)) W_d, act "relu", "silu" or
+    "gelu".  Returns a dict: y, and with ``keep`` g and u (what
+    ``gated_ffn_backward`` reads; None without)."""
+    M, K = _dims2(x, "x", "gated_ffn")
+    N = _dims2(wg_t, "wg_t", "gated_ffn")[0]
+    dev = x.device
+    out = {
+        "y": torch.empty((M, K), dtype=out_dtype, device=dev),
+        "g": torch.empty((M, N), dtype=_BF16, device=dev) if keep else None,
+        "u": torch.empty((M, N), dtype=_BF16, device=dev) if keep else None,
+    }
+    ws = _scratch(tw_gated_ffn_workspace_bytes(M, K, N), dev) if ws is None else ws
+    tw_gated_ffn_fwd(x, wg_t, wu_t, wd, out["y"], ws, act=act, g=out["g"], u=out["u"])
+    return out
+
+
+def gated_ffn_backward(dy, x, wg_t, wu_t, wd, g, u, act="silu", dx_dtype=torch.bfloat16,
+                       dw_dtype=torch.bfloat16, ws=None):
+    """Gradient of ``gated_ffn`` from its g and u.  Returns a dict: dx, dwg_t,
+    dwu_t, dwd."""
+    M, K = _dims2(x, "x", "gated_ffn_backward")
+    N = _dims2(wg_t, "wg_t", "gated_ffn_backward")[0]
+    dev = x.device
+    out = {"dx": torch.empty((M, K), dtype=dx_dtype, device=dev)}
+    for k in ("dwg_t", "dwu_t", "dwd"):
+        out[k] = torch.empty((N, K), dtype=dw_dtype, device=dev)
+    ws = _scratch(tw_gated_ffn_bwd_workspace_bytes(M, K, N), dev) if ws is None else ws
+    tw_gated_ffn_bwd(dy, x, wg_t, wu_t, wd, g, u, ws, act=act, **out)
+    return out
+
+
+def linear_ce(x, w, target, ws=None):
+    """Cross entropy of the logits x w^T against one target a row (w: [V][K];
+    a target outside [0, V) leaves its row out).  Returns a dict: loss and lse
+    (log-sum-exp) of every row, fp32."""
+    M, K = _dims2(x, "x", "linear_ce")
+    V = _dims2(w, "w", "linear_ce")[0]
+    out = {k: torch.empty((M,), dtype=_F32, device=x.device) for k in ("loss", "lse")}
+    ws = _scratch(tw_linear_ce_workspace_bytes(M, K, V), x.device) if ws is None else ws
+    tw_linear_ce_fwd(x, w, target, out["loss"], out["lse"], ws)
+    return out
+
+
+def linear_ce_backward(dloss, x, w, target, lse, dx_dtype=torch.bfloat16, dw_dtype=torch.bfloat16,
+                       ws=None):
+    """Gradient of ``linear_ce`` for dloss (fp32, one a row).  Returns a dict:
+    dx, dw."""
+    M, K = _dims2(x, "x", "linear_ce_backward")
+    V = _dims2(w, "w", "linear_ce_backward")[0]
+    out = {"dx": torch.empty((M, K), dtype=dx_dtype, device=x.device),
+           "dw": torch.empty((V, K), dtype=dw_dtype, device=x.device)}
+    ws = _scratch(tw_linear_ce_bwd_workspace_bytes(M, K, V), x.device) if ws is None else ws
+    tw_linear_ce_bwd(dloss, x, w, target, lse, ws, **out)
+    return out
+
+
+def _grads(grads, where):
+    grads = list(grads)
+    if not grads:
+        raise ValueError(f"{where}: there are no gradients")
+    if not isinstance(grads[0], torch.Tensor):
+        raise TypeError(f"{where}: grads must be tensors of {_FLOATS}")
+    return grads
+
+
+def grad_norm(grads):
+    """The norm over all elements of a list of tensors (bf16 or fp32), as a
+    scalar tensor."""
+    grads = _grads(grads, "grad_norm")
+    dev = grads[0].device
+    norm = torch.empty((), dtype=_F32, device=dev)
+    tw_grad_norm(grads, norm, _scratch(tw_grad_norm_workspace_bytes([t.numel() for t in grads]), dev))
+    return norm
+
+
+def clip_grads(grads, max_norm, eps=1e-6, out=None):
+    """Scales the gradients by min(1, max_norm / (norm + eps)), in place or
+    into ``out`` (a list of tensors of the same shapes, bf16 or fp32).  Returns the
+    norm before, a scalar tensor."""
+    grads = _grads(grads, "clip_grads")
+    dev = grads[0].device
+    norm = torch.empty((), dtype=_F32, device=dev)
+    tw_grad_clip(grads, grads if out is None else list(out), max_norm, eps, norm,
+                 _scratch(tw_grad_norm_workspace_bytes([t.numel() for t in grads]), dev))
+    return norm
 
 
 def library_path() -> str:

@@ -26,8 +26,12 @@
  * over the hybrid storage of sections 3-6 and 3-7, and tw_hybrid_bwd_dh,
  * tw_hybrid_bwd_dx and tw_hybrid_bwd_dw its backward.  tw_layernorm_fwd and
  * tw_layernorm_bwd are the layer norm in front of the block, and
- * tw_quant_gateup and tw_quant_linear its dense projections in 8-bit integers
- * (declared at the end).
+ * tw_quant_gateup and tw_quant_linear its dense projections in 8-bit integers.
+ * The dense training step beside it (declared at the end): the RMS norm
+ * tw_rmsnorm_fwd, tw_rmsnorm_quant and tw_rmsnorm_bwd, the gated FFN with any of
+ * three activations tw_gated_ffn_fwd and tw_gated_ffn_bwd, the cross entropy of an
+ * output projection tw_linear_ce_fwd and tw_linear_ce_bwd, and gradient clipping,
+ * tw_grad_norm and tw_grad_clip.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -91,7 +95,17 @@ typedef enum tw_status {
 } tw_status;
 
 /* Element type of a row buffer, where an entry point takes more than one. */
-typedef enum tw_type { TW_BF16 = 0, TW_F32 = 1, TW_INT8 = 2 } tw_type;
+typedef enum tw_type {
+    TW_BF16 = 0,
+    TW_F32 = 1,
+    TW_INT8 = 2,
+    TW_INT32 = 3, /* targets of tw_linear_ce_fwd, tw_linear_ce_bwd */
+    TW_INT64 = 4
+} tw_type;
+
+/* Activation of the gated FFN: ReLU, SiLU (g / (1 + e^-g)), GELU in its tanh
+ * form (g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2). */
+typedef enum tw_act { TW_RELU = 0, TW_SILU = 1, TW_GELU = 2 } tw_act;
 
 /* Static name of a status code. */
 const char *tw_status_str(int status);
@@ -520,6 +534,143 @@ tw_status tw_quant_gateup(const void *x, int x_type, int64_t x_stride, const flo
                           const float *g_scale, const int8_t *wu, const float *u_scale, int M,
                           int K, int N, void *h, int h_type, void *ws, size_t ws_bytes,
                           void *stream, void *const *events);
+
+/*
+ * RMS norm over the last dimension.  For every row m, in fp32:
+ *     z = x[m] (+ add[m]),  rstd = 1 / sqrt(sum(z^2) / K + eps),
+ *     y[m] = z * rstd * gamma.
+ * Arguments, types and limits as in tw_layernorm_fwd (there is no mean and no
+ * beta); tw_rmsnorm_quant quantises the unrounded norm as tw_layernorm_quant
+ * does.  A row holding a NaN gives NaN; one holding an infinity gives NaN there
+ * and zeros elsewhere.  events: [0] before, [1] after the kernel.
+ */
+tw_status tw_rmsnorm_fwd(const void *x, int x_type, int64_t x_stride, const void *add,
+                         int add_type, const float *gamma, float eps, int M, int K, void *sum,
+                         void *y, int y_type, float *rstd, void *stream, void *const *events);
+tw_status tw_rmsnorm_quant(const void *x, int x_type, int64_t x_stride, const void *add,
+                           int add_type, const float *gamma, float eps, int M, int K, void *sum,
+                           int8_t *q, float *scale, void *stream, void *const *events);
+
+/*
+ * RMS norm, backward: with n = x rstd (x: the forward's z as stored, in `sum`
+ * if there was an add) and t = dy gamma,
+ *     dx = rstd (t - n sum(t n) / K) (+ dres),   dgamma = sum over rows of dy n.
+ * Arguments, order of the sums, workspace and events as in tw_layernorm_bwd.
+ */
+size_t tw_rmsnorm_bwd_workspace_bytes(int M, int K);
+tw_status tw_rmsnorm_bwd(const void *dy, int dy_type, const void *x, int x_type, int64_t x_stride,
+                         const float *gamma, const float *rstd, const void *dres, int M, int K,
+                         void *dx, int dx_type, float *dgamma, void *ws, size_t ws_bytes,
+                         void *stream, void *const *events);
+
+/*
+ * Dense gated FFN, forward: y = h W_d with h = act(g) u, g = x W_g, u = x W_u
+ * (act: a tw_act).  h is rounded to bf16 between the two products; sums are
+ * fp32.
+ *
+ *   x       [M] rows of K bf16, x_stride elements apart
+ *   wg_t, wu_t, wd [N][K] bf16, as above
+ *   g, u    [M][N]  bf16, each may be NULL: the projections before the
+ *                   activation, which tw_gated_ffn_bwd reads
+ *   y       [M][K]  bf16 or fp32
+ *
+ * K, N and x_stride multiples of 8, K and N at most 2^20, x_stride from K to
+ * 2^20; M at most 2^24.  ws_bytes >= tw_gated_ffn_workspace_bytes(M, K, N) (0
+ * for sizes the call rejects; ws may be NULL when M is 0).  Results are
+ * bit-identical run to run.  events: [0] before, [1] after h, [2] after y.
+ */
+size_t tw_gated_ffn_workspace_bytes(int M, int K, int N);
+tw_status tw_gated_ffn_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
+                           const uint16_t *wu_t, const uint16_t *wd, int act, int M, int K, int N,
+                           uint16_t *g, uint16_t *u, void *y, int y_type, void *ws,
+                           size_t ws_bytes, void *stream, void *const *events);
+
+/*
+ * Dense gated FFN, backward, from dy = dLoss/dy and the forward's g and u:
+ *     dh = dy W_d^T,  du = dh act(g),  dz = dh u act'(g),  h = act(g) u,
+ *     dx = dz W_g^T + du W_u^T,
+ *     dwg_t = dz^T x,  dwu_t = du^T x,  dwd = h^T dy.
+ * dz, du and h are rounded to bf16 between the products; sums are fp32.
+ *
+ *   dy      [M][K]  bf16;  x as in the forward;  g, u [M][N] bf16
+ *   dx      [M][K]  bf16 or fp32, or NULL
+ *   dwg_t, dwu_t, dwd [N][K] bf16 or fp32, all three or none (NULL)
+ *
+ * Limits as in the forward.  With M = 0 the weight gradients are zeros.
+ * ws_bytes >= tw_gated_ffn_bwd_workspace_bytes(M, K, N).  events: [0] before,
+ * [1] after dz, du and h, [2] after dx, [3] after the weight gradients.
+ */
+size_t tw_gated_ffn_bwd_workspace_bytes(int M, int K, int N);
+tw_status tw_gated_ffn_bwd(const uint16_t *dy, const uint16_t *x, int64_t x_stride,
+                           const uint16_t *wg_t, const uint16_t *wu_t, const uint16_t *wd, int act,
+                           const uint16_t *g, const uint16_t *u, int M, int K, int N, void *dx,
+                           int dx_type, void *dwg_t, void *dwu_t, void *dwd, int dw_type, void *ws,
+                           size_t ws_bytes, void *stream, void *const *events);
+
+/*
+ * Softmax cross entropy of an output projection: with the logits l = x w^T
+ * (never stored) and a row's target t,
+ *     lse[m] = log sum_v exp(l[m][v]),   loss[m] = lse[m] - l[m][t].
+ * A row whose target lies outside [0, V) is left out: its loss is 0 (lse is
+ * there all the same).
+ *
+ *   x       [M] rows of K bf16, x_stride elements apart
+ *   w       [V][K] bf16
+ *   target  [M]  32- or 64-bit integers (target_type TW_INT32 or TW_INT64)
+ *   loss, lse [M] fp32
+ *
+ * K and x_stride multiples of 8, K at most 2^20, x_stride from K to 2^20, V up
+ * to 2^24, M up to 2^24.  ws_bytes >= tw_linear_ce_workspace_bytes(M, K, V).
+ * Results are bit-identical run to run.  events: [0] before, [1] after the
+ * kernels.
+ */
+size_t tw_linear_ce_workspace_bytes(int M, int K, int V);
+tw_status tw_linear_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w,
+                           const void *target, int target_type, int M, int K, int V, float *loss,
+                           float *lse, void *ws, size_t ws_bytes, void *stream,
+                           void *const *events);
+
+/*
+ * Its gradient, for dloss[m] = dLoss/dloss[m] (fp32) and the forward's lse:
+ *     D[m][v] = dloss[m] (exp(l[m][v] - lse[m]) - [v = t]),
+ *     dx = D w,   dw = D^T x
+ * (rows of D of rows that are left out are 0; their x enters dw times 0, so it
+ * has to be finite).  The logits are computed again, a piece of the vocabulary
+ * at a time, and D is rounded to bf16; sums are fp32.
+ *
+ *   dx      [M][K]  bf16 or fp32, or NULL;  dw [V][K] bf16 or fp32, or NULL
+ *
+ * Limits as in the forward.  With M = 0, dw is zeros.  ws_bytes >=
+ * tw_linear_ce_bwd_workspace_bytes(M, K, V): a piece of D (at most 256 MB, or
+ * 256 columns) and fp32 sums of dx.
+ */
+size_t tw_linear_ce_bwd_workspace_bytes(int M, int K, int V);
+tw_status tw_linear_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride,
+                           const uint16_t *w, const void *target, int target_type,
+                           const float *lse, int M, int K, int V, void *dx, int dx_type, void *dw,
+                           int dw_type, void *ws, size_t ws_bytes, void *stream,
+                           void *const *events);
+
+/*
+ * Gradient norm and clipping over `count` buffers of n[i] elements each:
+ *     norm = sqrt(sum over all elements of g^2),
+ *     out = g min(1, max_norm / (norm + eps)).
+ * The arrays g, n, g_type, out and out_type are read on the host during the
+ * call.  A buffer's type is TW_BF16 or TW_F32; its address is aligned to its
+ * type and may be NULL where n is 0.  out[i] may be g[i] itself (of the same
+ * type); otherwise no output may overlap another buffer of the call, which is
+ * checked.  A norm that is NaN makes every output NaN.  n[i] at most 2^34;
+ * count at most 2^20.  ws_bytes >= tw_grad_norm_workspace_bytes(count, n).
+ * Squares are summed in fp32, in a fixed order (bit-identical run to run).
+ * norm: one fp32, aligned to 4.  events of tw_grad_norm: [0] before, [1] after;
+ * of tw_grad_clip: [0] before, [1] after the squares' sums, [2] after.
+ */
+size_t tw_grad_norm_workspace_bytes(int count, const int64_t *n);
+tw_status tw_grad_norm(int count, const void *const *g, const int64_t *n, const int *g_type,
+                       float *norm, void *ws, size_t ws_bytes, void *stream, void *const *events);
+tw_status tw_grad_clip(int count, const void *const *g, const int64_t *n, const int *g_type,
+                       void *const *out, const int *out_type, float max_norm, float eps,
+                       float *norm, void *ws, size_t ws_bytes, void *stream, void *const *events);
 
 #ifdef __cplusplus
 }
