@@ -55,19 +55,22 @@ __device__ __forceinline__ Slope activate_slope(float g) {
 template <int ACT>
 struct EpiGlu {
     static constexpr bool kStats = false;
-    uint16_t *g, *u, *h;  // g, u or null
-    int M, N;
-    struct Row {};
-    __device__ Row row(int) const { return {}; }
-    __device__ __forceinline__ void quad(int, int, Row &, int m, int n, f32x4 v, f32x4 w) const {
-        if (n >= N) return;
-        const int64_t at = (int64_t)m * N + n;
-        f32x4 o;
+    static constexpr int kOuts = 3;
+    uint16_t *h, *g, *u;  // g, u or null
+    int N;
+    struct Raw {};
+    struct Row {
+        __device__ Row(const EpiGlu &, Raw) {}
+    };
+    __device__ Raw raw(int) const { return {}; }
+    __device__ __forceinline__ Dest dest(int o, int, int) const {
+        return {o == 0 ? h : o == 1 ? g : u, TW_T_BF16, N, N, false};
+    }
+    __device__ __forceinline__ void values(Row &, int, int, f32x4 v, f32x4 w, f32x4 *o) const {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = activate<ACT>(v[e]) * w[e];
-        store4(h, TW_T_BF16, at, o);
-        if (g) store4(g, TW_T_BF16, at, v);
-        if (u) store4(u, TW_T_BF16, at, w);
+        for (int e = 0; e < 4; ++e) o[0][e] = activate<ACT>(v[e]) * w[e];
+        o[1] = v;
+        o[2] = w;
     }
 };
 
@@ -75,37 +78,39 @@ struct EpiGlu {
 template <int ACT>
 struct EpiDh {
     static constexpr bool kStats = false;
+    static constexpr int kOuts = 3;
     const uint16_t *g, *u;
     uint16_t *dz, *du, *h;
-    int M, N;
-    struct Row {};
-    __device__ Row row(int) const { return {}; }
-    __device__ __forceinline__ void quad(int, int, Row &, int m, int n, f32x4 v, f32x4) const {
-        if (n >= N) return;
-        const int64_t at = (int64_t)m * N + n;
+    int N;
+    struct Raw {};
+    struct Row {
+        __device__ Row(const EpiDh &, Raw) {}
+    };
+    __device__ Raw raw(int) const { return {}; }
+    __device__ __forceinline__ Dest dest(int o, int, int) const {
+        return {o == 0 ? dz : o == 1 ? du : h, TW_T_BF16, N, N, false};
+    }
+    __device__ __forceinline__ void values(Row &, int m, int n, f32x4 v, f32x4, f32x4 *o) const {
+        const int64_t at = (int64_t)m * N + min(n, N - 4);
         const f32x4 gv = load4_bf16(g, at), uv = load4_bf16(u, at);
-        f32x4 oz, ou, oh;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const Slope a = activate_slope<ACT>(gv[e]);
-            oz[e] = v[e] * uv[e] * a.slope;
-            ou[e] = v[e] * a.value;
-            oh[e] = a.value * uv[e];
+            o[0][e] = v[e] * uv[e] * a.slope;
+            o[1][e] = v[e] * a.value;
+            o[2][e] = a.value * uv[e];
         }
-        store4(dz, TW_T_BF16, at, oz);
-        store4(du, TW_T_BF16, at, ou);
-        store4(h, TW_T_BF16, at, oh);
     }
 };
 
 template <int ACT>
 hipError_t ffn_up(const TileArgs &p, uint16_t *g, uint16_t *u, uint16_t *h, hipStream_t s) {
-    return launch_ring<kRows, kRows, 2, 1>(p, EpiGlu<ACT>{g, u, h, p.M, p.N}, 1, s);
+    return launch_tiles<kRows, kRows, 2, 1>(p, EpiGlu<ACT>{h, g, u, p.N}, s);
 }
 template <int ACT>
 hipError_t ffn_dh(const TileArgs &p, const uint16_t *g, const uint16_t *u, uint16_t *dz,
                   uint16_t *du, uint16_t *h, hipStream_t s) {
-    return launch_ring<kRows, kRows, 1, 1>(p, EpiDh<ACT>{g, u, dz, du, h, p.M, p.N}, 1, s);
+    return launch_tiles<kRows, kRows, 1, 1>(p, EpiDh<ACT>{g, u, dz, du, h, p.N}, s);
 }
 
 }  // namespace
@@ -116,7 +121,7 @@ size_t ffn_bwd_part_bytes(int, int, int) { return 0; }
 hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
                          const uint16_t *wu_t, int act, int M, int K, int N, uint16_t *g,
                          uint16_t *u, uint16_t *h, float *, hipStream_t s) {
-    const TileArgs p{{x}, {wg_t, wu_t}, x_stride, K, M, N, K, 1};
+    const TileArgs p{{x}, {wg_t, wu_t}, x_stride, K, M, N, K};
     if (act == TW_A_RELU) return ffn_up<TW_A_RELU>(p, g, u, h, s);
     if (act == TW_A_SILU) return ffn_up<TW_A_SILU>(p, g, u, h, s);
     return ffn_up<TW_A_GELU>(p, g, u, h, s);
@@ -124,14 +129,14 @@ hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg
 
 hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, int N, void *y,
                            int y_type, float *, hipStream_t s) {
-    const TileArgs p{{h}, {wd}, N, K, M, K, N, 1};
-    return launch_ring<kRows, kCols, 1, 1>(p, EpiStore{{y}, y_type, nullptr, 0, M, K}, 1, s);
+    const TileArgs p{{h}, {wd}, N, K, M, K, N};
+    return launch_tiles<kRows, kCols, 1, 1>(p, EpiStore{{y}, y_type, nullptr, 0, M, K}, s);
 }
 
 hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const uint16_t *g,
                          const uint16_t *u, int M, int K, int N, uint16_t *dz, uint16_t *du,
                          uint16_t *h, hipStream_t s) {
-    const TileArgs p{{dy}, {wd}, K, K, M, N, K, 1};
+    const TileArgs p{{dy}, {wd}, K, K, M, N, K};
     if (act == TW_A_RELU) return ffn_dh<TW_A_RELU>(p, g, u, dz, du, h, s);
     if (act == TW_A_SILU) return ffn_dh<TW_A_SILU>(p, g, u, dz, du, h, s);
     return ffn_dh<TW_A_GELU>(p, g, u, dz, du, h, s);
@@ -140,8 +145,8 @@ hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const 
 hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t *wg_t,
                          const uint16_t *wu_t, int M, int K, int N, void *dx, int dx_type,
                          float *, hipStream_t s) {
-    const TileArgs p{{dz, du}, {wg_t, wu_t}, N, K, M, K, N, 1};
-    return launch_ring<kRows, kCols, 1, 2>(p, EpiStore{{dx}, dx_type, nullptr, 0, M, K}, 1, s);
+    const TileArgs p{{dz, du}, {wg_t, wu_t}, N, K, M, K, N};
+    return launch_tiles<kRows, kCols, 1, 2>(p, EpiStore{{dx}, dx_type, nullptr, 0, M, K}, s);
 }
 
 hipError_t launch_ffn_dw(const uint16_t *dz, const uint16_t *du, const uint16_t *h,
@@ -149,12 +154,12 @@ hipError_t launch_ffn_dw(const uint16_t *dz, const uint16_t *du, const uint16_t 
                          int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, float *,
                          hipStream_t s) {
     // W_g and W_u share x; dy, of another stride, is W_d's
-    const TileArgs p{{dz, du}, {x, x}, N, x_stride, N, K, M, 1};
-    hipError_t e = launch_ring<kCols, kCols, 1, 1>(
-        p, EpiStore{{dwg_t, dwu_t}, dw_type, nullptr, 0, N, K}, 2, s);
+    const TileArgs p{{dz, du}, {x, x}, N, x_stride, N, K, M, 1, 2};
+    hipError_t e = launch_tiles<kCols, kCols, 1, 1>(
+        p, EpiStore{{dwg_t, dwu_t}, dw_type, nullptr, 0, N, K}, s);
     if (e != hipSuccess) return e;
-    const TileArgs q{{h}, {dy}, N, K, N, K, M, 1};
-    return launch_ring<kCols, kCols, 1, 1>(q, EpiStore{{dwd}, dw_type, nullptr, 0, N, K}, 1, s);
+    const TileArgs q{{h}, {dy}, N, K, N, K, M};
+    return launch_tiles<kCols, kCols, 1, 1>(q, EpiStore{{dwd}, dw_type, nullptr, 0, N, K}, s);
 }
 
 }  // namespace tw

@@ -22,12 +22,9 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// A row's target if it lies in [first, first + count), relative to first, else -1.
-__device__ __forceinline__ int target_of(Targets t, int m, int64_t first, int64_t count) {
-    const int64_t v = (t.wide ? static_cast<const int64_t *>(t.p)[m]
-                              : (int64_t) static_cast<const int32_t *>(t.p)[m]);
-    // (v - first may overflow for a target far outside)
-    return v >= first && v < first + count ? (int)(v - first) : -1;
+__device__ __forceinline__ int64_t target(Targets t, int m) {
+    return t.wide ? static_cast<const int64_t *>(t.p)[m]
+                  : (int64_t) static_cast<const int32_t *>(t.p)[m];
 }
 
 // Largest logit and sum of exponentials of a set of columns, in units of
@@ -47,10 +44,12 @@ struct EpiSoft {
     static constexpr bool kStats = true;
     Soft *part;  // [column blocks][M]
     int M, N;
+    struct Raw {};
     struct Row {
-        float most, top, sum;
+        float most = -INFINITY, top = 0.0f, sum = 0.0f;
+        __device__ Row(const EpiSoft &, Raw) {}
     };
-    __device__ Row row(int) const { return {-INFINITY, 0.0f, 0.0f}; }
+    __device__ Raw raw(int) const { return {}; }
     __device__ __forceinline__ void most(Row &r, int n, f32x4 v) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -81,6 +80,9 @@ struct EpiSoft {
         for (int w = 1; w < W; ++w) j = join_soft(j, s[w * 256]);
         part[(int64_t)cb * M + m] = j;
     }
+    __device__ __forceinline__ void whole(const Row &r, int m, int cb) const {
+        part[(int64_t)cb * M + m] = {r.top, r.sum};
+    }
 };
 
 // Joins the column blocks of a row and takes the target's logit: 16 threads a
@@ -104,10 +106,10 @@ __global__ __launch_bounds__(256) void ce_rows_kernel(const Soft *__restrict__ p
     // the dot products have 16 neighbouring threads a row
     const int dr = threadIdx.x >> 4, di = threadIdx.x & 15;
     const int dm = blockIdx.x * 16 + dr;
-    const int tgt = dm < M ? target_of(t, dm, 0, V) : -1;
+    const int64_t tgt = dm < M ? target(t, dm) : -1;
     float d = 0.0f;
-    if (tgt >= 0) {
-        const uint16_t *xr = x + dm * x_stride, *wr = w + (int64_t)tgt * K;
+    if (tgt >= 0 && tgt < V) {
+        const uint16_t *xr = x + dm * x_stride, *wr = w + tgt * K;
         for (int k = 8 * di; k < K; k += 128) {
             const u32x4 a = ld16(xr + k), b = ld16(wr + k);
 #pragma unroll
@@ -126,35 +128,45 @@ __global__ __launch_bounds__(256) void ce_rows_kernel(const Soft *__restrict__ p
     lse[m] = l;
     // a loss is never negative; the two sums may cross by a rounding
     const float v = l - dots[r];
-    loss[m] = target_of(t, m, 0, V) < 0 ? 0.0f : v < 0.0f ? 0.0f : v;
+    const int64_t tm = target(t, m);
+    loss[m] = tm < 0 || tm >= V || v < 0.0f ? 0.0f : v;
 }
 
 // D of a piece of the vocabulary, columns first .. first + N - 1 of V.
 struct EpiD {
     static constexpr bool kStats = false;
+    static constexpr int kOuts = 1;
     const float *lse, *dloss;
     Targets t;
     uint16_t *d;
     int64_t ldd;  // N rounded up to 8; the columns past N are written as zeros
-    int M, N, first, V;
+    int N, first, V;
+    struct Raw {
+        float lse, dloss;
+        int64_t t;
+    };
     struct Row {
         float top, scale;
         int t;
         bool live;
+        __device__ __forceinline__ Row(const EpiD &e, const Raw &r) {
+            live = r.t >= 0 && r.t < e.V;
+            t = live && r.t >= e.first && r.t < e.first + e.N ? (int)(r.t - e.first) : -1;
+            top = r.lse * kLog2e;
+            scale = r.dloss;
+        }
     };
-    __device__ __forceinline__ Row row(int m) const {
-        return {lse[m] * kLog2e, dloss[m], target_of(t, m, first, N), target_of(t, m, 0, V) >= 0};
+    __device__ __forceinline__ Raw raw(int m) const { return {lse[m], dloss[m], target(t, m)}; }
+    __device__ __forceinline__ Dest dest(int, int, int) const {
+        return {d, TW_T_BF16, ldd, (int)ldd, false};
     }
-    __device__ __forceinline__ void quad(int, int, Row &r, int m, int n, f32x4 v, f32x4) const {
-        if (n >= ldd) return;
-        f32x4 o;
+    __device__ __forceinline__ void values(Row &r, int, int n, f32x4 v, f32x4, f32x4 *o) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float p = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
             if (n + e == r.t) p -= 1.0f;
-            o[e] = r.live && n + e < N ? p * r.scale : 0.0f;
+            o[0][e] = r.live && n + e < N ? p * r.scale : 0.0f;
         }
-        store4(d, TW_T_BF16, m * ldd + n, o);
     }
 };
 
@@ -179,17 +191,17 @@ Pieces pieces_of(int M, int K, int V) {
 }  // namespace
 
 size_t ce_fwd_bytes(int M, int, int V) {
-    return up256((size_t)M * (((size_t)V + kRingBN - 1) / kRingBN) * sizeof(Soft));
+    return up256((size_t)M * (((size_t)V + 127) / 128) * sizeof(Soft));
 }
 
 hipError_t launch_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w, Targets t, int M,
                          int K, int V, float *loss, float *lse, void *ws, hipStream_t s) {
     if (M == 0) return hipSuccess;
-    const TileArgs p{{x}, {w}, x_stride, K, M, V, K, 1};
+    const TileArgs p{{x}, {w}, x_stride, K, M, V, K};
     Soft *part = static_cast<Soft *>(ws);
-    hipError_t e = launch_ring<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, 1, s);
+    hipError_t e = launch_tiles<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, s);
     if (e != hipSuccess) return e;
-    ce_rows_kernel<<<(M + 15) / 16, 256, 0, s>>>(part, (V + kRingBN - 1) / kRingBN, x, x_stride, w,
+    ce_rows_kernel<<<(M + 15) / 16, 256, 0, s>>>(part, (V + 127) / 128, x, x_stride, w,
                                                  t, M, K, V, loss, lse);
     return hipGetLastError();
 }
@@ -211,18 +223,15 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
         const int64_t ldd = (N + 7) / 8 * 8;
         const uint16_t *wp = w + (int64_t)first * K;
         if (M > 0)
-            e = launch_ring<kRows, kRows, 1, 1>(
-                TileArgs{{x}, {wp}, x_stride, K, M, N, K, 1},
-                EpiD{lse, dloss, t, d, ldd, M, N, first, V}, 1, s);
+            e = launch_tiles<kRows, kRows, 1, 1>(TileArgs{{x}, {wp}, x_stride, K, M, N, K},
+                                                 EpiD{lse, dloss, t, d, ldd, N, first, V}, s);
         if (e == hipSuccess && dx)
-            e = launch_ring<kRows, kCols, 1, 1>(
-                TileArgs{{d}, {wp}, ldd, K, M, K, N, 1},
-                EpiStore{{dx}, dx_type, part, first > 0, M, K}, 1, s);
+            e = launch_tiles<kRows, kCols, 1, 1>(TileArgs{{d}, {wp}, ldd, K, M, K, N},
+                                                 EpiStore{{dx}, dx_type, part, first > 0, M, K}, s);
         if (e == hipSuccess && dw) {
             char *out = static_cast<char *>(dw) + (int64_t)first * K * (dw_type == TW_T_F32 ? 4 : 2);
-            e = launch_ring<kCols, kCols, 1, 1>(
-                TileArgs{{d}, {x}, ldd, x_stride, N, K, M, 1},
-                EpiStore{{out}, dw_type, nullptr, 0, N, K}, 1, s);
+            e = launch_tiles<kCols, kCols, 1, 1>(TileArgs{{d}, {x}, ldd, x_stride, N, K, M},
+                                                 EpiStore{{out}, dw_type, nullptr, 0, N, K}, s);
         }
     }
     if (e == hipSuccess && dx && part) e = launch_sum_parts(part, 1, (int64_t)M * K, dx, dx_type, s);

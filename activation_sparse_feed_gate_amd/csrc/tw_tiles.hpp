@@ -11,6 +11,7 @@
 #pragma once
 
 #include "tw_gemm.hpp"
+#include "tw_quant_rules.hpp"
 #include "tw_rows.hpp"
 
 namespace tw {
@@ -23,14 +24,39 @@ constexpr uint32_t kPastEnd = 1u << 30;
 constexpr int64_t kMaxStride = 1 << 20;  // elements between operand rows
 
 // The operands of one launch.  What a[1], b[1], ... are is the kernel's: a
-// second weight matrix next to b[0] (NB = 2), further terms of the sum (SEG),
-// or other products of the same shape (blockIdx.y).
+// second weight matrix next to b[0] (NB = 2), a second term of the sum (SEG =
+// 2: the reduction runs over both), or other products of the same shape.
 struct TileArgs {
     const uint16_t *a[3], *b[3];
     int64_t lda, ldb;  // elements between rows
     int M, N, R;
-    int splits;        // parts of the reduction (blockIdx.z)
+    int splits = 1;  // parts of the reduction
+    int groups = 1;  // products of the same shape: a[z], b[z]
 };
+
+// Where one of an epilogue's outputs goes: rows of ld elements, the first
+// `cols` columns stored (a multiple of 8); p null: nowhere.  add: to what is
+// there (fp32).
+struct Dest {
+    void *p;
+    int type;
+    int64_t ld;
+    int cols;
+    bool add;
+};
+
+__device__ __forceinline__ void store4(void *p, int type, int64_t at, f32x4 v) {
+    if (type == TW_T_F32) {
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(p) + at) = v;
+    } else {
+        u32x2 w{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p) + at) = w;
+    }
+}
+__device__ __forceinline__ f32x4 load4_bf16(const uint16_t *p, int64_t at) {
+    const u32x2 w = *reinterpret_cast<const u32x2 *>(p + at);
+    return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+}
 
 // 32 rows x 16 reduction elements of a kCols region (32 reduction rows of 128
 // columns, 256 bytes each, chunk c of row r at c ^ 4 (r % 4)): lane l receives
@@ -103,14 +129,17 @@ struct RingOperand {
     }
 };
 
-// An epilogue has a Row (what it keeps of one row m: row(m)) and
-//   quad(z, split, row, m, n, v, u)   takes the outputs n .. n + 3 of row m (u:
-//                                     those of the second weight matrix), or,
+// An epilogue has, for a row m of the tile, a Raw (what it loads: raw(m)) and a
+// Row made of it, and
+//   values(row, m, n, v, u, o)   makes its kOuts outputs of columns n .. n + 3 from
+//                                those of the product (u: of the second weights),
+//   dest(o, z, split)            says where output o goes, or,
 // where it reduces over the columns (kStats),
-//   most(row, n, v), add(row, n, v)   two passes over a lane's outputs,
+//   most(row, n, v), add(row, n, v)   two passes over a lane's columns,
 //   join<L>(row)                      lanes l and l ^ L hold one row,
 //   put(row, lds, w, r)               wave column w's part of the tile's row r,
-//   finish<W>(lds, r, m, cb)          joins the W wave columns.
+//   finish<W>(lds, r, m, cb)          joins W wave columns of 128 columns' block cb,
+//   whole(row, m, cb)                 a wave that holds all 128 columns.
 template <int LA, int LB, int NB, int SEG, class Epi>
 __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
     constexpr int NI = 1 + NB, STAGE = NI * kRingPart;
@@ -119,7 +148,7 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int l32 = lane & 31;
-    const int z = blockIdx.y, sp = blockIdx.z;
+    const int z = blockIdx.y, sp = blockIdx.z;  // product, part of the reduction
     int rb, cb;
     xcd_tile(blockIdx.x, (p.M + kRingBM - 1) / kRingBM, (p.N + kRingBN - 1) / kRingBN, rb, cb);
     const int m0 = rb * kRingBM, n0 = cb * kRingBN;
@@ -174,7 +203,7 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int m = m0 + wm * 64 + 32 * i + l32;
-        typename Epi::Row row = epi.row(min(m, p.M - 1));
+        typename Epi::Row row(epi, epi.raw(min(m, p.M - 1)));
         auto each = [&](auto f) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -192,9 +221,20 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
             each([&](int n, f32x4 v, f32x4) { epi.add(row, n, v); });
             epi.template join<32>(row);
             if (lane < 32) epi.put(row, smem, wn, wm * 64 + 32 * i + l32);
-        } else {
-            if (m < p.M)
-                each([&](int n, f32x4 v, f32x4 u) { epi.quad(z, sp, row, m, n, v, u); });
+        } else if (m < p.M) {
+            each([&](int n, f32x4 v, f32x4 u) {
+                f32x4 out[Epi::kOuts];
+                if (n >= epi.dest(0, z, sp).cols) return;
+                epi.values(row, m, n, v, u, out);
+#pragma unroll
+                for (int o = 0; o < Epi::kOuts; ++o) {
+                    const Dest d = epi.dest(o, z, sp);
+                    if (!d.p) continue;
+                    const int64_t at = m * d.ld + n;
+                    if (d.add) out[o] += *reinterpret_cast<f32x4 *>(static_cast<float *>(d.p) + at);
+                    store4(d.p, d.type, at, out[o]);
+                }
+            });
         }
     }
     if constexpr (Epi::kStats) {
@@ -204,7 +244,7 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
 }
 
 template <int LA, int LB, int NB, int SEG, class Epi>
-hipError_t launch_ring(const TileArgs &p, const Epi &epi, int groups, hipStream_t s) {
+hipError_t launch_ring(const TileArgs &p, const Epi &epi, hipStream_t s) {
     constexpr auto kernel = &ring_tiles_kernel<LA, LB, NB, SEG, Epi>;
     constexpr int lds = kRingS * (1 + NB) * kRingPart;
     const hipError_t e = lds_limit_once<kernel>(lds);
@@ -212,46 +252,481 @@ hipError_t launch_ring(const TileArgs &p, const Epi &epi, int groups, hipStream_
     const int64_t tiles = ((int64_t)p.M + kRingBM - 1) / kRingBM *
                           (((int64_t)p.N + kRingBN - 1) / kRingBN);
     if (tiles == 0) return hipSuccess;
-    kernel<<<dim3((unsigned)tiles, groups, p.splits), 512, lds, s>>>(p, epi);
+    kernel<<<dim3((unsigned)tiles, p.groups, p.splits), 512, lds, s>>>(p, epi);
     return hipGetLastError();
 }
 
-// ------------------------------- epilogues ----------------------------------
-__device__ __forceinline__ void store4(void *p, int type, int64_t at, f32x4 v) {
-    if (type == TW_T_F32) {
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(p) + at) = v;
-    } else {
-        u32x2 w{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p) + at) = w;
+// ----------------------------- 256 x 256 tiles ------------------------------
+// 256 x 256 outputs (NB = 2: 256 x 128 of each weight matrix) a workgroup of 8
+// waves, 64 x 128 outputs each (wave row wm, wave column wn); a workgroup a CU,
+// walking tiles, the next tile's first stages on their way while a tile is
+// written.  A stage is 64 reduction elements, 32 KB of each operand; two stages
+// fill 128 KB of LDS, and the loads of the stage after next enter a stage's slot in two
+// parts, as soon as no wave reads what they replace:
+//
+//   step   matrix instructions   fragments read              loads into this slot
+//   0      A x B0                B1 of this stage
+//   -- X: this stage's B2, B3 have landed; its A, B0, B1 are in registers
+//   1      A x B1                B2                          A, B0, B1
+//   2      A x B2                B3
+//   -- Y: the next stage's A, B0, B1 have landed; all of this one is in registers
+//   3      A x B3                A and B0 of the next stage  B2, B3
+//
+// with A the wave's 64 rows and B0 .. B3 its blocks of 32 columns.  A step is 16
+// matrix instructions of 16 x 16 x 32, so its reads are there when the next one
+// begins.
+//
+// A kRows operand lies in LDS as 256 rows of 128 bytes, chunk c of row r at c ^ ((r
+// >> 1) & 7): 16 consecutive rows of one chunk fall on 16 different bank groups.
+// A kCols operand is two regions of 64 reduction rows of 128 columns (256
+// bytes), read with the transposing ds_read_b64_tr_b16; chunk c of row r lies at c ^
+// 2 f(r), f = r % 4 + 4 (r / 8 % 2): the 8 rows that 32 lanes read, two
+// chunks of each, fill the 16 chunks of a row of banks once.  Loads of either
+// cover whole 128-byte lines.
+constexpr int kWideTile = 256, kWideK = 64;
+constexpr int kWideLine = 128;                    // bytes of a kRows row in a stage
+constexpr int kWidePart = 256 * kWideLine;        // one operand of a stage
+constexpr int kWideSlot = 2 * kWidePart;
+constexpr int kWideRegion = kWideK * 256;         // half of a kCols operand
+constexpr int kWideStage4K = 32 * kWideLine;      // a wave's outputs on their way to memory
+constexpr int kWideBytes = 2 * kWideSlot + 8 * kWideStage4K;
+constexpr int kWideGrid = 256;                    // workgroups: one a CU
+
+__device__ __forceinline__ int line_swz(int r) { return (r >> 1) & 7; }
+
+template <int LA, int LB, int NB, int SEG, class Epi>
+__global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_regions, Epi epi) {
+    static_assert(NB == 1 || (LB == kRows && SEG == 1), "two weight matrices: rows, one term");
+    constexpr int BN = kWideTile / NB;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int l16 = lane & 15;
+    const int KT = (p.R + kWideK - 1) / kWideK;  // stages of one term
+    const int all = SEG * KT, per = (all + p.splits - 1) / p.splits;
+    const int nbm = (p.M + kWideTile - 1) / kWideTile, nbn = (p.N + BN - 1) / BN;
+    const int tiles = nbm * nbn, items = tiles * p.groups * p.splits;
+
+    // The item being loaded: its tile, product, part of the reduction.
+    int m0, n0, z, sp, k0, kn;
+    rsrc_t ra[SEG], rb[SEG == 2 ? 2 : NB];  // (kRows)
+    // Lane's place in a load.  kRows: 8 rows of a group of 64, rows 8 wave ..+7,
+    // a chunk of 8 lanes each; kCols: 4 reduction rows of a region, rows 4 wave
+    // ..+3 of each half of 32, 16 chunks each.
+    const int lrow = 8 * wave + (lane >> 3);
+    const int chunk = (lane & 7) ^ line_swz(lrow);
+    const int crow = 4 * wave + (lane >> 4);
+    const int cchunk = (lane & 15) ^ (2 * ((crow & 3) | ((crow >> 3) & 1) << 2));
+    uint32_t va[2], vb[2];  // offsets; kCols: of the two regions
+    auto at_item = [&](int t) {
+        const int unit = t / tiles;
+        z = unit / p.splits;
+        sp = unit % p.splits;
+        k0 = min(sp * per, all);
+        kn = min(k0 + per, all) - k0;
+        int bm, bn;
+        if (row_regions == 8) xcd_tile<8>(t % tiles, nbm, nbn, bm, bn);
+        else if (row_regions == 4) xcd_tile<4>(t % tiles, nbm, nbn, bm, bn);
+        else xcd_tile<2>(t % tiles, nbm, nbn, bm, bn);
+        m0 = bm * kWideTile;
+        n0 = bn * BN;
+        const int pad = (p.R + 7) & ~7;  // a row's last piece may lie in its padding
+        if constexpr (LA == kRows) {
+            const int rows = min(kWideTile, p.M - m0);
+#pragma unroll
+            for (int g = 0; g < SEG; ++g)
+                ra[g] = make_rsrc((SEG == 2 ? p.a[g] : z == 0 ? p.a[0] : z == 1 ? p.a[1] : p.a[2]) +
+                                      m0 * p.lda,
+                                  ((uint64_t)(rows - 1) * p.lda + pad) * 2);
+            va[0] = (uint32_t)lrow * (uint32_t)p.lda * 2 + chunk * 16;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = 128 * q + 8 * cchunk;
+                va[q] = m0 + c < p.M ? (uint32_t)crow * (uint32_t)p.lda * 2 + c * 2 : kPastEnd;
+            }
+        }
+        if constexpr (LB == kRows) {
+            const int rows = min(BN, p.N - n0);
+#pragma unroll
+            for (int g = 0; g < (SEG == 2 ? 2 : NB); ++g)
+                rb[g] = make_rsrc((SEG == 2 || NB == 2 ? p.b[g]
+                                   : z == 0            ? p.b[0]
+                                   : z == 1            ? p.b[1]
+                                                       : p.b[2]) +
+                                      n0 * p.ldb,
+                                  ((uint64_t)(rows - 1) * p.ldb + pad) * 2);
+            vb[0] = (uint32_t)lrow * (uint32_t)p.ldb * 2 + chunk * 16;
+        } else {
+            // region q holds both wave columns' blocks 2 q and 2 q + 1
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int c = 64 * q + 8 * cchunk + (cchunk & 8 ? 64 : 0);
+                vb[q] = n0 + c < p.N ? (uint32_t)crow * (uint32_t)p.ldb * 2 + c * 2 : kPastEnd;
+            }
+        }
+    };
+    // descriptor of a kCols operand's stage kt (it moves with the stage: an
+    // operand may be larger than 32-bit offsets reach)
+    auto col_rsrc = [&](const uint16_t *base, int64_t ld, int kt, int i0, int I) {
+        const int rows = min(kWideK, p.R - kt * kWideK);
+        const int cols = (min(kWideTile, I - i0) + 7) & ~7;
+        return make_rsrc(base + (int64_t)kt * kWideK * ld + i0,
+                         ((uint64_t)(rows - 1) * ld + cols) * 2);
+    };
+    auto group_of = [&](const uint16_t *const *q, int kt) {
+        return SEG == 2 ? (kt >= KT ? q[1] : q[0]) : z == 0 ? q[0] : z == 1 ? q[1] : q[2];
+    };
+    auto load_a = [&](int i) {
+        const int kt = k0 + i, ks = SEG == 2 && kt >= KT ? kt - KT : kt;
+        char *slot = smem + (i & 1) * kWideSlot;
+        if constexpr (LA == kRows) {
+            const bool past = ks * kWideK + chunk * 8 >= p.R;
+            const uint32_t v64 = 64u * (uint32_t)p.lda * 2;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                dma16(SEG == 2 && kt >= KT ? ra[SEG - 1] : ra[0],
+                      past ? kPastEnd : va[0] + g * v64, ks * kWideLine,
+                      slot + (64 * g + 8 * wave) * kWideLine);
+        } else {
+            const rsrc_t d = col_rsrc(group_of(p.a, kt), p.lda, ks, m0, p.M);
+            const uint32_t v32 = 32u * (uint32_t)p.lda * 2;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    dma16(d, va[q] + h * v32, 0,
+                          slot + q * kWideRegion + (32 * h + 4 * wave) * 256);
+        }
+    };
+    // pair q of the column blocks: 0: B0, B1; 1: B2, B3.  kRows: groups of 64 rows;
+    // one matrix: 2 i + q, i the wave column, two: matrix q, its groups 2 q + i
+    auto load_b = [&](int i, int q) {
+        const int kt = k0 + i, ks = SEG == 2 && kt >= KT ? kt - KT : kt;
+        char *slot = smem + (i & 1) * kWideSlot + kWidePart;
+        if constexpr (LB == kRows) {
+            const bool past = ks * kWideK + chunk * 8 >= p.R;
+            const uint32_t v64 = 64u * (uint32_t)p.ldb * 2;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int g = NB == 1 ? 2 * w + q : 2 * q + w;
+                dma16(NB == 2 ? rb[NB == 2 ? q : 0] : SEG == 2 && kt >= KT ? rb[SEG - 1] : rb[0],
+                      past ? kPastEnd : vb[0] + (NB == 1 ? g : w) * v64, ks * kWideLine,
+                      slot + (64 * g + 8 * wave) * kWideLine);
+            }
+        } else {
+            const rsrc_t d = col_rsrc(group_of(p.b, kt), p.ldb, ks, n0, p.N);
+            const uint32_t v32 = 32u * (uint32_t)p.ldb * 2;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                dma16(d, vb[q] + h * v32, 0, slot + q * kWideRegion + (32 * h + 4 * wave) * 256);
+        }
+    };
+    constexpr int kAB = 6, kB = 2;  // loads of a wave in each part
+    auto load_ab = [&](int i) {
+        load_a(i);
+        load_b(i, 0);
+    };
+    auto load_first = [&] {
+        if (kn > 0) {
+            load_ab(0);
+            load_b(0, 1);
+        }
+        if (kn > 1) {
+            load_ab(1);
+            load_b(1, 1);
+        }
+    };
+    // Fragment of 16 rows (columns of the product's other operand) from `row` on,
+    // 32 reduction elements of sub-step s: lane l holds row l % 16, elements 32 s + 8
+    // (l / 16) ..+7.
+    auto read_rows = [&](const char *part, int row, int s) {
+        const int c = (4 * s + (lane >> 4)) ^ line_swz(l16);
+        return lds_ld16(part, (row + l16) * kWideLine + (c << 4));
+    };
+    // the same of a kCols region, its columns 8 c ..8 c + 15
+    const int fr = 8 * (lane >> 4) + (l16 >> 2);  // reduction row within a sub-step
+    const int fx = 2 * ((l16 >> 2) | ((lane >> 4) & 1) << 2);
+    const int fo = fr * 256 + (((l16 & 3) >> 1) << 4) + (l16 & 1) * 8;
+    auto read_cols = [&](const char *region, int c, int s) {
+        i16x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            v[h] = lds_tr16((const lds_i16x4 *)(region + fo + ((c ^ fx) << 4) + (32 * s + 4 * h) * 256));
+        const u32x2 lo = __builtin_bit_cast(u32x2, v[0]);
+        const u32x2 hi = __builtin_bit_cast(u32x2, v[1]);
+        return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    };
+    auto read_a = [&](int k, int i, int s) {  // 16 rows i of the wave's 64
+        const char *part = smem + (k & 1) * kWideSlot;
+        if constexpr (LA == kRows) return read_rows(part, wm * 64 + 16 * i, s);
+        else return read_cols(part + (wm >> 1) * kWideRegion, (wm & 1) * 8 + 2 * i, s);
+    };
+    u32x4 fa[2][4], fb[2][2][2];  // [sub-step][16 rows], [register set][sub-step][16 columns]
+    auto read_b = [&](int k, int j) {  // block j of 32 columns
+        const char *part = smem + (k & 1) * kWideSlot + kWidePart;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (LB == kRows)
+                    fb[j & 1][s][h] = read_rows(
+                        part, (NB == 1 ? wn * 128 + j * 32 : (j >> 1) * 128 + wn * 64 + (j & 1) * 32) +
+                                  16 * h, s);
+                else
+                    fb[j & 1][s][h] =
+                        read_cols(part + (j >> 1) * kWideRegion, wn * 8 + (j & 1) * 4 + 2 * h, s);
+            }
+    };
+    // [16 rows][16 columns]: register r of a block is row l16, column 4 (lane / 16) + r
+    f32x4 acc[4][8];
+    auto mma = [&](int j, int s, int i, int h) {
+        acc[i][2 * j + h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, fb[j & 1][s][h]), __builtin_bit_cast(bf16x8, fa[s][i]),
+            acc[i][2 * j + h], 0, 0, 0);
+    };
+    // The scheduling barriers keep each step's reads ahead of its matrix
+    // instructions.
+    auto step = [&](int k, int j) {
+        read_b(k, j + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) mma(j, s, i, h);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto last_step = [&](int k) {
+        read_b(k + 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mma(3, s, i, 0);
+                mma(3, s, i, 1);
+                __builtin_amdgcn_sched_barrier(0);
+                fa[s][i] = read_a(k + 1, i, s);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    };
+    // what the epilogue loads for the lane's rows, l16 of each 16
+    typename Epi::Raw raw[4], next[4];
+    auto load_raw = [&](typename Epi::Raw *r) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = epi.raw(min(m0 + wm * 64 + 16 * i + l16, p.M - 1));
+    };
+
+    at_item(blockIdx.x);
+    load_raw(raw);
+    load_first();
+    for (int t = blockIdx.x; t < items; t += gridDim.x) {
+        const int mt = m0, nt = n0, zt = z, st = sp, n = kn;  // m0, ... move on below
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{};
+        // What may be outstanding besides the loads below is younger (the last
+        // tile's stores), so these waits hold for at least the loads they name.
+        if (n > 0) {
+            if (n > 1) wait_vmcnt<kB + kAB + kB>();
+            else wait_vmcnt<kB>();
+            __builtin_amdgcn_s_barrier();
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fa[s][i] = read_a(0, i, s);
+            read_b(0, 0);
+            int k = 0;
+            for (; k + 2 < n; ++k) {
+                step(k, 0);
+                wait_vmcnt<kAB + kB>();
+                wait_lgkm0();
+                __builtin_amdgcn_s_barrier();  // X
+                load_ab(k + 2);
+                step(k, 1);
+                step(k, 2);
+                wait_vmcnt<kB + kAB>();
+                wait_lgkm0();
+                __builtin_amdgcn_s_barrier();  // Y
+                load_b(k + 2, 1);
+                last_step(k);
+            }
+            if (k + 1 < n) {
+                step(k, 0);
+                wait_vmcnt<kAB + kB>();
+                wait_lgkm0();
+                __builtin_amdgcn_s_barrier();
+                step(k, 1);
+                step(k, 2);
+                wait_vmcnt<kB>();
+                wait_lgkm0();
+                __builtin_amdgcn_s_barrier();
+                last_step(k);
+                ++k;
+            }
+            step(k, 0);
+            wait_vmcnt<0>();
+            __builtin_amdgcn_s_barrier();
+            step(k, 1);
+            step(k, 2);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) mma(3, s, i, h);
+        }
+
+        // The next tile's first loads (after every wave has read its last
+        // fragments) are on their way while this tile is written.
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        const bool more = t + (int)gridDim.x < items;
+        if (more) {
+            at_item(t + gridDim.x);
+            load_raw(next);
+            load_first();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+
+        // (The lane's number is read anew: the addresses below, computed ahead of
+        // the tile loop, would fill the registers that the k-loop needs.)
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int lr = ln & 15, lc = 4 * (ln >> 4);
+        const int mw = mt + wm * 64, nw = nt + wn * (BN / 2);  // the wave's outputs
+        if constexpr (Epi::kStats) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                typename Epi::Row row(epi, raw[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) epi.most(row, nw + 16 * j + lc, acc[i][j]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) epi.add(row, nw + 16 * j + lc, acc[i][j]);
+                epi.template join<16>(row);
+                epi.template join<32>(row);
+                const int m = mw + 16 * i + lr;
+                if (ln < 16 && m < p.M && nw < p.N) epi.whole(row, m, nw / 128);
+            }
+        } else {
+            // Outputs go through 4 KB of LDS a wave, 32 rows of 128 bytes at a
+            // time, so that they are stored in whole lines.
+            char *out = smem + 2 * kWideSlot + wave * kWideStage4K;
+            constexpr int JB = 8 / NB;  // the wave's blocks of 16 columns
+            auto write = [&](auto type) {
+                constexpr bool kF32 = decltype(type)::value == TW_T_F32;
+                constexpr int JP = kF32 ? 2 : 4;  // blocks in 128 bytes
+#pragma unroll
+                for (int i0 = 0; i0 < 4; i0 += 2)
+#pragma unroll
+                    for (int j0 = 0; j0 < JB; j0 += JP) {
+                        if (nw + 16 * j0 >= epi.dest(0, zt, st).cols) continue;
+                        f32x4 o[2][JP][Epi::kOuts];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            typename Epi::Row row(epi, raw[i0 + i]);
+                            const int m = min(mw + 16 * (i0 + i) + lr, p.M - 1);
+#pragma unroll
+                            for (int j = 0; j < JP; ++j)
+                                epi.values(row, m, nw + 16 * (j0 + j) + lc, acc[i0 + i][j0 + j],
+                                           acc[i0 + i][NB == 2 ? 4 + j0 + j : j0 + j], o[i][j]);
+                        }
+#pragma unroll
+                        for (int k = 0; k < Epi::kOuts; ++k) {
+                            const Dest d = epi.dest(k, zt, st);
+                            if (!d.p) continue;
+                            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int j = 0; j < JP; ++j) {
+                                    const int r = 16 * i + lr, byte = (16 * j + lc) * (kF32 ? 4 : 2);
+                                    store4(out + r * kWideLine + (((byte >> 4) ^ line_swz(r)) << 4) +
+                                               (byte & 15),
+                                           decltype(type)::value, 0, o[i][j][k]);
+                                }
+                            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int r = 8 * q + (ln >> 3), c = ln & 7;
+                                const u32x4 w = lds_ld16(out, r * kWideLine + ((c ^ line_swz(r)) << 4));
+                                const int m = mw + 16 * i0 + r;
+                                const int col = nw + 16 * j0 + c * (kF32 ? 4 : 8);
+                                if (m >= p.M || col >= d.cols) continue;
+                                char *to = static_cast<char *>(d.p) +
+                                           (m * d.ld + col) * (kF32 ? 4 : 2);
+                                if (kF32 && d.add) {
+                                    f32x4 *f = reinterpret_cast<f32x4 *>(to);
+                                    *f += __builtin_bit_cast(f32x4, w);
+                                } else {
+                                    st16(to, w);
+                                }
+                            }
+                            __builtin_amdgcn_wave_barrier();
+                        }
+                    }
+            };
+            if (epi.dest(0, zt, st).type == TW_T_F32) write(std::integral_constant<int, TW_T_F32>{});
+            else write(std::integral_constant<int, TW_T_BF16>{});
+        }
+        if (more) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = next[i];
+        }
     }
 }
-__device__ __forceinline__ f32x4 load4_bf16(const uint16_t *p, int64_t at) {
-    const u32x2 w = *reinterpret_cast<const u32x2 *>(p + at);
-    return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+
+template <int LA, int LB, int NB, int SEG, class Epi>
+hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
+    constexpr auto kernel = &wide_tiles_kernel<LA, LB, NB, SEG, Epi>;
+    const hipError_t e = lds_limit_once<kernel>(kWideBytes);
+    if (e != hipSuccess) return e;
+    const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
+    const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
+    const int64_t items = nbm * nbn * p.groups * p.splits;
+    if (items == 0) return hipSuccess;
+    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), 512, kWideBytes, s>>>(
+        p, wide_row_regions(nbm, nbn), epi);
+    return hipGetLastError();
 }
 
+// The larger tiles where their number leaves few CUs idle (to be measured).
+template <int LA, int LB, int NB, int SEG, class Epi>
+hipError_t launch_tiles(const TileArgs &p, const Epi &epi, hipStream_t s) {
+    const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
+    const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
+    if (nbm * nbn * p.groups * p.splits >= 128)
+        return launch_wide<LA, LB, NB, SEG>(p, epi, s);
+    return launch_ring<LA, LB, NB, SEG>(p, epi, s);
+}
+
+// ------------------------------- epilogues ----------------------------------
 // Outputs stored as they are: to out[z] in its type, or, where the reduction
 // is taken in parts, to part[split] in fp32 (added to what is there with
-// `more`: a later piece of the reduction).  ld is a multiple of 8, and N of 4.
+// `more`: a later piece of the reduction).
 struct EpiStore {
     static constexpr bool kStats = false;
+    static constexpr int kOuts = 1;
     void *out[3];
     int type;
     float *part;  // or null
     int more;
     int M, N;
-    struct Row {};
-    __device__ Row row(int) const { return {}; }
-    __device__ __forceinline__ void quad(int z, int split, Row &, int m, int n, f32x4 v,
-                                         f32x4) const {
-        if (n >= N) return;
-        const int64_t at = (int64_t)m * N + n;
-        if (part) {
-            f32x4 *q = reinterpret_cast<f32x4 *>(part + (int64_t)split * M * N + at);
-            *q = more ? *q + v : v;
-        } else {
-            store4(z == 0 ? out[0] : z == 1 ? out[1] : out[2], type, at, v);
-        }
+    struct Raw {};
+    struct Row {
+        __device__ Row(const EpiStore &, Raw) {}
+    };
+    __device__ Raw raw(int) const { return {}; }
+    __device__ __forceinline__ Dest dest(int, int z, int split) const {
+        if (part) return {part + (int64_t)split * M * N, TW_T_F32, N, N, more != 0};
+        return {z == 0 ? out[0] : z == 1 ? out[1] : out[2], type, N, N, false};
+    }
+    __device__ __forceinline__ void values(Row &, int, int, f32x4 v, f32x4, f32x4 *o) const {
+        o[0] = v;
     }
 };
 

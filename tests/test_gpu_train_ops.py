@@ -189,7 +189,9 @@ def test_rms_gradient_by_differences(tw):
 SHAPES = [(1, 8, 8), (1, 2048, 5632), (2, 136, 264), (3, 1024, 4096), (5, 1000, 2728), (8, 512, 1032),
           (16, 2048, 1024), (17, 264, 520), (32, 1024, 72), (64, 1016, 1000), (127, 128, 128),
           (128, 128, 256), (129, 136, 136), (200, 8, 1000), (300, 1000, 8), (777, 1000, 2728),
-          (1024, 1024, 1024), (2048, 520, 1096)]
+          (1024, 1024, 1024), (2048, 520, 1096),
+          # enough for the larger tiles: whole ones, and ragged in every size
+          (4096, 2048, 2048), (4100, 2056, 2104), (4104, 72, 4168), (520, 4104, 4104)]
 
 
 def weights(K, N, seed=0):
@@ -309,7 +311,8 @@ def test_ffn_gradient_by_differences(tw):
 # -------------------------------------------------------------- cross entropy --
 CE = [(1, 8, 1), (1, 64, 2), (1, 1024, 32768), (2, 136, 127), (4, 1024, 5000), (5, 72, 128), (16, 520, 129),
       (17, 64, 1000), (33, 256, 333), (64, 1000, 2049), (127, 128, 257), (129, 136, 4097),
-      (300, 520, 1000), (777, 256, 5003), (1025, 64, 2000)]
+      (300, 520, 1000), (777, 256, 5003), (1025, 64, 2000), (2048, 1024, 8192), (1029, 72, 9001),
+      (2100, 2056, 4099)]
 
 
 def ce_case(M, K, V, wide=True, seed=0):
