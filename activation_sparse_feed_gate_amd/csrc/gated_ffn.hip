@@ -14,6 +14,7 @@
 // Activations of the form g s(a(g)) with the logistic function s: SiLU has
 // a = g, the tanh form of GELU a = 2 sqrt(2 / pi) (g + 0.044715 g^3), since
 // (1 + tanh(v)) / 2 = s(2 v).  Their derivative is s + g s (1 - s) a'.
+#include "tw_few.hpp"
 #include "tw_tiles.hpp"
 #include "tw_train.hpp"
 
@@ -103,6 +104,69 @@ struct EpiDh {
     }
 };
 
+// Up to 16 token rows: a workgroup takes 16 C hidden neurons of both matrices, its 8
+// waves a slice of K each; their sums meet in LDS.
+constexpr int kFewUpThreads = 512;
+template <int ACT, int C>
+__global__ __launch_bounds__(kFewUpThreads) void few_up_kernel(
+    const uint16_t *__restrict__ x, int64_t x_stride, const uint16_t *__restrict__ wg_t,
+    const uint16_t *__restrict__ wu_t, int M, int K, int N, int share, uint16_t *__restrict__ g,
+    uint16_t *__restrict__ u, uint16_t *__restrict__ h) {
+    constexpr int NW = kFewUpThreads / kWave;
+    __shared__ __attribute__((aligned(16))) float sums[NW][2 * C][kWave][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n0 = blockIdx.x * share, n1 = min(n0 + share, N);
+    const int k8 = 8 * (lane >> 4);
+    const uint16_t *wp[2 * C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t row = min(n0 + 16 * c + (lane & 15), n1 - 1);
+        wp[2 * c] = wg_t + row * K + k8;
+        wp[2 * c + 1] = wu_t + row * K + k8;
+    }
+    const uint16_t *xp = x + min(lane & 15, M - 1) * x_stride + k8;
+    const int steps = (K + 31) / 32, per = (steps + NW - 1) / NW;
+    f32x4 acc[2 * C] = {};
+    few_product<2 * C, 4 / C>(wp, xp, K, wave * per, min(wave * per + per, steps), acc);
+#pragma unroll
+    for (int b = 0; b < 2 * C; ++b) *reinterpret_cast<f32x4 *>(sums[wave][b][lane]) = acc[b];
+    __syncthreads();
+    if (wave >= C) return;
+    f32x4 v{}, w{};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        v += *reinterpret_cast<const f32x4 *>(sums[i][2 * wave][lane]);
+        w += *reinterpret_cast<const f32x4 *>(sums[i][2 * wave + 1][lane]);
+    }
+    const int m = lane & 15;
+    if (m >= M) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int n = 16 * wave + 4 * (lane >> 4) + e;
+        if (n0 + n >= n1) continue;
+        const int64_t at = (int64_t)m * N + n0 + n;
+        h[at] = (uint16_t)pack_bf16(activate<ACT>(v[e]) * w[e], 0.0f);
+        if (g) g[at] = (uint16_t)pack_bf16(v[e], 0.0f);
+        if (u) u[at] = (uint16_t)pack_bf16(w[e], 0.0f);
+    }
+}
+
+template <int ACT>
+hipError_t few_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t, const uint16_t *wu_t,
+                  int M, int K, int N, uint16_t *g, uint16_t *u, uint16_t *h, hipStream_t s) {
+    // an even share of the neurons for each of 256 workgroups, at most 32
+    int share = (N + 255) / 256;
+    share = share < 4 ? 4 : share > 32 ? 32 : share;
+    const unsigned grid = (unsigned)((N + share - 1) / share);
+    if (share <= 16)
+        few_up_kernel<ACT, 1><<<grid, kFewUpThreads, 0, s>>>(x, x_stride, wg_t, wu_t, M, K, N,
+                                                             share, g, u, h);
+    else
+        few_up_kernel<ACT, 2><<<grid, kFewUpThreads, 0, s>>>(x, x_stride, wg_t, wu_t, M, K, N,
+                                                             share, g, u, h);
+    return hipGetLastError();
+}
+
 template <int ACT>
 hipError_t ffn_up(const TileArgs &p, uint16_t *g, uint16_t *u, uint16_t *h, hipStream_t s) {
     return launch_tiles<kRows, kRows, 2, 1>(p, EpiGlu<ACT>{h, g, u, p.N}, s);
@@ -115,12 +179,24 @@ hipError_t ffn_dh(const TileArgs &p, const uint16_t *g, const uint16_t *u, uint1
 
 }  // namespace
 
-size_t ffn_fwd_part_bytes(int, int, int) { return 0; }
-size_t ffn_bwd_part_bytes(int, int, int) { return 0; }
+size_t ffn_fwd_part_bytes(int M, int K, int N) {
+    if (M <= kFewRowsMax) return (size_t)few_down_splits(K, N) * M * K * 4;
+    return parts_bytes<kRows, kCols, 1, 1>(TileArgs{{}, {}, N, K, M, K, N});
+}
+size_t ffn_bwd_part_bytes(int M, int K, int N) {
+    return parts_bytes<kRows, kCols, 1, 2>(TileArgs{{}, {}, N, K, M, K, N});
+}
 
 hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
                          const uint16_t *wu_t, int act, int M, int K, int N, uint16_t *g,
-                         uint16_t *u, uint16_t *h, float *, hipStream_t s) {
+                         uint16_t *u, uint16_t *h, hipStream_t s) {
+    if (M <= kFewRowsMax) {
+        if (act == TW_A_RELU)
+            return few_up<TW_A_RELU>(x, x_stride, wg_t, wu_t, M, K, N, g, u, h, s);
+        if (act == TW_A_SILU)
+            return few_up<TW_A_SILU>(x, x_stride, wg_t, wu_t, M, K, N, g, u, h, s);
+        return few_up<TW_A_GELU>(x, x_stride, wg_t, wu_t, M, K, N, g, u, h, s);
+    }
     const TileArgs p{{x}, {wg_t, wu_t}, x_stride, K, M, N, K};
     if (act == TW_A_RELU) return ffn_up<TW_A_RELU>(p, g, u, h, s);
     if (act == TW_A_SILU) return ffn_up<TW_A_SILU>(p, g, u, h, s);
@@ -128,9 +204,13 @@ hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg
 }
 
 hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, int N, void *y,
-                           int y_type, float *, hipStream_t s) {
-    const TileArgs p{{h}, {wd}, N, K, M, K, N};
-    return launch_tiles<kRows, kCols, 1, 1>(p, EpiStore{{y}, y_type, nullptr, 0, M, K}, s);
+                           int y_type, float *part, hipStream_t s) {
+    if (M <= kFewRowsMax) {
+        const hipError_t e = launch_few_down(h, wd, M, K, N, part, s);
+        if (e != hipSuccess) return e;
+        return launch_sum_parts(part, few_down_splits(K, N), (int64_t)M * K, y, y_type, s);
+    }
+    return launch_split<kRows, kCols, 1, 1>(TileArgs{{h}, {wd}, N, K, M, K, N}, y, y_type, part, s);
 }
 
 hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const uint16_t *g,
@@ -144,22 +224,19 @@ hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const 
 
 hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t *wg_t,
                          const uint16_t *wu_t, int M, int K, int N, void *dx, int dx_type,
-                         float *, hipStream_t s) {
-    const TileArgs p{{dz, du}, {wg_t, wu_t}, N, K, M, K, N};
-    return launch_tiles<kRows, kCols, 1, 2>(p, EpiStore{{dx}, dx_type, nullptr, 0, M, K}, s);
+                         float *part, hipStream_t s) {
+    return launch_split<kRows, kCols, 1, 2>(TileArgs{{dz, du}, {wg_t, wu_t}, N, K, M, K, N}, dx,
+                                            dx_type, part, s);
 }
 
 hipError_t launch_ffn_dw(const uint16_t *dz, const uint16_t *du, const uint16_t *h,
                          const uint16_t *x, int64_t x_stride, const uint16_t *dy, int M, int K,
-                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, float *,
-                         hipStream_t s) {
-    // W_g and W_u share x; dy, of another stride, is W_d's
-    const TileArgs p{{dz, du}, {x, x}, N, x_stride, N, K, M, 1, 2};
-    hipError_t e = launch_tiles<kCols, kCols, 1, 1>(
-        p, EpiStore{{dwg_t, dwu_t}, dw_type, nullptr, 0, N, K}, s);
-    if (e != hipSuccess) return e;
-    const TileArgs q{{h}, {dy}, N, K, N, K, M};
-    return launch_tiles<kCols, kCols, 1, 1>(q, EpiStore{{dwd}, dw_type, nullptr, 0, N, K}, s);
+                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, hipStream_t s) {
+    TileArgs p{{dz, du, h}, {x, x, dy}, N, x_stride, N, K, M};
+    p.groups = 3;
+    p.ldb_last = K;
+    return launch_tiles<kCols, kCols, 1, 1>(
+        p, EpiStore{{dwg_t, dwu_t, dwd}, dw_type, nullptr, 0, N, K}, s);
 }
 
 }  // namespace tw

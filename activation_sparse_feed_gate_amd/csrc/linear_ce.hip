@@ -13,6 +13,7 @@
 //
 // A row whose target is outside [0, V) is left out: its loss and its row of D
 // are 0.
+#include "tw_few.hpp"
 #include "tw_tiles.hpp"
 #include "tw_train.hpp"
 
@@ -84,6 +85,40 @@ struct EpiSoft {
         part[(int64_t)cb * M + m] = {r.top, r.sum};
     }
 };
+
+// Up to 16 token rows: a wave takes 32 words and all of K, a workgroup of 4 waves
+// the 128 of a column block.
+constexpr int kFewSoftThreads = 256;
+__global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
+    const uint16_t *__restrict__ x, int64_t x_stride, const uint16_t *__restrict__ w, int M, int K,
+    int V, Soft *__restrict__ part) {
+    __shared__ Soft all[kFewSoftThreads / kWave][16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int v0 = blockIdx.x * 128 + 32 * wave;
+    const int k8 = 8 * (lane >> 4);
+    const uint16_t *wp[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+        wp[b] = w + (int64_t)min(v0 + 16 * b + (lane & 15), V - 1) * K + k8;
+    const uint16_t *xp = x + min(lane & 15, M - 1) * x_stride + k8;
+    f32x4 acc[2] = {};
+    few_product<2, 6>(wp, xp, K, 0, (K + 31) / 32, acc);
+    const EpiSoft epi{part, M, V};
+    EpiSoft::Row row(epi, {});
+#pragma unroll
+    for (int b = 0; b < 2; ++b) epi.most(row, v0 + 16 * b + 4 * (lane >> 4), acc[b]);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) epi.add(row, v0 + 16 * b + 4 * (lane >> 4), acc[b]);
+    epi.join<16>(row);
+    epi.join<32>(row);
+    if (lane < 16) all[wave][lane] = {row.top, row.sum};
+    __syncthreads();
+    if (threadIdx.x >= M) return;
+    Soft j = all[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < kFewSoftThreads / kWave; ++i) j = join_soft(j, all[i][threadIdx.x]);
+    part[(int64_t)blockIdx.x * M + threadIdx.x] = j;
+}
 
 // Joins the column blocks of a row and takes the target's logit: 16 threads a
 // row.
@@ -172,7 +207,8 @@ struct EpiD {
 
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The backward pass's pieces of the vocabulary: columns of D in at most 256 MB.
+// The backward pass's pieces of the vocabulary: columns of D in at most 256 MB,
+// and the parts of dx's reduction, which every piece adds to.
 struct Pieces {
     int width;
     size_t d_bytes, part_bytes;
@@ -183,8 +219,8 @@ Pieces pieces_of(int M, int K, int V) {
     const int64_t most = (int64_t)(256 << 20) / 2 / (M > 0 ? M : 1) / 256 * 256;
     p.width = (int)(most < 256 ? 256 : most < V ? most : V);
     p.d_bytes = up256((size_t)M * ((p.width + 7) / 8 * 8) * 2);
-    p.splits = 1;
-    p.part_bytes = p.width < V ? up256((size_t)M * K * 4) : 0;
+    p.splits = splits_of<kRows, kCols, 1, 1>(TileArgs{{}, {}, 0, 0, M, K, p.width});
+    p.part_bytes = p.width < V || p.splits > 1 ? up256((size_t)p.splits * M * K * 4) : 0;
     return p;
 }
 
@@ -199,7 +235,13 @@ hipError_t launch_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w,
     if (M == 0) return hipSuccess;
     const TileArgs p{{x}, {w}, x_stride, K, M, V, K};
     Soft *part = static_cast<Soft *>(ws);
-    hipError_t e = launch_tiles<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, s);
+    hipError_t e;
+    if (M <= kFewRowsMax) {
+        few_soft_kernel<<<(V + 127) / 128, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
+        e = hipGetLastError();
+    } else {
+        e = launch_tiles<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, s);
+    }
     if (e != hipSuccess) return e;
     ce_rows_kernel<<<(M + 15) / 16, 256, 0, s>>>(part, (V + 127) / 128, x, x_stride, w,
                                                  t, M, K, V, loss, lse);
@@ -226,7 +268,7 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
             e = launch_tiles<kRows, kRows, 1, 1>(TileArgs{{x}, {wp}, x_stride, K, M, N, K},
                                                  EpiD{lse, dloss, t, d, ldd, N, first, V}, s);
         if (e == hipSuccess && dx)
-            e = launch_tiles<kRows, kCols, 1, 1>(TileArgs{{d}, {wp}, ldd, K, M, K, N},
+            e = launch_tiles<kRows, kCols, 1, 1>(TileArgs{{d}, {wp}, ldd, K, M, K, N, pc.splits},
                                                  EpiStore{{dx}, dx_type, part, first > 0, M, K}, s);
         if (e == hipSuccess && dw) {
             char *out = static_cast<char *>(dw) + (int64_t)first * K * (dw_type == TW_T_F32 ? 4 : 2);
@@ -234,7 +276,7 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
                                                  EpiStore{{out}, dw_type, nullptr, 0, N, K}, s);
         }
     }
-    if (e == hipSuccess && dx && part) e = launch_sum_parts(part, 1, (int64_t)M * K, dx, dx_type, s);
+    if (e == hipSuccess && dx && part) e = launch_sum_parts(part, pc.splits, (int64_t)M * K, dx, dx_type, s);
     return e;
 }
 

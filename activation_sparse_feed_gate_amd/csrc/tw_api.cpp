@@ -1181,7 +1181,7 @@ tw_status tw_gated_ffn_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *
     }
     uint16_t *h = static_cast<uint16_t *>(ws);
     float *part = reinterpret_cast<float *>(static_cast<char *>(ws) + act_bytes(M, N));
-    TW_TRY(launched(tw::launch_ffn_up(x, x_stride, wg_t, wu_t, act, M, K, N, g, u, h, part, s),
+    TW_TRY(launched(tw::launch_ffn_up(x, x_stride, wg_t, wu_t, act, M, K, N, g, u, h, s),
                     "gate and up launch"));
     TW_TRY(record(events, 1, s));
     TW_TRY(launched(tw::launch_ffn_down(h, wd, M, K, N, y, y_type, part, s), "down launch"));
@@ -1233,7 +1233,7 @@ tw_status tw_gated_ffn_bwd(const uint16_t *dy, const uint16_t *x, int64_t x_stri
     TW_TRY(record(events, 2, s));
     if (dwg_t)
         TW_TRY(launched(tw::launch_ffn_dw(dz, du, h, x, x_stride, dy, M, K, N, dwg_t, dwu_t, dwd,
-                                          dw_type, part, s),
+                                          dw_type, s),
                         "weight-gradient launch"));
     return record(events, 3, s);
 }

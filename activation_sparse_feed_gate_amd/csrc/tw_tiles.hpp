@@ -32,6 +32,7 @@ struct TileArgs {
     int M, N, R;
     int splits = 1;  // parts of the reduction
     int groups = 1;  // products of the same shape: a[z], b[z]
+    int64_t ldb_last = 0;  // ldb of the third product
 };
 
 // Where one of an epilogue's outputs goes: rows of ld elements, the first
@@ -152,12 +153,13 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
     int rb, cb;
     xcd_tile(blockIdx.x, (p.M + kRingBM - 1) / kRingBM, (p.N + kRingBN - 1) / kRingBN, rb, cb);
     const int m0 = rb * kRingBM, n0 = cb * kRingBN;
+    const int64_t ldb = z == 2 ? p.ldb_last : p.ldb;
     const int KT = (p.R + kPK - 1) / kPK;
 
     const RingOperand<LA> a0(p.a[SEG == 2 ? 0 : z], p.lda, p.M, p.R, m0, wave, lane);
-    const RingOperand<LB> b0(p.b[SEG == 2 || NB == 2 ? 0 : z], p.ldb, p.N, p.R, n0, wave, lane);
+    const RingOperand<LB> b0(p.b[SEG == 2 || NB == 2 ? 0 : z], ldb, p.N, p.R, n0, wave, lane);
     const RingOperand<LA> a1(SEG == 2 ? p.a[1] : p.a[0], p.lda, p.M, p.R, m0, wave, lane);
-    const RingOperand<LB> b1(SEG == 2 || NB == 2 ? p.b[1] : p.b[0], p.ldb, p.N, p.R, n0, wave, lane);
+    const RingOperand<LB> b1(SEG == 2 || NB == 2 ? p.b[1] : p.b[0], ldb, p.N, p.R, n0, wave, lane);
     auto issue = [&](int kt, char *st) {
         char *d = st + wave * 1024;
         if (SEG == 2 && kt >= KT) {
@@ -310,6 +312,7 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
 
     // The item being loaded: its tile, product, part of the reduction.
     int m0, n0, z, sp, k0, kn;
+    int64_t ldb;
     rsrc_t ra[SEG], rb[SEG == 2 ? 2 : NB];  // (kRows)
     // Lane's place in a load.  kRows: 8 rows of a group of 64, rows 8 wave ..+7,
     // a chunk of 8 lanes each; kCols: 4 reduction rows of a region, rows 4 wave
@@ -323,6 +326,7 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
         const int unit = t / tiles;
         z = unit / p.splits;
         sp = unit % p.splits;
+        ldb = z == 2 ? p.ldb_last : p.ldb;
         k0 = min(sp * per, all);
         kn = min(k0 + per, all) - k0;
         int bm, bn;
@@ -355,15 +359,15 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
                                    : z == 0            ? p.b[0]
                                    : z == 1            ? p.b[1]
                                                        : p.b[2]) +
-                                      n0 * p.ldb,
-                                  ((uint64_t)(rows - 1) * p.ldb + pad) * 2);
-            vb[0] = (uint32_t)lrow * (uint32_t)p.ldb * 2 + chunk * 16;
+                                      n0 * ldb,
+                                  ((uint64_t)(rows - 1) * ldb + pad) * 2);
+            vb[0] = (uint32_t)lrow * (uint32_t)ldb * 2 + chunk * 16;
         } else {
             // region q holds both wave columns' blocks 2 q and 2 q + 1
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int c = 64 * q + 8 * cchunk + (cchunk & 8 ? 64 : 0);
-                vb[q] = n0 + c < p.N ? (uint32_t)crow * (uint32_t)p.ldb * 2 + c * 2 : kPastEnd;
+                vb[q] = n0 + c < p.N ? (uint32_t)crow * (uint32_t)ldb * 2 + c * 2 : kPastEnd;
             }
         }
     };
@@ -407,7 +411,7 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
         char *slot = smem + (i & 1) * kWideSlot + kWidePart;
         if constexpr (LB == kRows) {
             const bool past = ks * kWideK + chunk * 8 >= p.R;
-            const uint32_t v64 = 64u * (uint32_t)p.ldb * 2;
+            const uint32_t v64 = 64u * (uint32_t)ldb * 2;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 const int g = NB == 1 ? 2 * w + q : 2 * q + w;
@@ -416,8 +420,8 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
                       slot + (64 * g + 8 * wave) * kWideLine);
             }
         } else {
-            const rsrc_t d = col_rsrc(group_of(p.b, kt), p.ldb, ks, n0, p.N);
-            const uint32_t v32 = 32u * (uint32_t)p.ldb * 2;
+            const rsrc_t d = col_rsrc(group_of(p.b, kt), ldb, ks, n0, p.N);
+            const uint32_t v32 = 32u * (uint32_t)ldb * 2;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
                 dma16(d, vb[q] + h * v32, 0, slot + q * kWideRegion + (32 * h + 4 * wave) * 256);
@@ -695,12 +699,15 @@ hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
 }
 
 // The larger tiles where their number leaves few CUs idle (to be measured).
-template <int LA, int LB, int NB, int SEG, class Epi>
-hipError_t launch_tiles(const TileArgs &p, const Epi &epi, hipStream_t s) {
+template <int LA, int LB, int NB, int SEG>
+bool use_wide(const TileArgs &p) {
     const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
     const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
-    if (nbm * nbn * p.groups * p.splits >= 128)
-        return launch_wide<LA, LB, NB, SEG>(p, epi, s);
+    return nbm * nbn * p.groups * p.splits >= 128;
+}
+template <int LA, int LB, int NB, int SEG, class Epi>
+hipError_t launch_tiles(const TileArgs &p, const Epi &epi, hipStream_t s) {
+    if (use_wide<LA, LB, NB, SEG>(p)) return launch_wide<LA, LB, NB, SEG>(p, epi, s);
     return launch_ring<LA, LB, NB, SEG>(p, epi, s);
 }
 
@@ -747,6 +754,45 @@ inline hipError_t launch_sum_parts(const float *part, int splits, int64_t n, voi
     if (type == TW_T_F32) sum_parts_kernel<TW_T_F32><<<grid, 256, 0, s>>>(part, splits, n, out);
     else sum_parts_kernel<TW_T_BF16><<<grid, 256, 0, s>>>(part, splits, n, out);
     return hipGetLastError();
+}
+
+// Parts of the reduction for a product of few output tiles, so that its work
+// fills the chip: the number (up to 8) with the least estimated time, from the rounds
+// of the larger tiles, 1.5 us a stage, and the parts' way through memory (8 bytes
+// an output and part at 4.5 TB/s).
+template <int LA, int LB, int NB, int SEG>
+int splits_of(const TileArgs &p) {
+    const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
+    const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
+    const int64_t stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 8 && s <= stages; ++s) {
+        const int64_t rounds = (nbm * nbn * p.groups * s + kWideGrid - 1) / kWideGrid;
+        const double us = 1.5 * rounds * ((stages + s - 1) / s) +
+                          (s > 1 ? 3.0 + (double)s * p.M * p.N * p.groups * 8 / 4.5e6 : 0.0);
+        if (s == 1 || us < least) {
+            best = s;
+            least = us;
+        }
+    }
+    return best;
+}
+template <int LA, int LB, int NB, int SEG>
+size_t parts_bytes(const TileArgs &p) {
+    const int s = splits_of<LA, LB, NB, SEG>(p);
+    return s > 1 ? (size_t)s * p.M * p.N * 4 : 0;
+}
+
+// A product stored as it is, its reduction in parts where that is faster; part:
+// parts_bytes.
+template <int LA, int LB, int NB, int SEG>
+hipError_t launch_split(TileArgs p, void *out, int type, float *part, hipStream_t s) {
+    p.splits = splits_of<LA, LB, NB, SEG>(p);
+    const EpiStore epi{{out}, type, p.splits > 1 ? part : nullptr, 0, p.M, p.N};
+    const hipError_t e = launch_tiles<LA, LB, NB, SEG>(p, epi, s);
+    if (e != hipSuccess || p.splits == 1) return e;
+    return launch_sum_parts(part, p.splits, (int64_t)p.M * p.N, out, type, s);
 }
 
 }  // namespace tw

@@ -29,13 +29,13 @@ hipError_t launch_rmsnorm_bwd(const void *dy, int dy_type, const void *x, int x_
 enum { TW_A_RELU = 0, TW_A_SILU = 1, TW_A_GELU = 2 };
 
 // The gated FFN (gated_ffn.hip).  h: [M][N] bf16 scratch, part: scratch of
-// ffn_part_bytes.  g and u (the projections before the activation) are
-// optional outputs.
+// ffn_fwd_part_bytes (down) or ffn_bwd_part_bytes (dx).  g and u (the
+// projections before the activation) are optional outputs.
 size_t ffn_fwd_part_bytes(int M, int K, int N);
 size_t ffn_bwd_part_bytes(int M, int K, int N);
 hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
                          const uint16_t *wu_t, int act, int M, int K, int N, uint16_t *g,
-                         uint16_t *u, uint16_t *h, float *part, hipStream_t s);
+                         uint16_t *u, uint16_t *h, hipStream_t s);
 hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, int N, void *y,
                            int y_type, float *part, hipStream_t s);
 // dz, du, h: [M][N] bf16 each.
@@ -47,8 +47,7 @@ hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t 
                          float *part, hipStream_t s);
 hipError_t launch_ffn_dw(const uint16_t *dz, const uint16_t *du, const uint16_t *h,
                          const uint16_t *x, int64_t x_stride, const uint16_t *dy, int M, int K,
-                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, float *part,
-                         hipStream_t s);
+                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, hipStream_t s);
 
 // Cross entropy of x w^T (linear_ce.hip).  Targets are 32- or 64-bit integers;
 // one outside [0, V) leaves its row out.

@@ -56,12 +56,14 @@ _lib = ctypes.CDLL(LIBRARY)
 try:
     from . import _tw_calls as _calls  # built beside the library
 except ImportError as _e:
-    warnings.warn(f"the native part of the binding does not load ({_e}): the layer norm and int8 "
-                  "calls take more host time each; build it with "
+    warnings.warn(f"the native part of the binding does not load ({_e}): the allocating calls "
+                  "take more host time each; build it with "
                   "`python -m activation_sparse_feed_gate_amd.build`", RuntimeWarning, stacklevel=2)
 
     class _calls:  # noqa: N801
         layernorm = layernorm_backward = quant_linear = quant_gateup = staticmethod(lambda *a: None)
+        rmsnorm = rmsnorm_quantize = rmsnorm_backward = layernorm
+        gated_ffn = gated_ffn_backward = linear_ce = linear_ce_backward = clip_grads = layernorm
 
 
 _vp = ctypes.c_void_p
@@ -1258,6 +1260,9 @@ def quant_gateup(x, wg, g_scale, wu, u_scale, gamma=None, beta=None, eps=1e-5, x
 def rmsnorm(x, gamma, eps=1e-5, add=None, out_dtype=torch.bfloat16):
     """RMS norm of the rows of x (+ add).  Returns a dict: y, rstd (fp32, for
     ``rmsnorm_backward``), and sum = x + add in x's type (None without add)."""
+    got = _calls.rmsnorm(x, gamma, eps, add, out_dtype)
+    if got is not None:
+        return got
     M, K = _dims2(x, "x", "rmsnorm")
     dev = x.device
     out = {
@@ -1273,6 +1278,9 @@ def rmsnorm_backward(dy, x, gamma, rstd, dres=None, dx_dtype=torch.float32):
     """Gradient of ``rmsnorm``: x is its input (``sum`` if there was an add),
     dres the gradient reaching x past the norm (dx's dtype).  Returns a dict
     with dx, dgamma."""
+    got = _calls.rmsnorm_backward(dy, x, gamma, rstd, dres, dx_dtype)
+    if got is not None:
+        return got
     M, K = _dims2(x, "x", "rmsnorm_backward")
     dev = x.device
     out = {
@@ -1287,6 +1295,9 @@ def rmsnorm_backward(dy, x, gamma, rstd, dres=None, dx_dtype=torch.float32):
 def rmsnorm_quantize(x, gamma, eps=1e-5, add=None):
     """The RMS norm of x (+ add) in int8.  Returns a dict: q, scale, and
     sum = x + add in x's type (None without add)."""
+    got = _calls.rmsnorm_quantize(x, gamma, eps, add)
+    if got is not None:
+        return got
     M, K = _dims2(x, "x", "rmsnorm_quantize")
     out = {
         "q": torch.empty((M, K), dtype=_I8, device=x.device),
@@ -1305,6 +1316,9 @@ def gated_ffn(x, wg_t, wu_t, wd, act="silu", keep=False, out_dtype=torch.bfloat1
     """The dense gated FFN (act(x W_g) * (x W_u)) W_d, act "relu", "silu" or
     "gelu".  Returns a dict: y, and with ``keep`` g and u (what
     ``gated_ffn_backward`` reads; None without)."""
+    got = _calls.gated_ffn(x, wg_t, wu_t, wd, act, keep, out_dtype, ws)
+    if got is not None:
+        return got
     M, K = _dims2(x, "x", "gated_ffn")
     N = _dims2(wg_t, "wg_t", "gated_ffn")[0]
     dev = x.device
@@ -1322,6 +1336,9 @@ def gated_ffn_backward(dy, x, wg_t, wu_t, wd, g, u, act="silu", dx_dtype=torch.b
                        dw_dtype=torch.bfloat16, ws=None):
     """Gradient of ``gated_ffn`` from its g and u.  Returns a dict: dx, dwg_t,
     dwu_t, dwd."""
+    got = _calls.gated_ffn_backward(dy, x, wg_t, wu_t, wd, g, u, act, dx_dtype, dw_dtype, ws)
+    if got is not None:
+        return got
     M, K = _dims2(x, "x", "gated_ffn_backward")
     N = _dims2(wg_t, "wg_t", "gated_ffn_backward")[0]
     dev = x.device
@@ -1337,6 +1354,9 @@ def linear_ce(x, w, target, ws=None):
     """Cross entropy of the logits x w^T against one target a row (w: [V][K];
     a target outside [0, V) leaves its row out).  Returns a dict: loss and lse
     (log-sum-exp) of every row, fp32."""
+    got = _calls.linear_ce(x, w, target, ws)
+    if got is not None:
+        return got
     M, K = _dims2(x, "x", "linear_ce")
     V = _dims2(w, "w", "linear_ce")[0]
     out = {k: torch.empty((M,), dtype=_F32, device=x.device) for k in ("loss", "lse")}
@@ -1349,6 +1369,9 @@ def linear_ce_backward(dloss, x, w, target, lse, dx_dtype=torch.bfloat16, dw_dty
                        ws=None):
     """Gradient of ``linear_ce`` for dloss (fp32, one a row).  Returns a dict:
     dx, dw."""
+    got = _calls.linear_ce_backward(dloss, x, w, target, lse, dx_dtype, dw_dtype, ws)
+    if got is not None:
+        return got
     M, K = _dims2(x, "x", "linear_ce_backward")
     V = _dims2(w, "w", "linear_ce_backward")[0]
     out = {"dx": torch.empty((M, K), dtype=dx_dtype, device=x.device),
@@ -1381,6 +1404,9 @@ def clip_grads(grads, max_norm, eps=1e-6, out=None):
     """Scales the gradients by min(1, max_norm / (norm + eps)), in place or
     into ``out`` (a list of tensors of the same shapes, bf16 or fp32).  Returns the
     norm before, a scalar tensor."""
+    got = _calls.clip_grads(grads, max_norm, eps, out)
+    if got is not None:
+        return got
     grads = _grads(grads, "clip_grads")
     dev = grads[0].device
     norm = torch.empty((), dtype=_F32, device=dev)

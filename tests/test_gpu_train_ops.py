@@ -580,6 +580,32 @@ def test_repeatable_and_on_another_stream(tw, name):
 
 
 @pytest.mark.parametrize("name", NAMES)
+def test_native_call_equals_the_checked_one(tw, name, monkeypatch):
+    """The native part of the binding takes the call, and the checked Python way
+    gives the same bits."""
+    f = all_calls(tw)[name]
+    native, taken = tw._calls, []
+
+    class Spy:
+        def __getattr__(self, k):
+            def run(*a):
+                got = getattr(native, k)(*a)
+                taken.append((k, got is not None))
+                return got
+            return run
+
+    class Never:
+        def __getattr__(self, k):
+            return lambda *a: None
+
+    monkeypatch.setattr(tw, "_calls", Spy())
+    first = copied(f())
+    assert taken and all(ok for _, ok in taken), taken
+    monkeypatch.setattr(tw, "_calls", Never())
+    same(first, f())
+
+
+@pytest.mark.parametrize("name", NAMES)
 def test_captured_and_replayed(tw, name):
     f = all_calls(tw)[name]
     first = copied(f())
