@@ -59,7 +59,7 @@ struct EpiGlu {
     static constexpr int kOuts = 3;
     uint16_t *h, *g, *u;  // g, u or null
     int N;
-    struct Raw {};
+    typedef NoRaw Raw;
     struct Row {
         __device__ Row(const EpiGlu &, Raw) {}
     };
@@ -67,11 +67,15 @@ struct EpiGlu {
     __device__ __forceinline__ Dest dest(int o, int, int) const {
         return {o == 0 ? h : o == 1 ? g : u, TW_T_BF16, N, N, false};
     }
-    __device__ __forceinline__ void values(Row &, int, int, f32x4 v, f32x4 w, f32x4 *o) const {
+    template <int W>
+    __device__ __forceinline__ void values(Row &, int, int, const float (&v)[W],
+                                           const float (&w)[W], float (&o)[kOuts][W]) const {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[0][e] = activate<ACT>(v[e]) * w[e];
-        o[1] = v;
-        o[2] = w;
+        for (int e = 0; e < W; ++e) {
+            o[0][e] = activate<ACT>(v[e]) * w[e];
+            o[1][e] = v[e];
+            o[2][e] = w[e];
+        }
     }
 };
 
@@ -83,7 +87,7 @@ struct EpiDh {
     const uint16_t *g, *u;
     uint16_t *dz, *du, *h;
     int N;
-    struct Raw {};
+    typedef NoRaw Raw;
     struct Row {
         __device__ Row(const EpiDh &, Raw) {}
     };
@@ -91,11 +95,14 @@ struct EpiDh {
     __device__ __forceinline__ Dest dest(int o, int, int) const {
         return {o == 0 ? dz : o == 1 ? du : h, TW_T_BF16, N, N, false};
     }
-    __device__ __forceinline__ void values(Row &, int m, int n, f32x4 v, f32x4, f32x4 *o) const {
-        const int64_t at = (int64_t)m * N + min(n, N - 4);
-        const f32x4 gv = load4_bf16(g, at), uv = load4_bf16(u, at);
+    template <int W>
+    __device__ __forceinline__ void values(Row &, int m, int n, const float (&v)[W],
+                                           const float (&)[W], float (&o)[kOuts][W]) const {
+        float gv[W], uv[W];
+        load_bf16<W>(g + (int64_t)m * N + n, gv);
+        load_bf16<W>(u + (int64_t)m * N + n, uv);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < W; ++e) {
             const Slope a = activate_slope<ACT>(gv[e]);
             o[0][e] = v[e] * uv[e] * a.slope;
             o[1][e] = v[e] * a.value;

@@ -45,21 +45,23 @@ struct EpiSoft {
     static constexpr bool kStats = true;
     Soft *part;  // [column blocks][M]
     int M, N;
-    struct Raw {};
+    typedef NoRaw Raw;
     struct Row {
         float most = -INFINITY, top = 0.0f, sum = 0.0f;
         __device__ Row(const EpiSoft &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
-    __device__ __forceinline__ void most(Row &r, int n, f32x4 v) const {
+    template <int W>
+    __device__ __forceinline__ void most(Row &r, int n, const float (&v)[W]) const {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < W; ++e)
             if (n + e < N) r.most = fmaxf(r.most, v[e]);
     }
-    __device__ __forceinline__ void add(Row &r, int n, f32x4 v) const {
+    template <int W>
+    __device__ __forceinline__ void add(Row &r, int n, const float (&v)[W]) const {
         r.top = r.most == -INFINITY ? 0.0f : r.most * kLog2e;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < W; ++e)
             if (n + e < N) r.sum += __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
     }
     template <int L>
@@ -105,10 +107,15 @@ __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
     few_product<2, 6>(wp, xp, K, 0, (K + 31) / 32, acc);
     const EpiSoft epi{part, M, V};
     EpiSoft::Row row(epi, {});
+    float l[2][4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) epi.most(row, v0 + 16 * b + 4 * (lane >> 4), acc[b]);
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) epi.add(row, v0 + 16 * b + 4 * (lane >> 4), acc[b]);
+        for (int e = 0; e < 4; ++e) l[b][e] = acc[b][e];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) epi.most<4>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) epi.add<4>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
     epi.join<16>(row);
     epi.join<32>(row);
     if (lane < 16) all[wave][lane] = {row.top, row.sum};
@@ -120,8 +127,10 @@ __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
     part[(int64_t)blockIdx.x * M + threadIdx.x] = j;
 }
 
-// Joins the column blocks of a row and takes the target's logit: 16 threads a
-// row.
+// Joins the column blocks of a row and takes the target's logit.  TPR threads a row:
+// 16 where rows are many (16 neighbouring rows of a block are then read together),
+// a workgroup where they are few.
+template <int TPR>
 __global__ __launch_bounds__(256) void ce_rows_kernel(const Soft *__restrict__ part, int blocks,
                                                       const uint16_t *__restrict__ x,
                                                       int64_t x_stride,
@@ -129,40 +138,47 @@ __global__ __launch_bounds__(256) void ce_rows_kernel(const Soft *__restrict__ p
                                                       int M, int K, int V,
                                                       float *__restrict__ loss,
                                                       float *__restrict__ lse) {
-    const int r = threadIdx.x & 15, i = threadIdx.x >> 4;  // row and thread of it
-    const int m = blockIdx.x * 16 + r;
-    const bool in = m < M;
+    constexpr int ROWS = 256 / TPR;
+    __shared__ Soft all[TPR][ROWS + 1];
+    __shared__ float dots[TPR][ROWS + 1];
+    // thread i of row r; the parts with the rows next to each other, the dot product with
+    // a row's threads next to each other
+    const int r = threadIdx.x % ROWS, i = threadIdx.x / ROWS;
+    const int dr = threadIdx.x / TPR, di = threadIdx.x % TPR;
+    const int m = blockIdx.x * ROWS + r, dm = blockIdx.x * ROWS + dr;
     Soft s{-INFINITY, 0.0f};
-    if (in)
-        for (int b = i; b < blocks; b += 16) s = join_soft(s, part[(int64_t)b * M + m]);
-    __shared__ Soft all[16][17];
-    __shared__ float dots[16];
+    if (m < M) {
+#pragma unroll 4
+        for (int b = i; b < blocks; b += TPR) s = join_soft(s, part[(int64_t)b * M + m]);
+    }
     all[i][r] = s;
-    // the dot products have 16 neighbouring threads a row
-    const int dr = threadIdx.x >> 4, di = threadIdx.x & 15;
-    const int dm = blockIdx.x * 16 + dr;
     const int64_t tgt = dm < M ? target(t, dm) : -1;
     float d = 0.0f;
     if (tgt >= 0 && tgt < V) {
         const uint16_t *xr = x + dm * x_stride, *wr = w + tgt * K;
-        for (int k = 8 * di; k < K; k += 128) {
+#pragma unroll 2
+        for (int k = 8 * di; k < K; k += 8 * TPR) {
             const u32x4 a = ld16(xr + k), b = ld16(wr + k);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 d += bf_lo(a[e]) * bf_lo(b[e]) + bf_hi(a[e]) * bf_hi(b[e]);
         }
     }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) d += __shfl_xor(d, o);
-    if (di == 0) dots[dr] = d;
-    __syncthreads();
-    if (threadIdx.x >= 16 || !in) return;
+    dots[di][dr] = d;
+    // halves of the threads join pairs, in a fixed order
+    for (int half = TPR / 2; half >= 1; half /= 2) {
+        __syncthreads();
+        if (i < half) {
+            all[i][r] = join_soft(all[i][r], all[i + half][r]);
+            dots[i][r] += dots[i + half][r];
+        }
+    }
+    if (i || m >= M) return;
     s = all[0][r];
-    for (int j = 1; j < 16; ++j) s = join_soft(s, all[j][r]);
     const float l = kLn2 * (s.top + __builtin_amdgcn_logf(s.sum));
     lse[m] = l;
     // a loss is never negative; the two sums may cross by a rounding
-    const float v = l - dots[r];
+    const float v = l - dots[0][r];
     const int64_t tm = target(t, m);
     loss[m] = tm < 0 || tm >= V || v < 0.0f ? 0.0f : v;
 }
@@ -178,29 +194,43 @@ struct EpiD {
     int N, first, V;
     struct Raw {
         float lse, dloss;
-        int64_t t;
+        uint32_t lo, hi;  // the target
+        __device__ __forceinline__ Raw of(int l) const {
+            return {__shfl(lse, l), __shfl(dloss, l), (uint32_t)__shfl((int)lo, l),
+                    (uint32_t)__shfl((int)hi, l)};
+        }
     };
     struct Row {
         float top, scale;
-        int t;
-        bool live;
+        int t;  // the target's column of the piece; -1: it has it not, -2: no target
         __device__ __forceinline__ Row(const EpiD &e, const Raw &r) {
-            live = r.t >= 0 && r.t < e.V;
-            t = live && r.t >= e.first && r.t < e.first + e.N ? (int)(r.t - e.first) : -1;
+            const int64_t v = (int64_t)((uint64_t)r.hi << 32 | r.lo);
             top = r.lse * kLog2e;
             scale = r.dloss;
+            t = v < 0 || v >= e.V                            ? -2
+                : v >= e.first && v < (int64_t)e.first + e.N ? (int)(v - e.first)
+                                                             : -1;
         }
     };
-    __device__ __forceinline__ Raw raw(int m) const { return {lse[m], dloss[m], target(t, m)}; }
+    __device__ __forceinline__ Raw raw(int m) const {
+        if (t.wide) {
+            const u32x2 v = static_cast<const u32x2 *>(t.p)[m];
+            return {lse[m], dloss[m], v[0], v[1]};
+        }
+        const int32_t v = static_cast<const int32_t *>(t.p)[m];
+        return {lse[m], dloss[m], (uint32_t)v, (uint32_t)(v >> 31)};
+    }
     __device__ __forceinline__ Dest dest(int, int, int) const {
         return {d, TW_T_BF16, ldd, (int)ldd, false};
     }
-    __device__ __forceinline__ void values(Row &r, int, int n, f32x4 v, f32x4, f32x4 *o) const {
+    template <int W>
+    __device__ __forceinline__ void values(Row &r, int, int n, const float (&v)[W],
+                                           const float (&)[W], float (&o)[kOuts][W]) const {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < W; ++e) {
             float p = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
             if (n + e == r.t) p -= 1.0f;
-            o[0][e] = r.live && n + e < N ? p * r.scale : 0.0f;
+            o[0][e] = r.t != -2 && n + e < N ? p * r.scale : 0.0f;
         }
     }
 };
@@ -243,8 +273,12 @@ hipError_t launch_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w,
         e = launch_tiles<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, s);
     }
     if (e != hipSuccess) return e;
-    ce_rows_kernel<<<(M + 15) / 16, 256, 0, s>>>(part, (V + 127) / 128, x, x_stride, w,
-                                                 t, M, K, V, loss, lse);
+    const int blocks = (V + 127) / 128;
+    if (M <= 256)
+        ce_rows_kernel<256><<<M, 256, 0, s>>>(part, blocks, x, x_stride, w, t, M, K, V, loss, lse);
+    else
+        ce_rows_kernel<16><<<(M + 15) / 16, 256, 0, s>>>(part, blocks, x, x_stride, w, t, M, K, V,
+                                                         loss, lse);
     return hipGetLastError();
 }
 

@@ -54,9 +54,39 @@ __device__ __forceinline__ void store4(void *p, int type, int64_t at, f32x4 v) {
         *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p) + at) = w;
     }
 }
-__device__ __forceinline__ f32x4 load4_bf16(const uint16_t *p, int64_t at) {
-    const u32x2 w = *reinterpret_cast<const u32x2 *>(p + at);
-    return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+// W (4 or 8) bf16 values.
+template <int W>
+__device__ __forceinline__ void load_bf16(const uint16_t *p, float (&f)[W]) {
+    uint32_t w[W / 2];
+    if constexpr (W == 8) {
+        const u32x4 v = ld16(p);
+        for (int i = 0; i < 4; ++i) w[i] = v[i];
+    } else {
+        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+        for (int i = 0; i < 2; ++i) w[i] = v[i];
+    }
+#pragma unroll
+    for (int e = 0; e < W; ++e) f[e] = e & 1 ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
+}
+// W outputs of row m from column n on (whole ones: n < cols).
+template <int W>
+__device__ __forceinline__ void put_out(const Dest &d, int m, int n, const float (&v)[W]) {
+    if (!d.p) return;
+    const int64_t at = m * d.ld + n;
+    if (d.type == TW_T_F32) {
+        f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(d.p) + at);
+#pragma unroll
+        for (int e = 0; e < W; e += 4) {
+            const f32x4 o{v[e], v[e + 1], v[e + 2], v[e + 3]};
+            q[e / 4] = d.add ? q[e / 4] + o : o;
+        }
+    } else if constexpr (W == 8) {
+        st16(static_cast<uint16_t *>(d.p) + at,
+             u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                   pack_bf16(v[6], v[7])});
+    } else {
+        store4(d.p, TW_T_BF16, at, f32x4{v[0], v[1], v[2], v[3]});
+    }
 }
 
 // 32 rows x 16 reduction elements of a kCols region (32 reduction rows of 128
@@ -130,17 +160,21 @@ struct RingOperand {
     }
 };
 
-// An epilogue has, for a row m of the tile, a Raw (what it loads: raw(m)) and a
-// Row made of it, and
-//   values(row, m, n, v, u, o)   makes its kOuts outputs of columns n .. n + 3 from
-//                                those of the product (u: of the second weights),
+// An epilogue has, for a row m of the tile, a Raw (what it loads: raw(m); of(l): lane
+// l's) and a Row made of it, and
+//   values<W>(row, m, n, v, u, o)  makes its kOuts outputs of columns n .. n + W - 1
+//                                from those of the product (u: of the second weights),
 //   dest(o, z, split)            says where output o goes, or,
 // where it reduces over the columns (kStats),
-//   most(row, n, v), add(row, n, v)   two passes over a lane's columns,
-//   join<L>(row)                      lanes l and l ^ L hold one row,
-//   put(row, lds, w, r)               wave column w's part of the tile's row r,
-//   finish<W>(lds, r, m, cb)          joins W wave columns of 128 columns' block cb,
-//   whole(row, m, cb)                 a wave that holds all 128 columns.
+//   most<W>(row, n, v), add<W>(row, n, v)   two passes over a lane's columns,
+//   join<L>(row)                            lanes l and l ^ L hold one row,
+//   put(row, lds, w, r)                     wave column w's part of the tile's row r,
+//   finish<W>(lds, r, m, cb)                joins W wave columns of 128 columns' block cb,
+//   whole(row, m, cb)                       a wave that holds all 128 columns.
+struct NoRaw {
+    __device__ NoRaw of(int) const { return {}; }
+};
+
 template <int LA, int LB, int NB, int SEG, class Epi>
 __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
     constexpr int NI = 1 + NB, STAGE = NI * kRingPart;
@@ -209,7 +243,7 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
         auto each = [&](auto f) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                f32x4 v, u;
+                float v[4], u[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     v[e] = acc[0][i][4 * q + e];
@@ -219,23 +253,17 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
             }
         };
         if constexpr (Epi::kStats) {
-            each([&](int n, f32x4 v, f32x4) { epi.most(row, n, v); });
-            each([&](int n, f32x4 v, f32x4) { epi.add(row, n, v); });
+            each([&](int n, auto &v, auto &) { epi.template most<4>(row, n, v); });
+            each([&](int n, auto &v, auto &) { epi.template add<4>(row, n, v); });
             epi.template join<32>(row);
             if (lane < 32) epi.put(row, smem, wn, wm * 64 + 32 * i + l32);
         } else if (m < p.M) {
-            each([&](int n, f32x4 v, f32x4 u) {
-                f32x4 out[Epi::kOuts];
+            each([&](int n, auto &v, auto &u) {
+                float out[Epi::kOuts][4];
                 if (n >= epi.dest(0, z, sp).cols) return;
-                epi.values(row, m, n, v, u, out);
+                epi.template values<4>(row, m, n, v, u, out);
 #pragma unroll
-                for (int o = 0; o < Epi::kOuts; ++o) {
-                    const Dest d = epi.dest(o, z, sp);
-                    if (!d.p) continue;
-                    const int64_t at = m * d.ld + n;
-                    if (d.add) out[o] += *reinterpret_cast<f32x4 *>(static_cast<float *>(d.p) + at);
-                    store4(d.p, d.type, at, out[o]);
-                }
+                for (int o = 0; o < Epi::kOuts; ++o) put_out<4>(epi.dest(o, z, sp), m, n, out[o]);
             });
         }
     }
@@ -285,19 +313,19 @@ hipError_t launch_ring(const TileArgs &p, const Epi &epi, hipStream_t s) {
 // 2 f(r), f = r % 4 + 4 (r / 8 % 2): the 8 rows that 32 lanes read, two
 // chunks of each, fill the 16 chunks of a row of banks once.  Loads of either
 // cover whole 128-byte lines.
-constexpr int kWideTile = 256, kWideK = 64;
+constexpr int kWideTile = 256, kWideK = 64, kWideThreads = 512;
 constexpr int kWideLine = 128;                    // bytes of a kRows row in a stage
 constexpr int kWidePart = 256 * kWideLine;        // one operand of a stage
 constexpr int kWideSlot = 2 * kWidePart;
 constexpr int kWideRegion = kWideK * 256;         // half of a kCols operand
-constexpr int kWideStage4K = 32 * kWideLine;      // a wave's outputs on their way to memory
-constexpr int kWideBytes = 2 * kWideSlot + 8 * kWideStage4K;
+constexpr int kWideOut = 4096;                    // a wave's outputs on their way to memory
+constexpr int kWideBytes = 2 * kWideSlot + 8 * kWideOut;
 constexpr int kWideGrid = 256;                    // workgroups: one a CU
 
 __device__ __forceinline__ int line_swz(int r) { return (r >> 1) & 7; }
 
 template <int LA, int LB, int NB, int SEG, class Epi>
-__global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_regions, Epi epi) {
+__global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, int row_regions, Epi epi) {
     static_assert(NB == 1 || (LB == kRows && SEG == 1), "two weight matrices: rows, one term");
     constexpr int BN = kWideTile / NB;
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -517,15 +545,11 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
                 __builtin_amdgcn_sched_barrier(0);
             }
     };
-    // what the epilogue loads for the lane's rows, l16 of each 16
-    typename Epi::Raw raw[4], next[4];
-    auto load_raw = [&](typename Epi::Raw *r) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = epi.raw(min(m0 + wm * 64 + 16 * i + l16, p.M - 1));
-    };
+    // what the epilogue loads for the wave's rows, one a lane
+    auto load_raw = [&]() { return epi.raw(min(m0 + wm * 64 + lane, p.M - 1)); };
 
     at_item(blockIdx.x);
-    load_raw(raw);
+    typename Epi::Raw raw = load_raw(), next = raw;
     load_first();
     for (int t = blockIdx.x; t < items; t += gridDim.x) {
         const int mt = m0, nt = n0, zt = z, st = sp, n = kn;  // m0, ... move on below
@@ -592,7 +616,7 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
         const bool more = t + (int)gridDim.x < items;
         if (more) {
             at_item(t + gridDim.x);
-            load_raw(next);
+            next = load_raw();
             load_first();
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -603,84 +627,111 @@ __global__ __launch_bounds__(512) void wide_tiles_kernel(TileArgs p, int row_reg
         asm volatile("" : "+v"(ln));
         const int lr = ln & 15, lc = 4 * (ln >> 4);
         const int mw = mt + wm * 64, nw = nt + wn * (BN / 2);  // the wave's outputs
+        char *out = smem + 2 * kWideSlot + wave * kWideOut;
         if constexpr (Epi::kStats) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                typename Epi::Row row(epi, raw[i]);
+                typename Epi::Row row(epi, raw.of(16 * i + lr));
+                auto each = [&](auto f) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) epi.most(row, nw + 16 * j + lc, acc[i][j]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) epi.add(row, nw + 16 * j + lc, acc[i][j]);
+                    for (int j = 0; j < 8; ++j) {
+                        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+                        f(nw + 16 * j + lc, v);
+                    }
+                };
+                each([&](int n, auto &v) { epi.template most<4>(row, n, v); });
+                each([&](int n, auto &v) { epi.template add<4>(row, n, v); });
                 epi.template join<16>(row);
                 epi.template join<32>(row);
                 const int m = mw + 16 * i + lr;
                 if (ln < 16 && m < p.M && nw < p.N) epi.whole(row, m, nw / 128);
             }
-        } else {
-            // Outputs go through 4 KB of LDS a wave, 32 rows of 128 bytes at a
-            // time, so that they are stored in whole lines.
-            char *out = smem + 2 * kWideSlot + wave * kWideStage4K;
-            constexpr int JB = 8 / NB;  // the wave's blocks of 16 columns
-            auto write = [&](auto type) {
-                constexpr bool kF32 = decltype(type)::value == TW_T_F32;
-                constexpr int JP = kF32 ? 2 : 4;  // blocks in 128 bytes
+        } else if constexpr (NB == 1) {
+            // 16 rows of 64 columns at a time go through LDS, 256 bytes a row, chunk c of
+            // row r at c ^ r; lanes then hold 8 consecutive columns, so that whole lines
+            // are read and stored.
+            const int r8 = ln >> 3, c8 = ln & 7;
 #pragma unroll
-                for (int i0 = 0; i0 < 4; i0 += 2)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j0 = 0; j0 < JB; j0 += JP) {
-                        if (nw + 16 * j0 >= epi.dest(0, zt, st).cols) continue;
-                        f32x4 o[2][JP][Epi::kOuts];
+                for (int j0 = 0; j0 < 8; j0 += 4) {
+                    const Dest first = epi.dest(0, zt, st);
+                    if (nw + 16 * j0 >= first.cols) continue;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            typename Epi::Row row(epi, raw[i0 + i]);
-                            const int m = min(mw + 16 * (i0 + i) + lr, p.M - 1);
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<f32x4 *>(out + lr * 256 +
+                                                   (((4 * j + (lc >> 2)) ^ lr) << 4)) =
+                            acc[i][j0 + j];
+                    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                            for (int j = 0; j < JP; ++j)
-                                epi.values(row, m, nw + 16 * (j0 + j) + lc, acc[i0 + i][j0 + j],
-                                           acc[i0 + i][NB == 2 ? 4 + j0 + j : j0 + j], o[i][j]);
+                    for (int q = 0; q < 2; ++q) {
+                        const int r = 8 * q + r8, m = mw + 16 * i + r;
+                        const int n = nw + 16 * j0 + 8 * c8;
+                        typename Epi::Row row(epi, raw.of(16 * i + r));
+                        float v[8], o[Epi::kOuts][8];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const u32x4 w = lds_ld16(out, r * 256 + (((2 * c8 + h) ^ r) << 4));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[4 * h + e] = __uint_as_float(w[e]);
                         }
+                        if (m >= p.M || n >= first.cols) continue;
+                        epi.template values<8>(row, m, n, v, v, o);
 #pragma unroll
-                        for (int k = 0; k < Epi::kOuts; ++k) {
-                            const Dest d = epi.dest(k, zt, st);
-                            if (!d.p) continue;
-                            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int j = 0; j < JP; ++j) {
-                                    const int r = 16 * i + lr, byte = (16 * j + lc) * (kF32 ? 4 : 2);
-                                    store4(out + r * kWideLine + (((byte >> 4) ^ line_swz(r)) << 4) +
-                                               (byte & 15),
-                                           decltype(type)::value, 0, o[i][j][k]);
-                                }
-                            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int r = 8 * q + (ln >> 3), c = ln & 7;
-                                const u32x4 w = lds_ld16(out, r * kWideLine + ((c ^ line_swz(r)) << 4));
-                                const int m = mw + 16 * i0 + r;
-                                const int col = nw + 16 * j0 + c * (kF32 ? 4 : 8);
-                                if (m >= p.M || col >= d.cols) continue;
-                                char *to = static_cast<char *>(d.p) +
-                                           (m * d.ld + col) * (kF32 ? 4 : 2);
-                                if (kF32 && d.add) {
-                                    f32x4 *f = reinterpret_cast<f32x4 *>(to);
-                                    *f += __builtin_bit_cast(f32x4, w);
-                                } else {
-                                    st16(to, w);
-                                }
-                            }
-                            __builtin_amdgcn_wave_barrier();
-                        }
+                        for (int k = 0; k < Epi::kOuts; ++k)
+                            put_out<8>(epi.dest(k, zt, st), m, n, o[k]);
                     }
-            };
-            if (epi.dest(0, zt, st).type == TW_T_F32) write(std::integral_constant<int, TW_T_F32>{});
-            else write(std::integral_constant<int, TW_T_BF16>{});
-        }
-        if (more) {
+                    __builtin_amdgcn_wave_barrier();
+                }
+        } else {
+            // The outputs (bf16) go through LDS, 32 rows of 128 bytes at a time.
 #pragma unroll
-            for (int i = 0; i < 4; ++i) raw[i] = next[i];
+            for (int i0 = 0; i0 < 4; i0 += 2) {
+                if (nw >= epi.dest(0, zt, st).cols) continue;
+                float o[2][4][Epi::kOuts][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    typename Epi::Row row(epi, raw.of(16 * (i0 + i) + lr));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float v[4], u[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            v[e] = acc[i0 + i][j][e];
+                            u[e] = acc[i0 + i][4 + j][e];
+                        }
+                        epi.template values<4>(row, 0, 0, v, u, o[i][j]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < Epi::kOuts; ++k) {
+                    const Dest d = epi.dest(k, zt, st);
+                    if (!d.p) continue;
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 16 * i + lr, byte = (16 * j + lc) * 2;
+                            const float(&f)[4] = o[i][j][k];
+                            store4(out + r * kWideLine + (((byte >> 4) ^ line_swz(r)) << 4) +
+                                       (byte & 15),
+                                   TW_T_BF16, 0, f32x4{f[0], f[1], f[2], f[3]});
+                        }
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int r = 8 * q + (ln >> 3), c = ln & 7;
+                        const u32x4 w = lds_ld16(out, r * kWideLine + ((c ^ line_swz(r)) << 4));
+                        const int m = mw + 16 * i0 + r, n = nw + 8 * c;
+                        if (m < p.M && n < d.cols)
+                            st16(static_cast<uint16_t *>(d.p) + m * d.ld + n, w);
+                    }
+                    __builtin_amdgcn_wave_barrier();
+                }
+            }
         }
+        raw = next;
     }
 }
 
@@ -692,8 +743,7 @@ hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
     const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
     const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
     const int64_t items = nbm * nbn * p.groups * p.splits;
-    if (items == 0) return hipSuccess;
-    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), 512, kWideBytes, s>>>(
+    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), kWideThreads, kWideBytes, s>>>(
         p, wide_row_regions(nbm, nbn), epi);
     return hipGetLastError();
 }
@@ -703,7 +753,7 @@ template <int LA, int LB, int NB, int SEG>
 bool use_wide(const TileArgs &p) {
     const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
     const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
-    return nbm * nbn * p.groups * p.splits >= 128;
+    return p.R > 0 && nbm * nbn * p.groups * p.splits >= 128;
 }
 template <int LA, int LB, int NB, int SEG, class Epi>
 hipError_t launch_tiles(const TileArgs &p, const Epi &epi, hipStream_t s) {
@@ -723,7 +773,7 @@ struct EpiStore {
     float *part;  // or null
     int more;
     int M, N;
-    struct Raw {};
+    typedef NoRaw Raw;
     struct Row {
         __device__ Row(const EpiStore &, Raw) {}
     };
@@ -732,27 +782,31 @@ struct EpiStore {
         if (part) return {part + (int64_t)split * M * N, TW_T_F32, N, N, more != 0};
         return {z == 0 ? out[0] : z == 1 ? out[1] : out[2], type, N, N, false};
     }
-    __device__ __forceinline__ void values(Row &, int, int, f32x4 v, f32x4, f32x4 *o) const {
-        o[0] = v;
+    template <int W>
+    __device__ __forceinline__ void values(Row &, int, int, const float (&v)[W], const float (&)[W],
+                                           float (&o)[kOuts][W]) const {
+#pragma unroll
+        for (int e = 0; e < W; ++e) o[0][e] = v[e];
     }
 };
 
 // out = the sum of the parts, in their order.
 template <int T>
-__global__ __launch_bounds__(256) void sum_parts_kernel(const float *__restrict__ part, int splits,
+__global__ __launch_bounds__(64) void sum_parts_kernel(const float *__restrict__ part, int splits,
                                                         int64_t n, void *__restrict__ out) {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    const int64_t at = ((int64_t)blockIdx.x * 64 + threadIdx.x) * 4;
     if (at >= n) return;
     f32x4 v = *reinterpret_cast<const f32x4 *>(part + at);
+#pragma unroll 8
     for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(part + s * n + at);
     store4(out, T, at, v);
 }
 inline hipError_t launch_sum_parts(const float *part, int splits, int64_t n, void *out, int type,
                                    hipStream_t s) {
     if (n == 0) return hipSuccess;
-    const unsigned grid = (unsigned)((n / 4 + 255) / 256);
-    if (type == TW_T_F32) sum_parts_kernel<TW_T_F32><<<grid, 256, 0, s>>>(part, splits, n, out);
-    else sum_parts_kernel<TW_T_BF16><<<grid, 256, 0, s>>>(part, splits, n, out);
+    const unsigned grid = (unsigned)((n / 4 + 63) / 64);
+    if (type == TW_T_F32) sum_parts_kernel<TW_T_F32><<<grid, 64, 0, s>>>(part, splits, n, out);
+    else sum_parts_kernel<TW_T_BF16><<<grid, 64, 0, s>>>(part, splits, n, out);
     return hipGetLastError();
 }
 
@@ -768,8 +822,10 @@ int splits_of(const TileArgs &p) {
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= 8 && s <= stages; ++s) {
+        const int64_t per = (stages + s - 1) / s;
+        if ((stages + per - 1) / per != s) continue;  // (every part has a stage)
         const int64_t rounds = (nbm * nbn * p.groups * s + kWideGrid - 1) / kWideGrid;
-        const double us = 1.5 * rounds * ((stages + s - 1) / s) +
+        const double us = 1.5 * rounds * per +
                           (s > 1 ? 3.0 + (double)s * p.M * p.N * p.groups * 8 / 4.5e6 : 0.0);
         if (s == 1 || us < least) {
             best = s;
