@@ -64,10 +64,11 @@ struct EpiGlu {
         __device__ Row(const EpiGlu &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
+    __device__ int stores() const { return 8 * (1 + (g != nullptr) + (u != nullptr)); }
     __device__ __forceinline__ Dest dest(int o, int, int) const {
         return {o == 0 ? h : o == 1 ? g : u, TW_T_BF16, N, N, false};
     }
-    template <int W>
+    template <int W, bool ALL>
     __device__ __forceinline__ void values(Row &, int, int, const float (&v)[W],
                                            const float (&w)[W], float (&o)[kOuts][W]) const {
 #pragma unroll
@@ -92,10 +93,11 @@ struct EpiDh {
         __device__ Row(const EpiDh &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
+    __device__ int stores() const { return 48; }
     __device__ __forceinline__ Dest dest(int o, int, int) const {
         return {o == 0 ? dz : o == 1 ? du : h, TW_T_BF16, N, N, false};
     }
-    template <int W>
+    template <int W, bool ALL>
     __device__ __forceinline__ void values(Row &, int m, int n, const float (&v)[W],
                                            const float (&)[W], float (&o)[kOuts][W]) const {
         float gv[W], uv[W];

@@ -51,18 +51,19 @@ struct EpiSoft {
         __device__ Row(const EpiSoft &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
-    template <int W>
+    __device__ int stores() const { return 0; }
+    template <int W, bool ALL>
     __device__ __forceinline__ void most(Row &r, int n, const float (&v)[W]) const {
 #pragma unroll
         for (int e = 0; e < W; ++e)
-            if (n + e < N) r.most = fmaxf(r.most, v[e]);
+            if (ALL || n + e < N) r.most = fmaxf(r.most, v[e]);
     }
-    template <int W>
+    template <int W, bool ALL>
     __device__ __forceinline__ void add(Row &r, int n, const float (&v)[W]) const {
         r.top = r.most == -INFINITY ? 0.0f : r.most * kLog2e;
 #pragma unroll
         for (int e = 0; e < W; ++e)
-            if (n + e < N) r.sum += __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
+            if (ALL || n + e < N) r.sum += __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
     }
     template <int L>
     __device__ __forceinline__ void join(Row &r) const {
@@ -113,9 +114,9 @@ __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) l[b][e] = acc[b][e];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) epi.most<4>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+    for (int b = 0; b < 2; ++b) epi.most<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) epi.add<4>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+    for (int b = 0; b < 2; ++b) epi.add<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
     epi.join<16>(row);
     epi.join<32>(row);
     if (lane < 16) all[wave][lane] = {row.top, row.sum};
@@ -223,14 +224,15 @@ struct EpiD {
     __device__ __forceinline__ Dest dest(int, int, int) const {
         return {d, TW_T_BF16, ldd, (int)ldd, false};
     }
-    template <int W>
+    __device__ int stores() const { return 16; }
+    template <int W, bool ALL>
     __device__ __forceinline__ void values(Row &r, int, int n, const float (&v)[W],
                                            const float (&)[W], float (&o)[kOuts][W]) const {
 #pragma unroll
         for (int e = 0; e < W; ++e) {
             float p = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
             if (n + e == r.t) p -= 1.0f;
-            o[0][e] = r.t != -2 && n + e < N ? p * r.scale : 0.0f;
+            o[0][e] = r.t != -2 && (ALL || n + e < N) ? p * r.scale : 0.0f;
         }
     }
 };

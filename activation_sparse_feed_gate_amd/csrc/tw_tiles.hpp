@@ -162,11 +162,14 @@ struct RingOperand {
 
 // An epilogue has, for a row m of the tile, a Raw (what it loads: raw(m); of(l): lane
 // l's) and a Row made of it, and
-//   values<W>(row, m, n, v, u, o)  makes its kOuts outputs of columns n .. n + W - 1
-//                                from those of the product (u: of the second weights),
-//   dest(o, z, split)            says where output o goes, or,
+//   values<W, ALL>(row, m, n, v, u, o)  makes its kOuts outputs of columns n .. n + W
+//                                - 1 from those of the product (u: of the second
+//                                weights); ALL: these columns are all within N,
+//   dest(o, z, split)            says where output o goes,
+//   stores()                     how many stores a wave of the larger tiles makes of a
+//                                whole tile, or,
 // where it reduces over the columns (kStats),
-//   most<W>(row, n, v), add<W>(row, n, v)   two passes over a lane's columns,
+//   most<W, ALL>(row, n, v), add<W, ALL>(row, n, v)   two passes over a lane's columns,
 //   join<L>(row)                            lanes l and l ^ L hold one row,
 //   put(row, lds, w, r)                     wave column w's part of the tile's row r,
 //   finish<W>(lds, r, m, cb)                joins W wave columns of 128 columns' block cb,
@@ -253,15 +256,15 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
             }
         };
         if constexpr (Epi::kStats) {
-            each([&](int n, auto &v, auto &) { epi.template most<4>(row, n, v); });
-            each([&](int n, auto &v, auto &) { epi.template add<4>(row, n, v); });
+            each([&](int n, auto &v, auto &) { epi.template most<4, false>(row, n, v); });
+            each([&](int n, auto &v, auto &) { epi.template add<4, false>(row, n, v); });
             epi.template join<32>(row);
             if (lane < 32) epi.put(row, smem, wn, wm * 64 + 32 * i + l32);
         } else if (m < p.M) {
             each([&](int n, auto &v, auto &u) {
                 float out[Epi::kOuts][4];
                 if (n >= epi.dest(0, z, sp).cols) return;
-                epi.template values<4>(row, m, n, v, u, out);
+                epi.template values<4, false>(row, m, n, v, u, out);
 #pragma unroll
                 for (int o = 0; o < Epi::kOuts; ++o) put_out<4>(epi.dest(o, z, sp), m, n, out[o]);
             });
@@ -323,6 +326,19 @@ constexpr int kWideBytes = 2 * kWideSlot + 8 * kWideOut;
 constexpr int kWideGrid = 256;                    // workgroups: one a CU
 
 __device__ __forceinline__ int line_swz(int r) { return (r >> 1) & 7; }
+
+// wait_vmcnt<N + more>, `more` a multiple of 8 up to 48.
+template <int N>
+__device__ __forceinline__ void wait_besides(int more) {
+    switch (more) {
+    case 8: wait_vmcnt<N + 8>(); break;
+    case 16: wait_vmcnt<N + 16>(); break;
+    case 24: wait_vmcnt<N + 24>(); break;
+    case 32: wait_vmcnt<N + 32>(); break;
+    case 48: wait_vmcnt<N + 48>(); break;
+    default: wait_vmcnt<N>(); break;
+    }
+}
 
 template <int LA, int LB, int NB, int SEG, class Epi>
 __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, int row_regions, Epi epi) {
@@ -548,6 +564,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     // what the epilogue loads for the wave's rows, one a lane
     auto load_raw = [&]() { return epi.raw(min(m0 + wm * 64 + lane, p.M - 1)); };
 
+    int after = 0;  // stores younger than a tile's first loads
     at_item(blockIdx.x);
     typename Epi::Raw raw = load_raw(), next = raw;
     load_first();
@@ -557,10 +574,10 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{};
-        // What may be outstanding besides the loads below is younger (the last
-        // tile's stores), so these waits hold for at least the loads they name.
+        // The last tile's stores are younger than the loads of stages 0 and 1, and may
+        // stay on their way while these are waited for.
         if (n > 0) {
-            if (n > 1) wait_vmcnt<kB + kAB + kB>();
+            if (n > 1) wait_besides<kB + kAB + kB>(after);
             else wait_vmcnt<kB>();
             __builtin_amdgcn_s_barrier();
 #pragma unroll
@@ -571,13 +588,13 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
             int k = 0;
             for (; k + 2 < n; ++k) {
                 step(k, 0);
-                wait_vmcnt<kAB + kB>();
+                wait_besides<kAB + kB>(k < 2 ? after : 0);
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();  // X
                 load_ab(k + 2);
                 step(k, 1);
                 step(k, 2);
-                wait_vmcnt<kB + kAB>();
+                wait_besides<kB + kAB>(k < 1 ? after : 0);
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();  // Y
                 load_b(k + 2, 1);
@@ -628,109 +645,126 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         const int lr = ln & 15, lc = 4 * (ln >> 4);
         const int mw = mt + wm * 64, nw = nt + wn * (BN / 2);  // the wave's outputs
         char *out = smem + 2 * kWideSlot + wave * kWideOut;
-        if constexpr (Epi::kStats) {
+        // ALL: every row and column of the wave's outputs is one of the product's
+        auto write = [&](auto whole) {
+            constexpr bool ALL = decltype(whole)::value;
+            if constexpr (Epi::kStats) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                typename Epi::Row row(epi, raw.of(16 * i + lr));
-                auto each = [&](auto f) {
+                for (int i = 0; i < 4; ++i) {
+                    typename Epi::Row row(epi, raw.of(16 * i + lr));
+                    auto each = [&](auto f) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                        f(nw + 16 * j + lc, v);
-                    }
-                };
-                each([&](int n, auto &v) { epi.template most<4>(row, n, v); });
-                each([&](int n, auto &v) { epi.template add<4>(row, n, v); });
-                epi.template join<16>(row);
-                epi.template join<32>(row);
-                const int m = mw + 16 * i + lr;
-                if (ln < 16 && m < p.M && nw < p.N) epi.whole(row, m, nw / 128);
-            }
-        } else if constexpr (NB == 1) {
-            // 16 rows of 64 columns at a time go through LDS, 256 bytes a row, chunk c of
-            // row r at c ^ r; lanes then hold 8 consecutive columns, so that whole lines
-            // are read and stored.
-            const int r8 = ln >> 3, c8 = ln & 7;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j0 = 0; j0 < 8; j0 += 4) {
-                    const Dest first = epi.dest(0, zt, st);
-                    if (nw + 16 * j0 >= first.cols) continue;
+                        for (int j = 0; j < 8; ++j) {
+                            const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2],
+                                                acc[i][j][3]};
+                            f(nw + 16 * j + lc, v);
+                        }
+                    };
+                    each([&](int n, auto &v) { epi.template most<4, ALL>(row, n, v); });
+                    each([&](int n, auto &v) { epi.template add<4, ALL>(row, n, v); });
+                    epi.template join<16>(row);
+                    epi.template join<32>(row);
+                    const int m = mw + 16 * i + lr;
+                    if (ln < 16 && (ALL || (m < p.M && nw < p.N))) epi.whole(row, m, nw / 128);
+                }
+            } else if constexpr (NB == 1) {
+                // 16 rows of 64 columns at a time go through LDS, 256 bytes a row, chunk c
+                // of row r at c ^ r; lanes then hold 8 consecutive columns, so that whole
+                // lines are read and stored.  The next block enters LDS before this one is
+                // worked on.
+                const int r8 = ln >> 3, c8 = ln & 7;
+                auto enter = [&](int b) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<f32x4 *>(out + lr * 256 +
-                                                   (((4 * j + (lc >> 2)) ^ lr) << 4)) =
-                            acc[i][j0 + j];
+                        *reinterpret_cast<f32x4 *>(
+                            out + lr * 256 + (((4 * j + (lc >> 2)) ^ lr) << 4)) =
+                            acc[b >> 1][4 * (b & 1) + j];
                     __builtin_amdgcn_wave_barrier();
+                };
+                const int cols = epi.dest(0, zt, st).cols;
+                enter(0);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int r = 8 * q + r8, m = mw + 16 * i + r;
-                        const int n = nw + 16 * j0 + 8 * c8;
-                        typename Epi::Row row(epi, raw.of(16 * i + r));
-                        float v[8], o[Epi::kOuts][8];
+                for (int b = 0; b < 8; ++b) {
+                    const int i = b >> 1, n = nw + 64 * (b & 1) + 8 * c8;
+                    float v[2][8];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
+                            const int r = 8 * q + r8;
                             const u32x4 w = lds_ld16(out, r * 256 + (((2 * c8 + h) ^ r) << 4));
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) v[4 * h + e] = __uint_as_float(w[e]);
+                            for (int e = 0; e < 4; ++e) v[q][4 * h + e] = __uint_as_float(w[e]);
                         }
-                        if (m >= p.M || n >= first.cols) continue;
-                        epi.template values<8>(row, m, n, v, v, o);
+                    __builtin_amdgcn_wave_barrier();
+                    if (b < 7) enter(b + 1);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int r = 16 * i + 8 * q + r8, m = mw + r;
+                        typename Epi::Row row(epi, raw.of(r));
+                        float o[Epi::kOuts][8];
+                        if (!ALL && (m >= p.M || n >= cols)) continue;
+                        epi.template values<8, ALL>(row, m, n, v[q], v[q], o);
 #pragma unroll
                         for (int k = 0; k < Epi::kOuts; ++k)
                             put_out<8>(epi.dest(k, zt, st), m, n, o[k]);
                     }
-                    __builtin_amdgcn_wave_barrier();
                 }
-        } else {
-            // The outputs (bf16) go through LDS, 32 rows of 128 bytes at a time.
+            } else {
+                // The outputs (bf16) go through LDS, 32 rows of 128 bytes at a time.
 #pragma unroll
-            for (int i0 = 0; i0 < 4; i0 += 2) {
-                if (nw >= epi.dest(0, zt, st).cols) continue;
-                float o[2][4][Epi::kOuts][4];
+                for (int i0 = 0; i0 < 4; i0 += 2) {
+                    if (nw >= epi.dest(0, zt, st).cols) continue;
+                    float o[2][4][Epi::kOuts][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    typename Epi::Row row(epi, raw.of(16 * (i0 + i) + lr));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float v[4], u[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            v[e] = acc[i0 + i][j][e];
-                            u[e] = acc[i0 + i][4 + j][e];
-                        }
-                        epi.template values<4>(row, 0, 0, v, u, o[i][j]);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < Epi::kOuts; ++k) {
-                    const Dest d = epi.dest(k, zt, st);
-                    if (!d.p) continue;
-                    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2; ++i) {
+                        typename Epi::Row row(epi, raw.of(16 * (i0 + i) + lr));
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int r = 16 * i + lr, byte = (16 * j + lc) * 2;
-                            const float(&f)[4] = o[i][j][k];
-                            store4(out + r * kWideLine + (((byte >> 4) ^ line_swz(r)) << 4) +
-                                       (byte & 15),
-                                   TW_T_BF16, 0, f32x4{f[0], f[1], f[2], f[3]});
-                        }
-                    __builtin_amdgcn_wave_barrier();
+                            float v[4], u[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int r = 8 * q + (ln >> 3), c = ln & 7;
-                        const u32x4 w = lds_ld16(out, r * kWideLine + ((c ^ line_swz(r)) << 4));
-                        const int m = mw + 16 * i0 + r, n = nw + 8 * c;
-                        if (m < p.M && n < d.cols)
-                            st16(static_cast<uint16_t *>(d.p) + m * d.ld + n, w);
+                            for (int e = 0; e < 4; ++e) {
+                                v[e] = acc[i0 + i][j][e];
+                                u[e] = acc[i0 + i][4 + j][e];
+                            }
+                            epi.template values<4, ALL>(row, 0, 0, v, u, o[i][j]);
+                        }
                     }
-                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int k = 0; k < Epi::kOuts; ++k) {
+                        const Dest d = epi.dest(k, zt, st);
+                        if (!d.p) continue;
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int r = 16 * i + lr, byte = (16 * j + lc) * 2;
+                                const float(&f)[4] = o[i][j][k];
+                                store4(out + r * kWideLine + (((byte >> 4) ^ line_swz(r)) << 4) +
+                                           (byte & 15),
+                                       TW_T_BF16, 0, f32x4{f[0], f[1], f[2], f[3]});
+                            }
+                        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = 8 * q + (ln >> 3), c = ln & 7;
+                            const u32x4 w =
+                                lds_ld16(out, r * kWideLine + ((c ^ line_swz(r)) << 4));
+                            const int m = mw + 16 * i0 + r, n = nw + 8 * c;
+                            if (ALL || (m < p.M && n < d.cols))
+                                st16(static_cast<uint16_t *>(d.p) + m * d.ld + n, w);
+                        }
+                        __builtin_amdgcn_wave_barrier();
+                    }
                 }
             }
-        }
+        };
+        const bool inside = mt + kWideTile <= p.M && nt + BN <= p.N;
+        if (inside) write(std::true_type{});
+        else write(std::false_type{});
+        // at least so many stores of this tile are younger than the next one's loads
+        after = inside ? epi.stores() : 0;
         raw = next;
     }
 }
@@ -778,11 +812,12 @@ struct EpiStore {
         __device__ Row(const EpiStore &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
+    __device__ int stores() const { return part || type == TW_T_F32 ? 32 : 16; }
     __device__ __forceinline__ Dest dest(int, int z, int split) const {
         if (part) return {part + (int64_t)split * M * N, TW_T_F32, N, N, more != 0};
         return {z == 0 ? out[0] : z == 1 ? out[1] : out[2], type, N, N, false};
     }
-    template <int W>
+    template <int W, bool ALL>
     __device__ __forceinline__ void values(Row &, int, int, const float (&v)[W], const float (&)[W],
                                            float (&o)[kOuts][W]) const {
 #pragma unroll
