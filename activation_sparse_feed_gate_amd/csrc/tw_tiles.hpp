@@ -426,64 +426,74 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     auto group_of = [&](const uint16_t *const *q, int kt) {
         return SEG == 2 ? (kt >= KT ? q[1] : q[0]) : z == 0 ? q[0] : z == 1 ? q[1] : q[2];
     };
-    auto load_a = [&](int i) {
-        const int kt = k0 + i, ks = SEG == 2 && kt >= KT ? kt - KT : kt;
-        char *slot = smem + (i & 1) * kWideSlot;
-        if constexpr (LA == kRows) {
-            const bool past = ks * kWideK + chunk * 8 >= p.R;
-            const uint32_t v64 = 64u * (uint32_t)p.lda * 2;
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                dma16(SEG == 2 && kt >= KT ? ra[SEG - 1] : ra[0],
-                      past ? kPastEnd : va[0] + g * v64, ks * kWideLine,
-                      slot + (64 * g + 8 * wave) * kWideLine);
-        } else {
-            const rsrc_t d = col_rsrc(group_of(p.a, kt), p.lda, ks, m0, p.M);
-            const uint32_t v32 = 32u * (uint32_t)p.lda * 2;
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    dma16(d, va[q] + h * v32, 0,
-                          slot + q * kWideRegion + (32 * h + 4 * wave) * 256);
-        }
+    // The loads of the item's stage i, begun together and issued one by one: put_a 0 ..
+    // 3, put_b of pair q of the column blocks (0: B0, B1; 1: B2, B3), 0 and 1.  kRows:
+    // groups of 64 rows; of one matrix 2 g + q, g the wave column, of two matrix q, its
+    // groups g.
+    struct Loads {
+        rsrc_t d[2];  // of one operand, or two matrices
+        uint32_t v[2], soff;
+        char *slot;
     };
-    // pair q of the column blocks: 0: B0, B1; 1: B2, B3.  kRows: groups of 64 rows;
-    // one matrix: 2 i + q, i the wave column, two: matrix q, its groups 2 q + i
-    auto load_b = [&](int i, int q) {
+    auto begin_a = [&](int i) {
         const int kt = k0 + i, ks = SEG == 2 && kt >= KT ? kt - KT : kt;
-        char *slot = smem + (i & 1) * kWideSlot + kWidePart;
-        if constexpr (LB == kRows) {
-            const bool past = ks * kWideK + chunk * 8 >= p.R;
-            const uint32_t v64 = 64u * (uint32_t)ldb * 2;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const int g = NB == 1 ? 2 * w + q : 2 * q + w;
-                dma16(NB == 2 ? rb[NB == 2 ? q : 0] : SEG == 2 && kt >= KT ? rb[SEG - 1] : rb[0],
-                      past ? kPastEnd : vb[0] + (NB == 1 ? g : w) * v64, ks * kWideLine,
-                      slot + (64 * g + 8 * wave) * kWideLine);
-            }
+        Loads l;
+        l.slot = smem + (i & 1) * kWideSlot;
+        l.soff = ks * kWideLine;
+        if constexpr (LA == kRows) {
+            l.d[0] = SEG == 2 && kt >= KT ? ra[SEG - 1] : ra[0];
+            l.v[0] = ks * kWideK + chunk * 8 >= p.R ? kPastEnd : va[0];
         } else {
-            const rsrc_t d = col_rsrc(group_of(p.b, kt), ldb, ks, n0, p.N);
-            const uint32_t v32 = 32u * (uint32_t)ldb * 2;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                dma16(d, vb[q] + h * v32, 0, slot + q * kWideRegion + (32 * h + 4 * wave) * 256);
+            l.d[0] = col_rsrc(group_of(p.a, kt), p.lda, ks, m0, p.M);
+            l.v[0] = va[0];
+            l.v[1] = va[1];
+        }
+        return l;
+    };
+    auto begin_b = [&](int i) {
+        const int kt = k0 + i, ks = SEG == 2 && kt >= KT ? kt - KT : kt;
+        Loads l;
+        l.slot = smem + (i & 1) * kWideSlot + kWidePart;
+        l.soff = ks * kWideLine;
+        if constexpr (LB == kRows) {
+            l.d[0] = SEG == 2 && kt >= KT ? rb[SEG - 1] : rb[0];
+            if constexpr (NB == 2) l.d[1] = rb[1];
+            l.v[0] = ks * kWideK + chunk * 8 >= p.R ? kPastEnd : vb[0];
+        } else {
+            l.d[0] = col_rsrc(group_of(p.b, kt), ldb, ks, n0, p.N);
+            l.v[0] = vb[0];
+            l.v[1] = vb[1];
+        }
+        return l;
+    };
+    auto put_a = [&](const Loads &l, int g) {
+        if constexpr (LA == kRows)
+            dma16(l.d[0], l.v[0] + g * (64u * (uint32_t)p.lda * 2), l.soff,
+                  l.slot + (64 * g + 8 * wave) * kWideLine);
+        else
+            dma16(l.d[0], l.v[g >> 1] + (g & 1) * (32u * (uint32_t)p.lda * 2), 0,
+                  l.slot + (g >> 1) * kWideRegion + (32 * (g & 1) + 4 * wave) * 256);
+    };
+    auto put_b = [&](const Loads &l, int q, int g) {
+        if constexpr (LB == kRows) {
+            const int at = NB == 1 ? 2 * g + q : 2 * q + g;
+            dma16(l.d[NB == 2 ? q : 0], l.v[0] + (NB == 1 ? at : g) * (64u * (uint32_t)ldb * 2),
+                  l.soff, l.slot + (64 * at + 8 * wave) * kWideLine);
+        } else {
+            dma16(l.d[0], l.v[q] + g * (32u * (uint32_t)ldb * 2), 0,
+                  l.slot + q * kWideRegion + (32 * g + 4 * wave) * 256);
         }
     };
     constexpr int kAB = 6, kB = 2;  // loads of a wave in each part
-    auto load_ab = [&](int i) {
-        load_a(i);
-        load_b(i, 0);
-    };
     auto load_first = [&] {
-        if (kn > 0) {
-            load_ab(0);
-            load_b(0, 1);
-        }
-        if (kn > 1) {
-            load_ab(1);
-            load_b(1, 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (i >= kn) break;
+            const Loads a = begin_a(i), b = begin_b(i);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) put_a(a, g);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) put_b(b, g >> 1, g & 1);
         }
     };
     // Fragment of 16 rows (columns of the product's other operand) from `row` on,
@@ -512,20 +522,15 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         else return read_cols(part + (wm >> 1) * kWideRegion, (wm & 1) * 8 + 2 * i, s);
     };
     u32x4 fa[2][4], fb[2][2][2];  // [sub-step][16 rows], [register set][sub-step][16 columns]
-    auto read_b = [&](int k, int j) {  // block j of 32 columns
+    auto read_b = [&](int k, int j, int s, int h) {  // half h of block j of 32 columns
         const char *part = smem + (k & 1) * kWideSlot + kWidePart;
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (LB == kRows)
-                    fb[j & 1][s][h] = read_rows(
-                        part, (NB == 1 ? wn * 128 + j * 32 : (j >> 1) * 128 + wn * 64 + (j & 1) * 32) +
-                                  16 * h, s);
-                else
-                    fb[j & 1][s][h] =
-                        read_cols(part + (j >> 1) * kWideRegion, wn * 8 + (j & 1) * 4 + 2 * h, s);
-            }
+        if constexpr (LB == kRows)
+            fb[j & 1][s][h] = read_rows(
+                part,
+                (NB == 1 ? wn * 128 + j * 32 : (j >> 1) * 128 + wn * 64 + (j & 1) * 32) + 16 * h, s);
+        else
+            fb[j & 1][s][h] =
+                read_cols(part + (j >> 1) * kWideRegion, wn * 8 + (j & 1) * 4 + 2 * h, s);
     };
     // [16 rows][16 columns]: register r of a block is row l16, column 4 (lane / 16) + r
     f32x4 acc[4][8];
@@ -534,33 +539,38 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
             __builtin_bit_cast(bf16x8, fb[j & 1][s][h]), __builtin_bit_cast(bf16x8, fa[s][i]),
             acc[i][2 * j + h], 0, 0, 0);
     };
-    // The scheduling barriers keep each step's reads ahead of its matrix
-    // instructions.
-    auto step = [&](int k, int j) {
-        read_b(k, j + 1);
-        __builtin_amdgcn_sched_barrier(0);
+    // A step: block j's 16 matrix instructions, two at a time, and before each pair what
+    // other(0 .. 7) issues.  (The scheduling barriers keep that order: loads and
+    // reads that all waves issue at once after a barrier hold up the matrix
+    // instructions behind them.)
+    auto step = [&](int j, auto other) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int q = 0; q < 8; ++q) {
+            other(q);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) mma(j, s, i, h);
-        __builtin_amdgcn_sched_barrier(0);
+            for (int h = 0; h < 2; ++h) mma(j, q >> 2, q & 3, h);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     };
-    auto last_step = [&](int k) {
-        read_b(k + 1, 0);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mma(3, s, i, 0);
-                mma(3, s, i, 1);
-                __builtin_amdgcn_sched_barrier(0);
-                fa[s][i] = read_a(k + 1, i, s);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+    // the fragments of stage k's block j, in the step before its own
+    auto read_next = [&](int k, int j, int q) {
+        if (q < 4) read_b(k, j, q >> 1, q & 1);
     };
+    auto last_step = [&](int k, auto other) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            read_next(k + 1, 0, q);
+            other(q);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma(3, q >> 2, q & 3, h);
+            __builtin_amdgcn_sched_barrier(0);
+            fa[q >> 2][q & 3] = read_a(k + 1, q & 3, q >> 2);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto nothing = [](int) {};
     // what the epilogue loads for the wave's rows, one a lane
     auto load_raw = [&]() { return epi.raw(min(m0 + wm * 64 + lane, p.M - 1)); };
 
@@ -584,46 +594,47 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) fa[s][i] = read_a(0, i, s);
-            read_b(0, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) read_next(0, 0, q);
             int k = 0;
             for (; k + 2 < n; ++k) {
-                step(k, 0);
+                step(0, [&](int q) { read_next(k, 1, q); });
                 wait_besides<kAB + kB>(k < 2 ? after : 0);
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();  // X
-                load_ab(k + 2);
-                step(k, 1);
-                step(k, 2);
+                const Loads la = begin_a(k + 2), lb = begin_b(k + 2);
+                step(1, [&](int q) {
+                    read_next(k, 2, q);
+                    if (q < 4) put_a(la, q);
+                    else if (q < 6) put_b(lb, 0, q - 4);
+                });
+                step(2, [&](int q) { read_next(k, 3, q); });
                 wait_besides<kB + kAB>(k < 1 ? after : 0);
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();  // Y
-                load_b(k + 2, 1);
-                last_step(k);
+                last_step(k, [&](int q) {
+                    if (q >= 4 && q < 6) put_b(lb, 1, q - 4);
+                });
             }
             if (k + 1 < n) {
-                step(k, 0);
+                step(0, [&](int q) { read_next(k, 1, q); });
                 wait_vmcnt<kAB + kB>();
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();
-                step(k, 1);
-                step(k, 2);
+                step(1, [&](int q) { read_next(k, 2, q); });
+                step(2, [&](int q) { read_next(k, 3, q); });
                 wait_vmcnt<kB>();
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();
-                last_step(k);
+                last_step(k, nothing);
                 ++k;
             }
-            step(k, 0);
+            step(0, [&](int q) { read_next(k, 1, q); });
             wait_vmcnt<0>();
             __builtin_amdgcn_s_barrier();
-            step(k, 1);
-            step(k, 2);
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) mma(3, s, i, h);
+            step(1, [&](int q) { read_next(k, 2, q); });
+            step(2, [&](int q) { read_next(k, 3, q); });
+            step(3, nothing);
         }
 
         // The next tile's first loads (after every wave has read its last
