@@ -598,18 +598,21 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
             for (int q = 0; q < 4; ++q) read_next(0, 0, q);
             int k = 0;
             for (; k + 2 < n; ++k) {
+                const Loads la = begin_a(k + 2), lb = begin_b(k + 2);
                 step(0, [&](int q) { read_next(k, 1, q); });
-                wait_besides<kAB + kB>(k < 2 ? after : 0);
+                if (after) wait_besides<kAB + kB>(after);
+                else wait_vmcnt<kAB + kB>();
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();  // X
-                const Loads la = begin_a(k + 2), lb = begin_b(k + 2);
                 step(1, [&](int q) {
                     read_next(k, 2, q);
                     if (q < 4) put_a(la, q);
                     else if (q < 6) put_b(lb, 0, q - 4);
                 });
                 step(2, [&](int q) { read_next(k, 3, q); });
-                wait_besides<kB + kAB>(k < 1 ? after : 0);
+                if (k) after = 0;
+                if (after) wait_besides<kB + kAB>(after);
+                else wait_vmcnt<kB + kAB>();
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();  // Y
                 last_step(k, [&](int q) {
