@@ -64,8 +64,8 @@ struct EpiGlu {
         __device__ Row(const EpiGlu &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
-    __device__ int stores() const { return 8 * (1 + (g != nullptr) + (u != nullptr)); }
-    __device__ __forceinline__ Dest dest(int o, int, int) const {
+    __device__ int stores(const Place &) const { return 8 * (1 + (g != nullptr) + (u != nullptr)); }
+    __device__ __forceinline__ Dest dest(int o, const Place &) const {
         return {o == 0 ? h : o == 1 ? g : u, TW_T_BF16, N, N, false};
     }
     template <int W, bool ALL>
@@ -93,8 +93,8 @@ struct EpiDh {
         __device__ Row(const EpiDh &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
-    __device__ int stores() const { return 48; }
-    __device__ __forceinline__ Dest dest(int o, int, int) const {
+    __device__ int stores(const Place &) const { return 48; }
+    __device__ __forceinline__ Dest dest(int o, const Place &) const {
         return {o == 0 ? dz : o == 1 ? du : h, TW_T_BF16, N, N, false};
     }
     template <int W, bool ALL>
@@ -188,12 +188,25 @@ hipError_t ffn_dh(const TileArgs &p, const uint16_t *g, const uint16_t *u, uint1
 
 }  // namespace
 
+static SplitPlan down_plan(int M, int K, int N) {
+    return split_plan<1, 1>(TileArgs{{}, {}, N, K, M, K, N}, false);
+}
+static SplitPlan dx_plan(int M, int K, int N) {
+    return split_plan<1, 2>(TileArgs{{}, {}, N, K, M, K, N}, false);
+}
+static SplitPlan dw_plan(int M, int K, int N) {
+    TileArgs p{{}, {}, N, K, N, K, M};
+    p.groups = 3;
+    return split_plan<1, 1>(p, false);
+}
+
 size_t ffn_fwd_part_bytes(int M, int K, int N) {
     if (M <= kFewRowsMax) return (size_t)few_down_splits(K, N) * M * K * 4;
-    return parts_bytes<kRows, kCols, 1, 1>(TileArgs{{}, {}, N, K, M, K, N});
+    return down_plan(M, K, N).bytes;
 }
 size_t ffn_bwd_part_bytes(int M, int K, int N) {
-    return parts_bytes<kRows, kCols, 1, 2>(TileArgs{{}, {}, N, K, M, K, N});
+    const size_t a = dx_plan(M, K, N).bytes, b = dw_plan(M, K, N).bytes;
+    return a > b ? a : b;
 }
 
 hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
@@ -219,7 +232,9 @@ hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, 
         if (e != hipSuccess) return e;
         return launch_sum_parts(part, few_down_splits(K, N), (int64_t)M * K, y, y_type, s);
     }
-    return launch_split<kRows, kCols, 1, 1>(TileArgs{{h}, {wd}, N, K, M, K, N}, y, y_type, part, s);
+    return launch_split<kRows, kCols, 1, 1>(TileArgs{{h}, {wd}, N, K, M, K, N},
+                                            down_plan(M, K, N), EpiStore{{y}, y_type, K, part},
+                                            true, s);
 }
 
 hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const uint16_t *g,
@@ -234,18 +249,20 @@ hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const 
 hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t *wg_t,
                          const uint16_t *wu_t, int M, int K, int N, void *dx, int dx_type,
                          float *part, hipStream_t s) {
-    return launch_split<kRows, kCols, 1, 2>(TileArgs{{dz, du}, {wg_t, wu_t}, N, K, M, K, N}, dx,
-                                            dx_type, part, s);
+    return launch_split<kRows, kCols, 1, 2>(TileArgs{{dz, du}, {wg_t, wu_t}, N, K, M, K, N},
+                                            dx_plan(M, K, N), EpiStore{{dx}, dx_type, K, part},
+                                            true, s);
 }
 
 hipError_t launch_ffn_dw(const uint16_t *dz, const uint16_t *du, const uint16_t *h,
                          const uint16_t *x, int64_t x_stride, const uint16_t *dy, int M, int K,
-                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, hipStream_t s) {
+                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, float *part,
+                         hipStream_t s) {
     TileArgs p{{dz, du, h}, {x, x, dy}, N, x_stride, N, K, M};
     p.groups = 3;
     p.ldb_last = K;
-    return launch_tiles<kCols, kCols, 1, 1>(
-        p, EpiStore{{dwg_t, dwu_t, dwd}, dw_type, nullptr, 0, N, K}, s);
+    return launch_split<kCols, kCols, 1, 1>(
+        p, dw_plan(M, K, N), EpiStore{{dwg_t, dwu_t, dwd}, dw_type, K, part}, true, s);
 }
 
 }  // namespace tw

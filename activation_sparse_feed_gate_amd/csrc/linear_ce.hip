@@ -13,6 +13,8 @@
 //
 // A row whose target is outside [0, V) is left out: its loss and its row of D
 // are 0.
+#include <algorithm>
+
 #include "tw_few.hpp"
 #include "tw_tiles.hpp"
 #include "tw_train.hpp"
@@ -51,7 +53,7 @@ struct EpiSoft {
         __device__ Row(const EpiSoft &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
-    __device__ int stores() const { return 0; }
+    __device__ int stores(const Place &) const { return 0; }
     template <int W, bool ALL>
     __device__ __forceinline__ void most(Row &r, int n, const float (&v)[W]) const {
 #pragma unroll
@@ -201,16 +203,17 @@ struct EpiD {
                     (uint32_t)__shfl((int)hi, l)};
         }
     };
+    // A row without a target has scale 0 and an infinite top, below which every
+    // exponential is 0.
     struct Row {
         float top, scale;
-        int t;  // the target's column of the piece; -1: it has it not, -2: no target
+        int t;  // the target's column of the piece, or -1
         __device__ __forceinline__ Row(const EpiD &e, const Raw &r) {
             const int64_t v = (int64_t)((uint64_t)r.hi << 32 | r.lo);
-            top = r.lse * kLog2e;
-            scale = r.dloss;
-            t = v < 0 || v >= e.V                            ? -2
-                : v >= e.first && v < (int64_t)e.first + e.N ? (int)(v - e.first)
-                                                             : -1;
+            const bool live = v >= 0 && v < e.V;
+            top = live ? r.lse * kLog2e : INFINITY;
+            scale = live ? r.dloss : 0.0f;
+            t = v >= e.first && v < (int64_t)e.first + e.N ? (int)(v - e.first) : -1;
         }
     };
     __device__ __forceinline__ Raw raw(int m) const {
@@ -221,38 +224,48 @@ struct EpiD {
         const int32_t v = static_cast<const int32_t *>(t.p)[m];
         return {lse[m], dloss[m], (uint32_t)v, (uint32_t)(v >> 31)};
     }
-    __device__ __forceinline__ Dest dest(int, int, int) const {
+    __device__ __forceinline__ Dest dest(int, const Place &) const {
         return {d, TW_T_BF16, ldd, (int)ldd, false};
     }
-    __device__ int stores() const { return 16; }
+    __device__ int stores(const Place &) const { return 16; }
     template <int W, bool ALL>
     __device__ __forceinline__ void values(Row &r, int, int n, const float (&v)[W],
                                            const float (&)[W], float (&o)[kOuts][W]) const {
+        float p[W];
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-            float p = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
-            if (n + e == r.t) p -= 1.0f;
-            o[0][e] = r.t != -2 && (ALL || n + e < N) ? p * r.scale : 0.0f;
+        for (int e = 0; e < W; ++e) p[e] = __builtin_amdgcn_exp2f(fmaf(v[e], kLog2e, -r.top));
+        const unsigned at = (unsigned)(r.t - n);  // (few lanes have the target: a branch)
+        if (at < W) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) p[e] -= at == (unsigned)e ? 1.0f : 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < W; ++e) o[0][e] = ALL || n + e < N ? p[e] * r.scale : 0.0f;
     }
 };
 
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The backward pass's pieces of the vocabulary: columns of D in at most 256 MB,
-// and the parts of dx's reduction, which every piece adds to.
+// The backward pass's pieces of the vocabulary: columns of D in at most 512 MB,
+// dx's sums in parts that every piece adds to, a piece's dw.
 struct Pieces {
     int width;
+    SplitPlan dx;
     size_t d_bytes, part_bytes;
-    int splits;
 };
+SplitPlan dw_plan(int M, int K, int width) {
+    return split_plan<1, 1>(TileArgs{{}, {}, 0, 0, width, K, M}, false);
+}
 Pieces pieces_of(int M, int K, int V) {
     Pieces p;
-    const int64_t most = (int64_t)(256 << 20) / 2 / (M > 0 ? M : 1) / 256 * 256;
+    const int64_t most = (int64_t)(512 << 20) / 2 / (M > 0 ? M : 1) / 256 * 256;
     p.width = (int)(most < 256 ? 256 : most < V ? most : V);
     p.d_bytes = up256((size_t)M * ((p.width + 7) / 8 * 8) * 2);
-    p.splits = splits_of<kRows, kCols, 1, 1>(TileArgs{{}, {}, 0, 0, M, K, p.width});
-    p.part_bytes = p.width < V || p.splits > 1 ? up256((size_t)p.splits * M * K * 4) : 0;
+    p.dx = split_plan<1, 1>(TileArgs{{}, {}, 0, 0, M, K, p.width}, p.width < V);
+    // the weight gradient's parts behind them, since dx's stay
+    size_t dw = dw_plan(M, K, p.width).bytes;
+    if (V % p.width) dw = std::max(dw, dw_plan(M, K, V % p.width).bytes);
+    p.part_bytes = up256(p.dx.bytes) + up256(dw);
     return p;
 }
 
@@ -294,7 +307,8 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
                          void *dx, int dx_type, void *dw, int dw_type, void *ws, hipStream_t s) {
     const Pieces pc = pieces_of(M, K, V);
     uint16_t *d = static_cast<uint16_t *>(ws);
-    float *part = pc.part_bytes ? reinterpret_cast<float *>((char *)ws + pc.d_bytes) : nullptr;
+    float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + pc.d_bytes);
+    float *dw_parts = parts + up256(pc.dx.bytes) / 4;
     hipError_t e = hipSuccess;
     for (int first = 0; first < V && e == hipSuccess; first += pc.width) {
         const int N = V - first < pc.width ? V - first : pc.width;
@@ -303,16 +317,17 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
         if (M > 0)
             e = launch_tiles<kRows, kRows, 1, 1>(TileArgs{{x}, {wp}, x_stride, K, M, N, K},
                                                  EpiD{lse, dloss, t, d, ldd, N, first, V}, s);
-        if (e == hipSuccess && dx)
-            e = launch_tiles<kRows, kCols, 1, 1>(TileArgs{{d}, {wp}, ldd, K, M, K, N, pc.splits},
-                                                 EpiStore{{dx}, dx_type, part, first > 0, M, K}, s);
+        if (e == hipSuccess && dx && M > 0)
+            e = launch_split<kRows, kCols, 1, 1>(
+                TileArgs{{d}, {wp}, ldd, K, M, K, N}, pc.dx,
+                EpiStore{{dx}, dx_type, K, parts, first > 0}, first + N == V, s);
         if (e == hipSuccess && dw) {
             char *out = static_cast<char *>(dw) + (int64_t)first * K * (dw_type == TW_T_F32 ? 4 : 2);
-            e = launch_tiles<kCols, kCols, 1, 1>(TileArgs{{d}, {x}, ldd, x_stride, N, K, M},
-                                                 EpiStore{{out}, dw_type, nullptr, 0, N, K}, s);
+            e = launch_split<kCols, kCols, 1, 1>(TileArgs{{d}, {x}, ldd, x_stride, N, K, M},
+                                                 dw_plan(M, K, N),
+                                                 EpiStore{{out}, dw_type, K, dw_parts}, true, s);
         }
     }
-    if (e == hipSuccess && dx && part) e = launch_sum_parts(part, pc.splits, (int64_t)M * K, dx, dx_type, s);
     return e;
 }
 

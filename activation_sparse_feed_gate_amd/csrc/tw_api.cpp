@@ -1233,7 +1233,7 @@ tw_status tw_gated_ffn_bwd(const uint16_t *dy, const uint16_t *x, int64_t x_stri
     TW_TRY(record(events, 2, s));
     if (dwg_t)
         TW_TRY(launched(tw::launch_ffn_dw(dz, du, h, x, x_stride, dy, M, K, N, dwg_t, dwu_t, dwd,
-                                          dw_type, s),
+                                          dw_type, part, s),
                         "weight-gradient launch"));
     return record(events, 3, s);
 }

@@ -23,6 +23,12 @@ enum { kRows = 0, kCols = 1 };
 constexpr uint32_t kPastEnd = 1u << 30;
 constexpr int64_t kMaxStride = 1 << 20;  // elements between operand rows
 
+// A tile of an output: its product, its first row and column, its side, and its place
+// among the parts (-1: it takes the whole reduction).
+struct Place {
+    int z, m0, n0, side, part;
+};
+
 // The operands of one launch.  What a[1], b[1], ... are is the kernel's: a
 // second weight matrix next to b[0] (NB = 2), a second term of the sum (SEG =
 // 2: the reduction runs over both), or other products of the same shape.
@@ -30,7 +36,8 @@ struct TileArgs {
     const uint16_t *a[3], *b[3];
     int64_t lda, ldb;  // elements between rows
     int M, N, R;
-    int splits = 1;  // parts of the reduction
+    int splits = 1;  // parts of the reduction, where it is taken in parts
+    int full = 0;    // (larger tiles) the first tiles, which take the reduction whole
     int groups = 1;  // products of the same shape: a[z], b[z]
     int64_t ldb_last = 0;  // ldb of the third product
 };
@@ -165,9 +172,9 @@ struct RingOperand {
 //   values<W, ALL>(row, m, n, v, u, o)  makes its kOuts outputs of columns n .. n + W
 //                                - 1 from those of the product (u: of the second
 //                                weights); ALL: these columns are all within N,
-//   dest(o, z, split)            says where output o goes,
-//   stores()                     how many stores a wave of the larger tiles makes of a
-//                                whole tile, or,
+//   dest(o, place)               says where output o of a tile goes,
+//   stores(place)                how many stores a wave of the larger tiles makes of a
+//                                tile inside the product, or,
 // where it reduces over the columns (kStats),
 //   most<W, ALL>(row, n, v), add<W, ALL>(row, n, v)   two passes over a lane's columns,
 //   join<L>(row)                            lanes l and l ^ L hold one row,
@@ -238,6 +245,8 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
     const int all = SEG * KT, per = (all + p.splits - 1) / p.splits;
     kloop_pipelined<kRingS, NI>(min(sp * per, all), min(sp * per + per, all), smem, STAGE, issue,
                                 load, mma);
+    const int part = p.splits > 1 ? (sp * p.groups + z) * (int)gridDim.x + (int)blockIdx.x : -1;
+    const Place at{z, m0, n0, kRingBM, part};
     if constexpr (Epi::kStats) __syncthreads();  // finish() uses the ring's memory
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -263,10 +272,10 @@ __global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
         } else if (m < p.M) {
             each([&](int n, auto &v, auto &u) {
                 float out[Epi::kOuts][4];
-                if (n >= epi.dest(0, z, sp).cols) return;
+                if (n >= epi.dest(0, at).cols) return;
                 epi.template values<4, false>(row, m, n, v, u, out);
 #pragma unroll
-                for (int o = 0; o < Epi::kOuts; ++o) put_out<4>(epi.dest(o, z, sp), m, n, out[o]);
+                for (int o = 0; o < Epi::kOuts; ++o) put_out<4>(epi.dest(o, at), m, n, out[o]);
             });
         }
     }
@@ -352,10 +361,12 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     const int KT = (p.R + kWideK - 1) / kWideK;  // stages of one term
     const int all = SEG * KT, per = (all + p.splits - 1) / p.splits;
     const int nbm = (p.M + kWideTile - 1) / kWideTile, nbn = (p.N + BN - 1) / BN;
-    const int tiles = nbm * nbn, items = tiles * p.groups * p.splits;
+    // Items: the first p.full tiles whole, then the others in p.splits parts.
+    const int tiles = nbm * nbn, rest = tiles * p.groups - p.full;
+    const int items = p.full + rest * p.splits;
 
     // The item being loaded: its tile, product, part of the reduction.
-    int m0, n0, z, sp, k0, kn;
+    int m0, n0, z, part, k0, kn;
     int64_t ldb;
     rsrc_t ra[SEG], rb[SEG == 2 ? 2 : NB];  // (kRows)
     // Lane's place in a load.  kRows: 8 rows of a group of 64, rows 8 wave ..+7,
@@ -367,16 +378,24 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     const int cchunk = (lane & 15) ^ (2 * ((crow & 3) | ((crow >> 3) & 1) << 2));
     uint32_t va[2], vb[2];  // offsets; kCols: of the two regions
     auto at_item = [&](int t) {
-        const int unit = t / tiles;
-        z = unit / p.splits;
-        sp = unit % p.splits;
+        int tile = t;
+        part = -1;
+        k0 = 0;
+        kn = all;
+        if (t >= p.full) {
+            const int sp = (t - p.full) / rest;
+            part = t - p.full;
+            tile = p.full + part - sp * rest;
+            k0 = min(sp * per, all);
+            kn = min(k0 + per, all) - k0;
+        }
+        z = tile / tiles;
+        tile -= z * tiles;
         ldb = z == 2 ? p.ldb_last : p.ldb;
-        k0 = min(sp * per, all);
-        kn = min(k0 + per, all) - k0;
         int bm, bn;
-        if (row_regions == 8) xcd_tile<8>(t % tiles, nbm, nbn, bm, bn);
-        else if (row_regions == 4) xcd_tile<4>(t % tiles, nbm, nbn, bm, bn);
-        else xcd_tile<2>(t % tiles, nbm, nbn, bm, bn);
+        if (row_regions == 8) xcd_tile<8>(tile, nbm, nbn, bm, bn);
+        else if (row_regions == 4) xcd_tile<4>(tile, nbm, nbn, bm, bn);
+        else xcd_tile<2>(tile, nbm, nbn, bm, bn);
         m0 = bm * kWideTile;
         n0 = bn * BN;
         const int pad = (p.R + 7) & ~7;  // a row's last piece may lie in its padding
@@ -579,7 +598,8 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     typename Epi::Raw raw = load_raw(), next = raw;
     load_first();
     for (int t = blockIdx.x; t < items; t += gridDim.x) {
-        const int mt = m0, nt = n0, zt = z, st = sp, n = kn;  // m0, ... move on below
+        const int mt = m0, nt = n0, n = kn;  // m0, ... move on below
+        const Place at{z, m0, n0, kWideTile, part};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -695,7 +715,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                             acc[b >> 1][4 * (b & 1) + j];
                     __builtin_amdgcn_wave_barrier();
                 };
-                const int cols = epi.dest(0, zt, st).cols;
+                const int cols = epi.dest(0, at).cols;
                 enter(0);
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
@@ -721,14 +741,14 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                         epi.template values<8, ALL>(row, m, n, v[q], v[q], o);
 #pragma unroll
                         for (int k = 0; k < Epi::kOuts; ++k)
-                            put_out<8>(epi.dest(k, zt, st), m, n, o[k]);
+                            put_out<8>(epi.dest(k, at), m, n, o[k]);
                     }
                 }
             } else {
                 // The outputs (bf16) go through LDS, 32 rows of 128 bytes at a time.
 #pragma unroll
                 for (int i0 = 0; i0 < 4; i0 += 2) {
-                    if (nw >= epi.dest(0, zt, st).cols) continue;
+                    if (nw >= epi.dest(0, at).cols) continue;
                     float o[2][4][Epi::kOuts][4];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -746,7 +766,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                     }
 #pragma unroll
                     for (int k = 0; k < Epi::kOuts; ++k) {
-                        const Dest d = epi.dest(k, zt, st);
+                        const Dest d = epi.dest(k, at);
                         if (!d.p) continue;
                         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -778,9 +798,15 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         if (inside) write(std::true_type{});
         else write(std::false_type{});
         // at least so many stores of this tile are younger than the next one's loads
-        after = inside ? epi.stores() : 0;
+        after = inside ? epi.stores(at) : 0;
         raw = next;
     }
+}
+
+template <int NB>
+int64_t wide_tiles(const TileArgs &p) {  // of all products
+    return ((int64_t)p.M + kWideTile - 1) / kWideTile *
+           (((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB)) * p.groups;
 }
 
 template <int LA, int LB, int NB, int SEG, class Epi>
@@ -790,46 +816,48 @@ hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
     const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
-    const int64_t items = nbm * nbn * p.groups * p.splits;
+    const int64_t items = p.full + (wide_tiles<NB>(p) - p.full) * p.splits;
     kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), kWideThreads, kWideBytes, s>>>(
         p, wide_row_regions(nbm, nbn), epi);
     return hipGetLastError();
 }
 
 // The larger tiles where their number leaves few CUs idle (to be measured).
-template <int LA, int LB, int NB, int SEG>
-bool use_wide(const TileArgs &p) {
-    const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
-    const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
-    return p.R > 0 && nbm * nbn * p.groups * p.splits >= 128;
-}
 template <int LA, int LB, int NB, int SEG, class Epi>
-hipError_t launch_tiles(const TileArgs &p, const Epi &epi, hipStream_t s) {
-    if (use_wide<LA, LB, NB, SEG>(p)) return launch_wide<LA, LB, NB, SEG>(p, epi, s);
+hipError_t launch_tiles(TileArgs p, const Epi &epi, hipStream_t s) {
+    static const char *force = getenv("TW_FORCE");
+    if (p.R > 0 && (force ? force[0] == 'w' : wide_tiles<NB>(p) >= 128)) {
+        p.full = (int)wide_tiles<NB>(p);
+        return launch_wide<LA, LB, NB, SEG>(p, epi, s);
+    }
     return launch_ring<LA, LB, NB, SEG>(p, epi, s);
 }
 
 // ------------------------------- epilogues ----------------------------------
-// Outputs stored as they are: to out[z] in its type, or, where the reduction
-// is taken in parts, to part[split] in fp32 (added to what is there with
-// `more`: a later piece of the reduction).
+// Outputs stored as they are: to out[z] in its type, or, where a tile takes a part of
+// the reduction, to that part in fp32 (added to what is there with `more`: a later
+// piece of the reduction).  A part holds its tile alone, side x side.
 struct EpiStore {
     static constexpr bool kStats = false;
     static constexpr int kOuts = 1;
     void *out[3];
     int type;
-    float *part;  // or null
+    int N;
+    float *parts;
     int more;
-    int M, N;
     typedef NoRaw Raw;
     struct Row {
         __device__ Row(const EpiStore &, Raw) {}
     };
     __device__ Raw raw(int) const { return {}; }
-    __device__ int stores() const { return part || type == TW_T_F32 ? 32 : 16; }
-    __device__ __forceinline__ Dest dest(int, int z, int split) const {
-        if (part) return {part + (int64_t)split * M * N, TW_T_F32, N, N, more != 0};
-        return {z == 0 ? out[0] : z == 1 ? out[1] : out[2], type, N, N, false};
+    __device__ int stores(const Place &p) const {
+        return p.part >= 0 || type == TW_T_F32 ? 32 : 16;
+    }
+    __device__ __forceinline__ Dest dest(int, const Place &p) const {
+        if (p.part >= 0)
+            return {parts + (int64_t)p.part * p.side * p.side - ((int64_t)p.m0 * p.side + p.n0),
+                    TW_T_F32, p.side, N, more != 0};
+        return {p.z == 0 ? out[0] : p.z == 1 ? out[1] : out[2], type, N, N, false};
     }
     template <int W, bool ALL>
     __device__ __forceinline__ void values(Row &, int, int, const float (&v)[W], const float (&)[W],
@@ -842,7 +870,7 @@ struct EpiStore {
 // out = the sum of the parts, in their order.
 template <int T>
 __global__ __launch_bounds__(64) void sum_parts_kernel(const float *__restrict__ part, int splits,
-                                                        int64_t n, void *__restrict__ out) {
+                                                       int64_t n, void *__restrict__ out) {
     const int64_t at = ((int64_t)blockIdx.x * 64 + threadIdx.x) * 4;
     if (at >= n) return;
     f32x4 v = *reinterpret_cast<const f32x4 *>(part + at);
@@ -859,45 +887,99 @@ inline hipError_t launch_sum_parts(const float *part, int splits, int64_t n, voi
     return hipGetLastError();
 }
 
-// Parts of the reduction for a product of few output tiles, so that its work
-// fills the chip: the number (up to 8) with the least estimated time, from the rounds
-// of the larger tiles, 1.5 us a stage, and the parts' way through memory (8 bytes
-// an output and part at 4.5 TB/s).
-template <int LA, int LB, int NB, int SEG>
-int splits_of(const TileArgs &p) {
-    const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
-    const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
-    const int64_t stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
-    int best = 1;
-    double least = 0.0;
-    for (int s = 1; s <= 8 && s <= stages; ++s) {
+// The same for tiles of SIDE x SIDE: part s of tile full + i lies at (s rest + i) SIDE^2.
+template <int SIDE>
+__global__ __launch_bounds__(256) void sum_tiles_kernel(const float *__restrict__ parts, int splits,
+                                                        int rest, int full, int row_regions,
+                                                        int nbm, int nbn, EpiStore epi, int M) {
+    constexpr int kBlocks = SIDE * SIDE / 1024;  // workgroups a tile
+    const int i = blockIdx.x / kBlocks;
+    int tile = full + i;
+    const int z = tile / (nbm * nbn);
+    tile -= z * (nbm * nbn);
+    int bm, bn;
+    if (row_regions == 8) xcd_tile<8>(tile, nbm, nbn, bm, bn);
+    else if (row_regions == 4) xcd_tile<4>(tile, nbm, nbn, bm, bn);
+    else xcd_tile<2>(tile, nbm, nbn, bm, bn);
+    const int at = (blockIdx.x % kBlocks * 256 + threadIdx.x) * 4;
+    const int m = bm * SIDE + at / SIDE, n = bn * SIDE + at % SIDE;
+    if (m >= M || n >= epi.N) return;
+    const float *q = parts + (int64_t)i * (SIDE * SIDE) + at;
+    f32x4 v = *reinterpret_cast<const f32x4 *>(q);
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s)
+        v += *reinterpret_cast<const f32x4 *>(q + (int64_t)s * rest * (SIDE * SIDE));
+    store4(z == 0 ? epi.out[0] : z == 1 ? epi.out[1] : epi.out[2], epi.type,
+           (int64_t)m * epi.N + n, v);
+}
+
+// How a product stored as it is takes its tiles: the first `full` of the larger ones whole
+// and the rest in `splits` parts, or the smaller tiles in `splits` parts.
+struct SplitPlan {
+    bool wide;
+    int splits, full;
+    size_t bytes;  // of the parts
+};
+// The plan of the least estimated time (us): 1.6 a stage and round of the larger tiles,
+// 0.7 of the smaller ones' 32-deep stages; the parts' way through memory, 8 bytes an
+// output and part at 4.5 TB/s.  `pieces`: the reduction comes in pieces, every
+// tile keeps its parts from one to the next.
+template <int NB, int SEG>
+SplitPlan split_plan(const TileArgs &p, bool pieces) {
+    const int64_t big = wide_tiles<NB>(p), stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
+    const int64_t small = ((int64_t)p.M + 127) / 128 * (((int64_t)p.N + 127) / 128) * p.groups;
+    SplitPlan best{};
+    double least = 1e30;
+    auto offer = [&](bool wide, int64_t full, int s, double us) {
+        if (us >= least) return;
+        least = us;
+        const int64_t rest = wide ? big - full : small, side = wide ? 256 : 128;
+        const bool parts = pieces || s > 1;
+        best = {wide, s, (int)(parts ? full : wide ? big : 0),
+                parts ? (size_t)rest * s * side * side * 4 : 0};
+    };
+    const int64_t whole = pieces ? 0 : big / kWideGrid * kWideGrid;
+    for (int s = 1; s <= 64 && s <= stages; ++s) {
         const int64_t per = (stages + s - 1) / s;
         if ((stages + per - 1) / per != s) continue;  // (every part has a stage)
-        const int64_t rounds = (nbm * nbn * p.groups * s + kWideGrid - 1) / kWideGrid;
-        const double us = 1.5 * rounds * per +
-                          (s > 1 ? 3.0 + (double)s * p.M * p.N * p.groups * 8 / 4.5e6 : 0.0);
-        if (s == 1 || us < least) {
-            best = s;
-            least = us;
-        }
+        auto parts_us = [&](int64_t tiles, int64_t side) {
+            return s == 1 && !pieces ? 0.0 : 3.0 + (double)tiles * s * side * side * 8 / 4.5e6;
+        };
+        const int64_t full = s == 1 ? 0 : whole, rest = big - full;
+        offer(true, full, s,
+              1.6 * (full / kWideGrid * stages + (rest * s + kWideGrid - 1) / kWideGrid * per) +
+                  parts_us(rest, 256));
+        if (!pieces)
+            offer(false, 0, s,
+                  0.7 * ((small * s + kWideGrid - 1) / kWideGrid) * 2 * per + parts_us(small, 128));
     }
     return best;
 }
-template <int LA, int LB, int NB, int SEG>
-size_t parts_bytes(const TileArgs &p) {
-    const int s = splits_of<LA, LB, NB, SEG>(p);
-    return s > 1 ? (size_t)s * p.M * p.N * 4 : 0;
-}
 
-// A product stored as it is, its reduction in parts where that is faster; part:
-// parts_bytes.
+// A product stored as it is.  parts: split_plan's bytes; `last`: the sums are to be
+// stored (with pieces: of the last one).
 template <int LA, int LB, int NB, int SEG>
-hipError_t launch_split(TileArgs p, void *out, int type, float *part, hipStream_t s) {
-    p.splits = splits_of<LA, LB, NB, SEG>(p);
-    const EpiStore epi{{out}, type, p.splits > 1 ? part : nullptr, 0, p.M, p.N};
-    const hipError_t e = launch_tiles<LA, LB, NB, SEG>(p, epi, s);
-    if (e != hipSuccess || p.splits == 1) return e;
-    return launch_sum_parts(part, p.splits, (int64_t)p.M * p.N, out, type, s);
+hipError_t launch_split(TileArgs p, const SplitPlan &plan, EpiStore epi, bool last, hipStream_t s) {
+    p.splits = plan.splits;
+    p.full = plan.full;
+    if (p.R == 0) {  // zeros
+        p.splits = 1;
+        return launch_ring<LA, LB, NB, SEG>(p, epi, s);
+    }
+    const hipError_t e = plan.wide ? launch_wide<LA, LB, NB, SEG>(p, epi, s)
+                                   : launch_ring<LA, LB, NB, SEG>(p, epi, s);
+    if (e != hipSuccess || !plan.bytes || !last) return e;
+    const int side = plan.wide ? 256 : 128;
+    const int nbm = (p.M + side - 1) / side, nbn = (p.N + side - 1) / side;
+    const int rest = nbm * nbn * p.groups - plan.full;
+    const unsigned grid = (unsigned)(side * side / 1024) * rest;
+    if (plan.wide)
+        sum_tiles_kernel<256><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full,
+                                                   wide_row_regions(nbm, nbn), nbm, nbn, epi, p.M);
+    else
+        sum_tiles_kernel<128><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, 0, 2, nbm, nbn,
+                                                   epi, p.M);
+    return hipGetLastError();
 }
 
 }  // namespace tw

@@ -29,7 +29,7 @@ hipError_t launch_rmsnorm_bwd(const void *dy, int dy_type, const void *x, int x_
 enum { TW_A_RELU = 0, TW_A_SILU = 1, TW_A_GELU = 2 };
 
 // The gated FFN (gated_ffn.hip).  h: [M][N] bf16 scratch, part: scratch of
-// ffn_fwd_part_bytes (down) or ffn_bwd_part_bytes (dx).  g and u (the
+// ffn_fwd_part_bytes (down) or ffn_bwd_part_bytes (dx, dw).  g and u (the
 // projections before the activation) are optional outputs.
 size_t ffn_fwd_part_bytes(int M, int K, int N);
 size_t ffn_bwd_part_bytes(int M, int K, int N);
@@ -47,7 +47,8 @@ hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t 
                          float *part, hipStream_t s);
 hipError_t launch_ffn_dw(const uint16_t *dz, const uint16_t *du, const uint16_t *h,
                          const uint16_t *x, int64_t x_stride, const uint16_t *dy, int M, int K,
-                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, hipStream_t s);
+                         int N, void *dwg_t, void *dwu_t, void *dwd, int dw_type, float *part,
+                         hipStream_t s);
 
 // Cross entropy of x w^T (linear_ce.hip).  Targets are 32- or 64-bit integers;
 // one outside [0, V) leaves its row out.

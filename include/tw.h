@@ -641,7 +641,7 @@ tw_status tw_linear_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *
  *   dx      [M][K]  bf16 or fp32, or NULL;  dw [V][K] bf16 or fp32, or NULL
  *
  * Limits as in the forward.  With M = 0, dw is zeros.  ws_bytes >=
- * tw_linear_ce_bwd_workspace_bytes(M, K, V): a piece of D (at most 256 MB, or
+ * tw_linear_ce_bwd_workspace_bytes(M, K, V): a piece of D (at most 512 MB, or
  * 256 columns) and fp32 sums of dx.
  */
 size_t tw_linear_ce_bwd_workspace_bytes(int M, int K, int V);
