@@ -113,51 +113,71 @@ struct EpiDh {
     }
 };
 
-// Up to 16 token rows: a workgroup takes 16 C hidden neurons of both matrices, its 8
-// waves a slice of K each; their sums meet in LDS.
+// Up to 64 token rows (16 MB): a workgroup takes up to 16 C hidden neurons of both
+// matrices, its 8 waves a slice of K each; their sums meet in LDS.
 constexpr int kFewUpThreads = 512;
-template <int ACT, int C>
+template <int ACT, int C, int MB>
 __global__ __launch_bounds__(kFewUpThreads) void few_up_kernel(
     const uint16_t *__restrict__ x, int64_t x_stride, const uint16_t *__restrict__ wg_t,
     const uint16_t *__restrict__ wu_t, int M, int K, int N, int share, uint16_t *__restrict__ g,
     uint16_t *__restrict__ u, uint16_t *__restrict__ h) {
     constexpr int NW = kFewUpThreads / kWave;
-    __shared__ __attribute__((aligned(16))) float sums[NW][2 * C][kWave][4];
+    extern __shared__ __attribute__((aligned(16))) char smem[];  // [NW][2 C MB][64] f32x4
+    f32x4 *sums = reinterpret_cast<f32x4 *>(smem);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n0 = blockIdx.x * share, n1 = min(n0 + share, N);
     const int k8 = 8 * (lane >> 4);
-    const uint16_t *wp[2 * C];
+    const uint16_t *wp[2 * C], *xp[MB];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t row = min(n0 + 16 * c + (lane & 15), n1 - 1);
         wp[2 * c] = wg_t + row * K + k8;
         wp[2 * c + 1] = wu_t + row * K + k8;
     }
-    const uint16_t *xp = x + min(lane & 15, M - 1) * x_stride + k8;
+#pragma unroll
+    for (int m = 0; m < MB; ++m) xp[m] = x + min(16 * m + (lane & 15), M - 1) * x_stride + k8;
     const int steps = (K + 31) / 32, per = (steps + NW - 1) / NW;
-    f32x4 acc[2 * C] = {};
-    few_product<2 * C, 4 / C>(wp, xp, K, wave * per, min(wave * per + per, steps), acc);
+    f32x4 acc[2 * C][MB] = {};
+    constexpr int U = 10 / (2 * C + MB) < 1 ? 1 : 10 / (2 * C + MB);  // loads in flight
+    few_product<2 * C, MB, U>(wp, xp, K, wave * per, min(wave * per + per, steps), acc);
 #pragma unroll
-    for (int b = 0; b < 2 * C; ++b) *reinterpret_cast<f32x4 *>(sums[wave][b][lane]) = acc[b];
+    for (int b = 0; b < 2 * C; ++b)
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+            sums[((wave * 2 * C + b) * MB + m) * kWave + lane] = acc[b][m];
     __syncthreads();
-    if (wave >= C) return;
-    f32x4 v{}, w{};
+    for (int i = wave; i < C * MB; i += NW) {  // block i / MB of neurons, i % MB of rows
+        f32x4 v{}, w{};
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        v += *reinterpret_cast<const f32x4 *>(sums[i][2 * wave][lane]);
-        w += *reinterpret_cast<const f32x4 *>(sums[i][2 * wave + 1][lane]);
-    }
-    const int m = lane & 15;
-    if (m >= M) return;
+        for (int q = 0; q < NW; ++q) {
+            v += sums[((q * 2 * C + 2 * (i / MB)) * MB + i % MB) * kWave + lane];
+            w += sums[((q * 2 * C + 2 * (i / MB) + 1) * MB + i % MB) * kWave + lane];
+        }
+        const int m = 16 * (i % MB) + (lane & 15);
+        if (m >= M) continue;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int n = 16 * wave + 4 * (lane >> 4) + e;
-        if (n0 + n >= n1) continue;
-        const int64_t at = (int64_t)m * N + n0 + n;
-        h[at] = (uint16_t)pack_bf16(activate<ACT>(v[e]) * w[e], 0.0f);
-        if (g) g[at] = (uint16_t)pack_bf16(v[e], 0.0f);
-        if (u) u[at] = (uint16_t)pack_bf16(w[e], 0.0f);
+        for (int e = 0; e < 4; ++e) {
+            const int n = n0 + 16 * (i / MB) + 4 * (lane >> 4) + e;
+            if (n >= n1) continue;
+            const int64_t at = (int64_t)m * N + n;
+            h[at] = (uint16_t)pack_bf16(activate<ACT>(v[e]) * w[e], 0.0f);
+            if (g) g[at] = (uint16_t)pack_bf16(v[e], 0.0f);
+            if (u) u[at] = (uint16_t)pack_bf16(w[e], 0.0f);
+        }
     }
+}
+
+template <int ACT, int C, int MB>
+hipError_t few_up_as(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
+                     const uint16_t *wu_t, int M, int K, int N, int share, uint16_t *g,
+                     uint16_t *u, uint16_t *h, hipStream_t s) {
+    constexpr auto kernel = &few_up_kernel<ACT, C, MB>;
+    constexpr int lds = kFewUpThreads / kWave * 2 * C * MB * kWave * 16;
+    const hipError_t e = lds_limit_once<kernel>(lds);
+    if (e != hipSuccess) return e;
+    kernel<<<(unsigned)((N + share - 1) / share), kFewUpThreads, lds, s>>>(
+        x, x_stride, wg_t, wu_t, M, K, N, share, g, u, h);
+    return hipGetLastError();
 }
 
 template <int ACT>
@@ -166,14 +186,16 @@ hipError_t few_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t, con
     // an even share of the neurons for each of 256 workgroups, at most 32
     int share = (N + 255) / 256;
     share = share < 4 ? 4 : share > 32 ? 32 : share;
-    const unsigned grid = (unsigned)((N + share - 1) / share);
-    if (share <= 16)
-        few_up_kernel<ACT, 1><<<grid, kFewUpThreads, 0, s>>>(x, x_stride, wg_t, wu_t, M, K, N,
-                                                             share, g, u, h);
-    else
-        few_up_kernel<ACT, 2><<<grid, kFewUpThreads, 0, s>>>(x, x_stride, wg_t, wu_t, M, K, N,
-                                                             share, g, u, h);
-    return hipGetLastError();
+    auto go = [&](auto c, auto mb) {
+        return few_up_as<ACT, decltype(c)::value, decltype(mb)::value>(
+            x, x_stride, wg_t, wu_t, M, K, N, share, g, u, h, s);
+    };
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, 4> four{};
+    const int mb = few_blocks_of(M);
+    if (share <= 16) return mb == 1 ? go(one, one) : mb == 2 ? go(one, two) : go(one, four);
+    return mb == 1 ? go(two, one) : mb == 2 ? go(two, two) : go(two, four);
 }
 
 template <int ACT>
@@ -201,7 +223,7 @@ static SplitPlan dw_plan(int M, int K, int N) {
 }
 
 size_t ffn_fwd_part_bytes(int M, int K, int N) {
-    if (M <= kFewRowsMax) return (size_t)few_down_splits(K, N) * M * K * 4;
+    if (M <= kFewDownMax) return (size_t)few_down_splits(K, N) * M * K * 4;
     return down_plan(M, K, N).bytes;
 }
 size_t ffn_bwd_part_bytes(int M, int K, int N) {
@@ -227,7 +249,7 @@ hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg
 
 hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, int N, void *y,
                            int y_type, float *part, hipStream_t s) {
-    if (M <= kFewRowsMax) {
+    if (M <= kFewDownMax) {
         const hipError_t e = launch_few_down(h, wd, M, K, N, part, s);
         if (e != hipSuccess) return e;
         return launch_sum_parts(part, few_down_splits(K, N), (int64_t)M * K, y, y_type, s);

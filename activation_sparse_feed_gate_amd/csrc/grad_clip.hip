@@ -71,6 +71,7 @@ __global__ __launch_bounds__(kClipThreads) void square_sums_kernel(Table t,
 // The parts' sum, the same in every thread.
 __device__ double sum_of_parts(const float *part, int parts, double *lds) {
     double s = 0.0;
+#pragma unroll 8
     for (int i = threadIdx.x; i < parts; i += blockDim.x) s += part[i];
 #pragma unroll
     for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o);

@@ -91,37 +91,42 @@ struct EpiSoft {
     }
 };
 
-// Up to 16 token rows: a wave takes 32 words and all of K, a workgroup of 4 waves
-// the 128 of a column block.
+// Up to 64 token rows (16 MB): a wave takes 32 words and all of K, a workgroup of 4
+// waves the 128 of a column block.
 constexpr int kFewSoftThreads = 256;
+template <int MB>
 __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
     const uint16_t *__restrict__ x, int64_t x_stride, const uint16_t *__restrict__ w, int M, int K,
     int V, Soft *__restrict__ part) {
-    __shared__ Soft all[kFewSoftThreads / kWave][16];
+    __shared__ Soft all[kFewSoftThreads / kWave][16 * MB];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int v0 = blockIdx.x * 128 + 32 * wave;
     const int k8 = 8 * (lane >> 4);
-    const uint16_t *wp[2];
+    const uint16_t *wp[2], *xp[MB];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
         wp[b] = w + (int64_t)min(v0 + 16 * b + (lane & 15), V - 1) * K + k8;
-    const uint16_t *xp = x + min(lane & 15, M - 1) * x_stride + k8;
-    f32x4 acc[2] = {};
-    few_product<2, 6>(wp, xp, K, 0, (K + 31) / 32, acc);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) xp[m] = x + min(16 * m + (lane & 15), M - 1) * x_stride + k8;
+    f32x4 acc[2][MB] = {};
+    few_product<2, MB, 18 / (2 + MB)>(wp, xp, K, 0, (K + 31) / 32, acc);
     const EpiSoft epi{part, M, V};
-    EpiSoft::Row row(epi, {});
-    float l[2][4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int m = 0; m < MB; ++m) {
+        EpiSoft::Row row(epi, {});
+        float l[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) l[b][e] = acc[b][e];
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) epi.most<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+            for (int e = 0; e < 4; ++e) l[b][e] = acc[b][m][e];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) epi.add<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
-    epi.join<16>(row);
-    epi.join<32>(row);
-    if (lane < 16) all[wave][lane] = {row.top, row.sum};
+        for (int b = 0; b < 2; ++b) epi.most<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) epi.add<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+        epi.join<16>(row);
+        epi.join<32>(row);
+        if (lane < 16) all[wave][16 * m + lane] = {row.top, row.sum};
+    }
     __syncthreads();
     if (threadIdx.x >= M) return;
     Soft j = all[0][threadIdx.x];
@@ -282,7 +287,13 @@ hipError_t launch_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w,
     Soft *part = static_cast<Soft *>(ws);
     hipError_t e;
     if (M <= kFewRowsMax) {
-        few_soft_kernel<<<(V + 127) / 128, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
+        const int mb = few_blocks_of(M), grid = (V + 127) / 128;
+        if (mb == 1)
+            few_soft_kernel<1><<<grid, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
+        else if (mb == 2)
+            few_soft_kernel<2><<<grid, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
+        else
+            few_soft_kernel<4><<<grid, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
         e = hipGetLastError();
     } else {
         e = launch_tiles<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, s);

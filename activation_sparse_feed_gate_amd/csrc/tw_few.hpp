@@ -1,4 +1,4 @@
-// tw_few.hpp -- products of up to 16 token rows with a weight matrix that is
+// tw_few.hpp -- products of up to 64 token rows with a weight matrix that is
 // streamed once from memory: the rows of a decoded batch.
 //
 // Weight fragments come straight from memory into registers (no other wave reads
@@ -12,18 +12,24 @@
 
 namespace tw {
 
-constexpr int kFewRowsMax = 16;
+constexpr int kFewRowsMax = 64;   // of the products that stream weight rows
+constexpr int kFewDownMax = 16;   // of few_down_kernel
 
-// acc[b] += w rows of block b times the token rows, over the steps [s0, s1) of 32
-// reduction elements.  wp[b]: the lane's weight row (l % 16 of each 16) and xp: its
-// token row, both at reduction element 8 (l / 16); a piece past K is zero on both
-// sides.  A lane of acc[b] holds token l % 16, weight rows 4 (l / 16) + r.
-template <int NBLK, int U>
-__device__ __forceinline__ void few_product(const uint16_t *const (&wp)[NBLK], const uint16_t *xp,
-                                            int K, int s0, int s1, f32x4 (&acc)[NBLK]) {
+// Blocks of 16 token rows that M rows take, rounded up to a power of 2.
+constexpr int few_blocks_of(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }
+
+// acc[b][m] += weight rows of block b times token rows of block m, over the steps
+// [s0, s1) of 32 reduction elements.  wp[b]: the lane's weight row (l % 16 of each
+// 16) and xp[m]: its token row, both at reduction element 8 (l / 16); a piece past K
+// is zero on both sides.  A lane of acc[b][m] holds token l % 16, weight rows 4 (l /
+// 16) + r.
+template <int NBLK, int MB, int U>
+__device__ __forceinline__ void few_product(const uint16_t *const (&wp)[NBLK],
+                                            const uint16_t *const (&xp)[MB], int K, int s0, int s1,
+                                            f32x4 (&acc)[NBLK][MB]) {
     const int lane8 = 8 * ((threadIdx.x & 63) >> 4);
     struct Batch {
-        u32x4 w[U][NBLK], x[U];
+        u32x4 w[U][NBLK], x[U][MB];
     };
     auto load = [&](Batch &b, int s) {
 #pragma unroll
@@ -32,7 +38,8 @@ __device__ __forceinline__ void few_product(const uint16_t *const (&wp)[NBLK], c
             const int k = 32 * (s + i);
             const bool in = s + i < s1 && k + lane8 < K;
             const int at = in ? k : -lane8;
-            b.x[i] = ld16(xp + at);
+#pragma unroll
+            for (int m = 0; m < MB; ++m) b.x[i][m] = ld16(xp[m] + at);
 #pragma unroll
             for (int n = 0; n < NBLK; ++n) b.w[i][n] = ld16(wp[n] + at);
         }
@@ -41,12 +48,17 @@ __device__ __forceinline__ void few_product(const uint16_t *const (&wp)[NBLK], c
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const bool in = s + i < s1 && 32 * (s + i) + lane8 < K;
-            const u32x4 x = in ? b.x[i] : u32x4{};
+            u32x4 x[MB];
+#pragma unroll
+            for (int m = 0; m < MB; ++m) x[m] = in ? b.x[i][m] : u32x4{};
 #pragma unroll
             for (int n = 0; n < NBLK; ++n) {
                 const u32x4 w = in ? b.w[i][n] : u32x4{};
-                acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc[n], 0, 0, 0);
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+                    acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x[m]), acc[n][m],
+                        0, 0, 0);
             }
         }
     };
