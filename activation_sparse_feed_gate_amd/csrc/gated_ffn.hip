@@ -44,12 +44,13 @@ struct Slope {
 template <int ACT>
 __device__ __forceinline__ Slope activate_slope(float g) {
     if constexpr (ACT == TW_A_RELU) return {g <= 0.0f ? 0.0f : g, g <= 0.0f ? 0.0f : 1.0f};
+    // s (1 + g a' (1 - s)).  GELU's g a' grows as g^3, but s is 0 or 1 long before |g| =
+    // 16, so it is taken there: 0 times an infinity would be NaN.
     const bool silu = ACT == TW_A_SILU;
     const float s = logistic(silu ? g : kGelu * g * (1.0f + kGelu3 * g * g));
-    const float da = silu ? 1.0f : kGelu * (1.0f + 3.0f * kGelu3 * g * g);
-    const float t = s * (1.0f - s);
-    // t = 0 far from 0, where g da may be infinite
-    return {g * s, s + (t == 0.0f ? 0.0f : g * t * da)};
+    const float c = fminf(fmaxf(g, -16.0f), 16.0f);
+    const float d = silu ? g : kGelu * c * (1.0f + 3.0f * kGelu3 * c * c);
+    return {g * s, s * fmaf(d, 1.0f - s, 1.0f)};
 }
 
 // Gate and up projections -> h (and g, u).
@@ -68,8 +69,9 @@ struct EpiGlu {
     __device__ __forceinline__ Dest dest(int o, const Place &) const {
         return {o == 0 ? h : o == 1 ? g : u, TW_T_BF16, N, N, false};
     }
+    typedef NoFetch Fetched;
     template <int W, bool ALL>
-    __device__ __forceinline__ void values(Row &, int, int, const float (&v)[W],
+    __device__ __forceinline__ void values(Row &, const Fetched &, int, const float (&v)[W],
                                            const float (&w)[W], float (&o)[kOuts][W]) const {
 #pragma unroll
         for (int e = 0; e < W; ++e) {
@@ -97,98 +99,122 @@ struct EpiDh {
     __device__ __forceinline__ Dest dest(int o, const Place &) const {
         return {o == 0 ? dz : o == 1 ? du : h, TW_T_BF16, N, N, false};
     }
+    struct Fetched {
+        u32x4 g, u;
+    };
+    __device__ __forceinline__ Fetched fetch(int m, int n) const {
+        const int64_t at = (int64_t)m * N + n;
+        return {ld16(g + at), ld16(u + at)};
+    }
     template <int W, bool ALL>
-    __device__ __forceinline__ void values(Row &, int m, int n, const float (&v)[W],
+    __device__ __forceinline__ void values(Row &, const Fetched &f, int, const float (&v)[W],
                                            const float (&)[W], float (&o)[kOuts][W]) const {
-        float gv[W], uv[W];
-        load_bf16<W>(g + (int64_t)m * N + n, gv);
-        load_bf16<W>(u + (int64_t)m * N + n, uv);
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-            const Slope a = activate_slope<ACT>(gv[e]);
-            o[0][e] = v[e] * uv[e] * a.slope;
+            const uint32_t gp = f.g[e >> 1], up = f.u[e >> 1];
+            const float uv = e & 1 ? bf_hi(up) : bf_lo(up);
+            const Slope a = activate_slope<ACT>(e & 1 ? bf_hi(gp) : bf_lo(gp));
+            o[0][e] = v[e] * uv * a.slope;
             o[1][e] = v[e] * a.value;
-            o[2][e] = a.value * uv[e];
+            o[2][e] = a.value * uv;
         }
     }
 };
 
-// Up to 64 token rows (16 MB): a workgroup takes up to 16 C hidden neurons of both
+// Up to 64 token rows (16 MB): a workgroup takes up to 16 C hidden neurons of NM
 // matrices, its 8 waves a slice of K each; their sums meet in LDS.
-constexpr int kFewUpThreads = 512;
-template <int ACT, int C, int MB>
-__global__ __launch_bounds__(kFewUpThreads) void few_up_kernel(
-    const uint16_t *__restrict__ x, int64_t x_stride, const uint16_t *__restrict__ wg_t,
-    const uint16_t *__restrict__ wu_t, int M, int K, int N, int share, uint16_t *__restrict__ g,
-    uint16_t *__restrict__ u, uint16_t *__restrict__ h) {
-    constexpr int NW = kFewUpThreads / kWave;
-    extern __shared__ __attribute__((aligned(16))) char smem[];  // [NW][2 C MB][64] f32x4
+template <int ACT>
+struct FewUp {
+    static constexpr int NM = 2;
+    uint16_t *g, *u, *h;
+    __device__ __forceinline__ void put(int64_t at, float v, float w) const {
+        h[at] = (uint16_t)pack_bf16(activate<ACT>(v) * w, 0.0f);
+        if (g) g[at] = (uint16_t)pack_bf16(v, 0.0f);
+        if (u) u[at] = (uint16_t)pack_bf16(w, 0.0f);
+    }
+};
+template <int ACT>
+struct FewDh {
+    static constexpr int NM = 1;
+    const uint16_t *g, *u;
+    uint16_t *dz, *du, *h;
+    __device__ __forceinline__ void put(int64_t at, float v, float) const {
+        const Slope a = activate_slope<ACT>(bf_lo((uint32_t)g[at]));
+        const float uv = bf_lo((uint32_t)u[at]);
+        dz[at] = (uint16_t)pack_bf16(v * uv * a.slope, 0.0f);
+        du[at] = (uint16_t)pack_bf16(v * a.value, 0.0f);
+        h[at] = (uint16_t)pack_bf16(a.value * uv, 0.0f);
+    }
+};
+
+constexpr int kFewThreads = 512;
+template <int C, int MB, class Put>
+__global__ __launch_bounds__(kFewThreads) void few_hidden_kernel(
+    const uint16_t *__restrict__ x, int64_t x_stride, const uint16_t *__restrict__ w0,
+    const uint16_t *__restrict__ w1, int M, int K, int N, int share, Put put) {
+    constexpr int NW = kFewThreads / kWave, NM = Put::NM;
+    extern __shared__ __attribute__((aligned(16))) char smem[];  // [NW][NM C MB][64] f32x4
     f32x4 *sums = reinterpret_cast<f32x4 *>(smem);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int n0 = blockIdx.x * share, n1 = min(n0 + share, N);
     const int k8 = 8 * (lane >> 4);
-    const uint16_t *wp[2 * C], *xp[MB];
+    const uint16_t *wp[NM * C], *xp[MB];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t row = min(n0 + 16 * c + (lane & 15), n1 - 1);
-        wp[2 * c] = wg_t + row * K + k8;
-        wp[2 * c + 1] = wu_t + row * K + k8;
+        wp[NM * c] = w0 + row * K + k8;
+        if constexpr (NM == 2) wp[2 * c + 1] = w1 + row * K + k8;
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m) xp[m] = x + min(16 * m + (lane & 15), M - 1) * x_stride + k8;
     const int steps = (K + 31) / 32, per = (steps + NW - 1) / NW;
-    f32x4 acc[2 * C][MB] = {};
-    constexpr int U = 10 / (2 * C + MB) < 1 ? 1 : 10 / (2 * C + MB);  // loads in flight
-    few_product<2 * C, MB, U>(wp, xp, K, wave * per, min(wave * per + per, steps), acc);
+    f32x4 acc[NM * C][MB] = {};
+    constexpr int U = 10 / (NM * C + MB) < 1 ? 1 : 10 / (NM * C + MB);  // steps in a batch
+    few_product<NM * C, MB, U>(wp, xp, K, wave * per, min(wave * per + per, steps), acc);
 #pragma unroll
-    for (int b = 0; b < 2 * C; ++b)
+    for (int b = 0; b < NM * C; ++b)
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
-            sums[((wave * 2 * C + b) * MB + m) * kWave + lane] = acc[b][m];
+        for (int m = 0; m < MB; ++m) sums[((wave * NM * C + b) * MB + m) * kWave + lane] = acc[b][m];
     __syncthreads();
     for (int i = wave; i < C * MB; i += NW) {  // block i / MB of neurons, i % MB of rows
-        f32x4 v{}, w{};
+        f32x4 s[2] = {};
 #pragma unroll
-        for (int q = 0; q < NW; ++q) {
-            v += sums[((q * 2 * C + 2 * (i / MB)) * MB + i % MB) * kWave + lane];
-            w += sums[((q * 2 * C + 2 * (i / MB) + 1) * MB + i % MB) * kWave + lane];
-        }
+        for (int q = 0; q < NW; ++q)
+#pragma unroll
+            for (int o = 0; o < NM; ++o)
+                s[o] += sums[((q * NM * C + NM * (i / MB) + o) * MB + i % MB) * kWave + lane];
         const int m = 16 * (i % MB) + (lane & 15);
         if (m >= M) continue;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int n = n0 + 16 * (i / MB) + 4 * (lane >> 4) + e;
-            if (n >= n1) continue;
-            const int64_t at = (int64_t)m * N + n;
-            h[at] = (uint16_t)pack_bf16(activate<ACT>(v[e]) * w[e], 0.0f);
-            if (g) g[at] = (uint16_t)pack_bf16(v[e], 0.0f);
-            if (u) u[at] = (uint16_t)pack_bf16(w[e], 0.0f);
+            if (n < n1) put.put((int64_t)m * N + n, s[0][e], s[1][e]);
         }
     }
 }
 
-template <int ACT, int C, int MB>
-hipError_t few_up_as(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
-                     const uint16_t *wu_t, int M, int K, int N, int share, uint16_t *g,
-                     uint16_t *u, uint16_t *h, hipStream_t s) {
-    constexpr auto kernel = &few_up_kernel<ACT, C, MB>;
-    constexpr int lds = kFewUpThreads / kWave * 2 * C * MB * kWave * 16;
+template <int C, int MB, class Put>
+hipError_t few_hidden_as(const uint16_t *x, int64_t x_stride, const uint16_t *w0,
+                         const uint16_t *w1, int M, int K, int N, int share, const Put &put,
+                         hipStream_t s) {
+    constexpr auto kernel = &few_hidden_kernel<C, MB, Put>;
+    constexpr int lds = kFewThreads / kWave * Put::NM * C * MB * kWave * 16;
     const hipError_t e = lds_limit_once<kernel>(lds);
     if (e != hipSuccess) return e;
-    kernel<<<(unsigned)((N + share - 1) / share), kFewUpThreads, lds, s>>>(
-        x, x_stride, wg_t, wu_t, M, K, N, share, g, u, h);
+    kernel<<<(unsigned)((N + share - 1) / share), kFewThreads, lds, s>>>(x, x_stride, w0, w1, M, K,
+                                                                        N, share, put);
     return hipGetLastError();
 }
 
-template <int ACT>
-hipError_t few_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t, const uint16_t *wu_t,
-                  int M, int K, int N, uint16_t *g, uint16_t *u, uint16_t *h, hipStream_t s) {
+template <class Put>
+hipError_t few_hidden(const uint16_t *x, int64_t x_stride, const uint16_t *w0, const uint16_t *w1,
+                      int M, int K, int N, const Put &put, hipStream_t s) {
     // an even share of the neurons for each of 256 workgroups, at most 32
     int share = (N + 255) / 256;
     share = share < 4 ? 4 : share > 32 ? 32 : share;
     auto go = [&](auto c, auto mb) {
-        return few_up_as<ACT, decltype(c)::value, decltype(mb)::value>(
-            x, x_stride, wg_t, wu_t, M, K, N, share, g, u, h, s);
+        return few_hidden_as<decltype(c)::value, decltype(mb)::value>(x, x_stride, w0, w1, M, K, N,
+                                                                      share, put, s);
     };
     constexpr std::integral_constant<int, 1> one{};
     constexpr std::integral_constant<int, 2> two{};
@@ -198,28 +224,139 @@ hipError_t few_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t, con
     return mb == 1 ? go(two, one) : mb == 2 ? go(two, two) : go(two, four);
 }
 
+// ------------------ rows times a matrix of reduction rows --------------------
+// part[split][m][k] = sum over n of the split of h[m][n] w[n][k]: w rows are read
+// whole, 128 columns a workgroup (16 lanes of 16 bytes, 4 rows a wave), the products
+// on the vector units (a matrix instruction would need w transposed), h from LDS.
+constexpr int kFewDownMax = 16;  // token rows
+constexpr int kDownThreads = 512, kDownRows = 256;  // reduction rows between two barriers
+
+template <int MT>
+__global__ __launch_bounds__(kDownThreads) void few_down_kernel(const uint16_t *__restrict__ h,
+                                                                const uint16_t *__restrict__ w,
+                                                                int M, int K, int N, int per,
+                                                                float *__restrict__ part) {
+    constexpr int NW = kDownThreads / kWave, STEPS = kDownRows / (4 * NW);
+    __shared__ float hs[MT][kDownRows];
+    __shared__ __attribute__((aligned(16))) float sums[NW / 2][MT][128];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = blockIdx.x * 128 + 8 * (lane & 15);
+    const int at = col < K ? col : K - 8;  // (columns past K repeat the last ones)
+    const int n0 = blockIdx.y * per, n1 = min(n0 + per, N);
+    const int r0 = 4 * wave + (lane >> 4);
+    float acc[MT][8] = {};
+    for (int c = n0; c < n1; c += kDownRows) {
+        u32x4 v[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int n = c + 4 * NW * i + r0;
+            v[i] = ld16(w + (int64_t)min(n, n1 - 1) * K + at);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < MT * kDownRows; i += kDownThreads) {
+            const int m = i / kDownRows, n = c + i % kDownRows;
+            hs[m][i % kDownRows] =
+                m < M && n < n1 ? bf_lo((uint32_t)h[(int64_t)m * N + n]) : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int r = 4 * NW * i + r0;
+            // (rows past the split repeat its last one, which must not enter: 0 times
+            // an infinity is NaN)
+            const bool in = c + r < n1;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = in ? (e & 1 ? bf_hi(v[i][e >> 1]) : bf_lo(v[i][e >> 1])) : 0.0f;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float hv = hs[m][r];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[m][e] = fmaf(hv, f[e], acc[m][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            acc[m][e] += __shfl_xor(acc[m][e], 16);
+            acc[m][e] += __shfl_xor(acc[m][e], 32);
+        }
+    // the waves' sums, halves of them at a time
+#pragma unroll
+    for (int half = NW / 2; half >= 1; half /= 2) {
+        __syncthreads();
+        if (wave >= half && wave < 2 * half && lane < 16)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sums[wave - half][m][8 * lane + e] = acc[m][e];
+        __syncthreads();
+        if (wave < half && lane < 16)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[m][e] += sums[wave][m][8 * lane + e];
+    }
+    if (wave || lane >= 16 || col >= K) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (m >= M) continue;
+        float *p = part + ((int64_t)blockIdx.y * M + m) * K + col;
+        *reinterpret_cast<f32x4 *>(p) = f32x4{acc[m][0], acc[m][1], acc[m][2], acc[m][3]};
+        *reinterpret_cast<f32x4 *>(p + 4) = f32x4{acc[m][4], acc[m][5], acc[m][6], acc[m][7]};
+    }
+}
+
+// Splits of N that give every CU a workgroup, none of fewer than 32 rows.
+int few_down_splits(int K, int N) {
+    const int cols = (K + 127) / 128, most = (N + 31) / 32;
+    const int want = (256 + cols - 1) / cols;
+    return want < most ? want : most;
+}
+
+hipError_t launch_few_down(const uint16_t *h, const uint16_t *w, int M, int K, int N,
+                                  float *part, hipStream_t s) {
+    const int splits = few_down_splits(K, N);
+    const int per = (N + splits - 1) / splits;
+    const dim3 grid((K + 127) / 128, splits);
+    if (M == 1) few_down_kernel<1><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
+    else if (M == 2) few_down_kernel<2><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
+    else if (M <= 4) few_down_kernel<4><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
+    else if (M <= 8) few_down_kernel<8><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
+    else few_down_kernel<16><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
+    return hipGetLastError();
+}
+
 template <int ACT>
 hipError_t ffn_up(const TileArgs &p, uint16_t *g, uint16_t *u, uint16_t *h, hipStream_t s) {
+    if (p.M <= kFewRowsMax)
+        return few_hidden(p.a[0], p.lda, p.b[0], p.b[1], p.M, p.R, p.N, FewUp<ACT>{g, u, h}, s);
     return launch_tiles<kRows, kRows, 2, 1>(p, EpiGlu<ACT>{h, g, u, p.N}, s);
 }
 template <int ACT>
 hipError_t ffn_dh(const TileArgs &p, const uint16_t *g, const uint16_t *u, uint16_t *dz,
                   uint16_t *du, uint16_t *h, hipStream_t s) {
+    if (p.M <= kFewRowsMax)
+        return few_hidden(p.a[0], p.lda, p.b[0], p.b[0], p.M, p.R, p.N,
+                          FewDh<ACT>{g, u, dz, du, h}, s);
     return launch_tiles<kRows, kRows, 1, 1>(p, EpiDh<ACT>{g, u, dz, du, h, p.N}, s);
 }
 
 }  // namespace
 
 static SplitPlan down_plan(int M, int K, int N) {
-    return split_plan<1, 1>(TileArgs{{}, {}, N, K, M, K, N}, false);
+    return split_plan<1>(TileArgs{{}, {}, N, K, M, K, N}, false);
 }
 static SplitPlan dx_plan(int M, int K, int N) {
-    return split_plan<1, 2>(TileArgs{{}, {}, N, K, M, K, N}, false);
+    return split_plan<2>(TileArgs{{}, {}, N, K, M, K, N}, false);
 }
 static SplitPlan dw_plan(int M, int K, int N) {
     TileArgs p{{}, {}, N, K, N, K, M};
     p.groups = 3;
-    return split_plan<1, 1>(p, false);
+    return split_plan<1>(p, false);
 }
 
 size_t ffn_fwd_part_bytes(int M, int K, int N) {
@@ -234,13 +371,6 @@ size_t ffn_bwd_part_bytes(int M, int K, int N) {
 hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg_t,
                          const uint16_t *wu_t, int act, int M, int K, int N, uint16_t *g,
                          uint16_t *u, uint16_t *h, hipStream_t s) {
-    if (M <= kFewRowsMax) {
-        if (act == TW_A_RELU)
-            return few_up<TW_A_RELU>(x, x_stride, wg_t, wu_t, M, K, N, g, u, h, s);
-        if (act == TW_A_SILU)
-            return few_up<TW_A_SILU>(x, x_stride, wg_t, wu_t, M, K, N, g, u, h, s);
-        return few_up<TW_A_GELU>(x, x_stride, wg_t, wu_t, M, K, N, g, u, h, s);
-    }
     const TileArgs p{{x}, {wg_t, wu_t}, x_stride, K, M, N, K};
     if (act == TW_A_RELU) return ffn_up<TW_A_RELU>(p, g, u, h, s);
     if (act == TW_A_SILU) return ffn_up<TW_A_SILU>(p, g, u, h, s);
@@ -254,7 +384,7 @@ hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, 
         if (e != hipSuccess) return e;
         return launch_sum_parts(part, few_down_splits(K, N), (int64_t)M * K, y, y_type, s);
     }
-    return launch_split<kRows, kCols, 1, 1>(TileArgs{{h}, {wd}, N, K, M, K, N},
+    return launch_split<kRows, kCols, 1>(TileArgs{{h}, {wd}, N, K, M, K, N},
                                             down_plan(M, K, N), EpiStore{{y}, y_type, K, part},
                                             true, s);
 }
@@ -271,7 +401,7 @@ hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const 
 hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t *wg_t,
                          const uint16_t *wu_t, int M, int K, int N, void *dx, int dx_type,
                          float *part, hipStream_t s) {
-    return launch_split<kRows, kCols, 1, 2>(TileArgs{{dz, du}, {wg_t, wu_t}, N, K, M, K, N},
+    return launch_split<kRows, kCols, 2>(TileArgs{{dz, du}, {wg_t, wu_t}, N, K, M, K, N},
                                             dx_plan(M, K, N), EpiStore{{dx}, dx_type, K, part},
                                             true, s);
 }
@@ -283,7 +413,7 @@ hipError_t launch_ffn_dw(const uint16_t *dz, const uint16_t *du, const uint16_t 
     TileArgs p{{dz, du, h}, {x, x, dy}, N, x_stride, N, K, M};
     p.groups = 3;
     p.ldb_last = K;
-    return launch_split<kCols, kCols, 1, 1>(
+    return launch_split<kCols, kCols, 1>(
         p, dw_plan(M, K, N), EpiStore{{dwg_t, dwu_t, dwd}, dw_type, K, part}, true, s);
 }
 

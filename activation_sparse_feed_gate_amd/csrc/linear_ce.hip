@@ -75,18 +75,7 @@ struct EpiSoft {
         r.most = r.top = j.top;
         r.sum = j.sum;
     }
-    __device__ __forceinline__ void put(const Row &r, char *lds, int w, int i) const {
-        reinterpret_cast<Soft *>(lds)[w * 256 + i] = {r.top, r.sum};
-    }
-    template <int W>
-    __device__ __forceinline__ void finish(const char *lds, int i, int m, int cb) const {
-        const Soft *s = reinterpret_cast<const Soft *>(lds) + i;
-        Soft j = s[0];
-#pragma unroll
-        for (int w = 1; w < W; ++w) j = join_soft(j, s[w * 256]);
-        part[(int64_t)cb * M + m] = j;
-    }
-    __device__ __forceinline__ void whole(const Row &r, int m, int cb) const {
+    __device__ __forceinline__ void put(const Row &r, int m, int cb) const {
         part[(int64_t)cb * M + m] = {r.top, r.sum};
     }
 };
@@ -233,8 +222,10 @@ struct EpiD {
         return {d, TW_T_BF16, ldd, (int)ldd, false};
     }
     __device__ int stores(const Place &) const { return 16; }
+    typedef NoFetch Fetched;
+    __device__ Fetched fetch(int, int) const { return {}; }
     template <int W, bool ALL>
-    __device__ __forceinline__ void values(Row &r, int, int n, const float (&v)[W],
+    __device__ __forceinline__ void values(Row &r, const Fetched &, int n, const float (&v)[W],
                                            const float (&)[W], float (&o)[kOuts][W]) const {
         float p[W];
 #pragma unroll
@@ -259,14 +250,14 @@ struct Pieces {
     size_t d_bytes, part_bytes;
 };
 SplitPlan dw_plan(int M, int K, int width) {
-    return split_plan<1, 1>(TileArgs{{}, {}, 0, 0, width, K, M}, false);
+    return split_plan<1>(TileArgs{{}, {}, 0, 0, width, K, M}, false);
 }
 Pieces pieces_of(int M, int K, int V) {
     Pieces p;
     const int64_t most = (int64_t)(512 << 20) / 2 / (M > 0 ? M : 1) / 256 * 256;
     p.width = (int)(most < 256 ? 256 : most < V ? most : V);
     p.d_bytes = up256((size_t)M * ((p.width + 7) / 8 * 8) * 2);
-    p.dx = split_plan<1, 1>(TileArgs{{}, {}, 0, 0, M, K, p.width}, p.width < V);
+    p.dx = split_plan<1>(TileArgs{{}, {}, 0, 0, M, K, p.width}, p.width < V);
     // the weight gradient's parts behind them, since dx's stay
     size_t dw = dw_plan(M, K, p.width).bytes;
     if (V % p.width) dw = std::max(dw, dw_plan(M, K, V % p.width).bytes);
@@ -329,12 +320,12 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
             e = launch_tiles<kRows, kRows, 1, 1>(TileArgs{{x}, {wp}, x_stride, K, M, N, K},
                                                  EpiD{lse, dloss, t, d, ldd, N, first, V}, s);
         if (e == hipSuccess && dx && M > 0)
-            e = launch_split<kRows, kCols, 1, 1>(
+            e = launch_split<kRows, kCols, 1>(
                 TileArgs{{d}, {wp}, ldd, K, M, K, N}, pc.dx,
                 EpiStore{{dx}, dx_type, K, parts, first > 0}, first + N == V, s);
         if (e == hipSuccess && dw) {
             char *out = static_cast<char *>(dw) + (int64_t)first * K * (dw_type == TW_T_F32 ? 4 : 2);
-            e = launch_split<kCols, kCols, 1, 1>(TileArgs{{d}, {x}, ldd, x_stride, N, K, M},
+            e = launch_split<kCols, kCols, 1>(TileArgs{{d}, {x}, ldd, x_stride, N, K, M},
                                                  dw_plan(M, K, N),
                                                  EpiStore{{out}, dw_type, K, dw_parts}, true, s);
         }

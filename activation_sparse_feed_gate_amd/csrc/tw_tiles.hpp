@@ -23,10 +23,10 @@ enum { kRows = 0, kCols = 1 };
 constexpr uint32_t kPastEnd = 1u << 30;
 constexpr int64_t kMaxStride = 1 << 20;  // elements between operand rows
 
-// A tile of an output: its product, its first row and column, its side, and its place
+// A tile of an output: its product, its first row and column, its size, and its place
 // among the parts (-1: it takes the whole reduction).
 struct Place {
-    int z, m0, n0, side, part;
+    int z, m0, n0, rows, cols, part;
 };
 
 // The operands of one launch.  What a[1], b[1], ... are is the kernel's: a
@@ -61,242 +61,42 @@ __device__ __forceinline__ void store4(void *p, int type, int64_t at, f32x4 v) {
         *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p) + at) = w;
     }
 }
-// W (4 or 8) bf16 values.
-template <int W>
-__device__ __forceinline__ void load_bf16(const uint16_t *p, float (&f)[W]) {
-    uint32_t w[W / 2];
-    if constexpr (W == 8) {
-        const u32x4 v = ld16(p);
-        for (int i = 0; i < 4; ++i) w[i] = v[i];
-    } else {
-        const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
-        for (int i = 0; i < 2; ++i) w[i] = v[i];
-    }
-#pragma unroll
-    for (int e = 0; e < W; ++e) f[e] = e & 1 ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
-}
-// W outputs of row m from column n on (whole ones: n < cols).
-template <int W>
-__device__ __forceinline__ void put_out(const Dest &d, int m, int n, const float (&v)[W]) {
+// The 8 outputs of row m from column n on (n < cols).
+__device__ __forceinline__ void put_out(const Dest &d, int m, int n, const float (&v)[8]) {
     if (!d.p) return;
     const int64_t at = m * d.ld + n;
     if (d.type == TW_T_F32) {
         f32x4 *q = reinterpret_cast<f32x4 *>(static_cast<float *>(d.p) + at);
 #pragma unroll
-        for (int e = 0; e < W; e += 4) {
+        for (int e = 0; e < 8; e += 4) {
             const f32x4 o{v[e], v[e + 1], v[e + 2], v[e + 3]};
             q[e / 4] = d.add ? q[e / 4] + o : o;
         }
-    } else if constexpr (W == 8) {
+    } else {
         st16(static_cast<uint16_t *>(d.p) + at,
              u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                    pack_bf16(v[6], v[7])});
-    } else {
-        store4(d.p, TW_T_BF16, at, f32x4{v[0], v[1], v[2], v[3]});
     }
 }
-
-// 32 rows x 16 reduction elements of a kCols region (32 reduction rows of 128
-// columns, 256 bytes each, chunk c of row r at c ^ 4 (r % 4)): lane l receives
-// column col32 + l % 32 at reduction rows 16 s + 8 (l / 32) ..+7, the layout
-// of frag().
-__device__ __forceinline__ u32x4 col_frag(const char *region, int col32, int s, int lane) {
-    const int g4 = (lane >> 4) & 3, i16 = lane & 15;
-    const int c0 = col32 + 16 * (g4 & 1) + 4 * (i16 & 3);
-    i16x4 v[2];
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        const int row = 16 * s + 8 * (g4 >> 1) + 4 * hh + (i16 >> 2);
-        const uint32_t off = row * 256 + (((c0 >> 3) ^ (4 * (row & 3))) << 4) + (c0 & 7) * 2;
-        v[hh] = lds_tr16((const lds_i16x4 *)(region + off));
-    }
-    const u32x2 lo = __builtin_bit_cast(u32x2, v[0]);
-    const u32x2 hi = __builtin_bit_cast(u32x2, v[1]);
-    return u32x4{lo[0], lo[1], hi[0], hi[1]};
-}
-
-// ----------------------------- 128 x 128 tiles ------------------------------
-// 8 waves of 64 x 32 outputs, stages of 32 reduction elements in the ring of
-// kloop_pipelined.  Every operand's share of a stage is 8 KB, one direct load
-// of a wave.
-constexpr int kRingBM = 128, kRingBN = 128, kRingS = 4;
-constexpr int kRingPart = 128 * kPRow;  // one operand of one stage
-
-// One operand's direct loads: rows (of the kRows layout) or columns i0 ..
-// i0 + 127, reduction elements 32 kt ..+31 of `R`.
-template <int L>
-struct RingOperand {
-    const uint16_t *p;
-    int64_t ld;
-    int I, R, i0;
-    uint32_t voff;
-    int red;  // reduction element of the lane's piece within a stage
-    __device__ __forceinline__ RingOperand(const uint16_t *p_, int64_t ld_, int I_, int R_, int i0_,
-                                           int wave, int lane)
-        : ld(ld_), I(I_), R(R_), i0(i0_) {
-        if constexpr (L == kRows) {
-            const int sr = 16 * wave + (lane >> 2);
-            p = p_ + i0 * ld;
-            red = 8 * ((lane & 3) ^ swz(sr));
-            voff = i0 + sr < I ? (uint32_t)sr * (uint32_t)ld * 2 + red * 2 : kPastEnd;
-        } else {
-            const int row = 4 * wave + (lane >> 4);
-            const int col = 8 * ((lane & 15) ^ (4 * (row & 3)));
-            p = p_ + i0;
-            red = row;
-            voff = i0 + col < I ? (uint32_t)row * (uint32_t)ld * 2 + col * 2 : kPastEnd;
-        }
-    }
-    __device__ __forceinline__ void issue(int kt, char *dst) const {
-        const uint32_t v = kt * kPK + red < R ? voff : kPastEnd;
-        if constexpr (L == kRows) {
-            // (a row's last 16-byte piece lies in its padding where R is no
-            // multiple of 8)
-            const int rows = min(kRingBM, I - i0);
-            const rsrc_t d = make_rsrc(p, ((uint64_t)(rows - 1) * ld + ((R + 7) & ~7)) * 2);
-            dma16(d, v, kt * kPK * 2, dst);
-        } else {
-            // the descriptor moves with the stage: an operand may be larger
-            // than 32-bit offsets reach
-            const int rows = max(1, min(kPK, R - kt * kPK));
-            const int cols = (min(kRingBN, I - i0) + 7) & ~7;
-            const rsrc_t d = make_rsrc(p + (int64_t)kt * kPK * ld,
-                                       ((uint64_t)(rows - 1) * ld + cols) * 2);
-            dma16(d, v, 0, dst);
-        }
-    }
-};
 
 // An epilogue has, for a row m of the tile, a Raw (what it loads: raw(m); of(l): lane
 // l's) and a Row made of it, and
-//   values<W, ALL>(row, m, n, v, u, o)  makes its kOuts outputs of columns n .. n + W
-//                                - 1 from those of the product (u: of the second
-//                                weights); ALL: these columns are all within N,
+//   Fetched, fetch(m, n)         what it loads of the 8 columns n .. n + 7 of row m,
+//                                ahead of
+//   values<W, ALL>(row, fetched, n, v, u, o)  which makes its kOuts outputs of columns
+//                                n .. n + W - 1 from those of the product (u: of the
+//                                second weights); ALL: these columns are all within N,
 //   dest(o, place)               says where output o of a tile goes,
 //   stores(place)                how many stores a wave of the larger tiles makes of a
 //                                tile inside the product, or,
 // where it reduces over the columns (kStats),
 //   most<W, ALL>(row, n, v), add<W, ALL>(row, n, v)   two passes over a lane's columns,
 //   join<L>(row)                            lanes l and l ^ L hold one row,
-//   put(row, lds, w, r)                     wave column w's part of the tile's row r,
-//   finish<W>(lds, r, m, cb)                joins W wave columns of 128 columns' block cb,
-//   whole(row, m, cb)                       a wave that holds all 128 columns.
+//   put(row, m, cb)                         the row's block cb of 128 columns.
 struct NoRaw {
     __device__ NoRaw of(int) const { return {}; }
 };
-
-template <int LA, int LB, int NB, int SEG, class Epi>
-__global__ __launch_bounds__(512) void ring_tiles_kernel(TileArgs p, Epi epi) {
-    constexpr int NI = 1 + NB, STAGE = NI * kRingPart;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
-    const int l32 = lane & 31;
-    const int z = blockIdx.y, sp = blockIdx.z;  // product, part of the reduction
-    int rb, cb;
-    xcd_tile(blockIdx.x, (p.M + kRingBM - 1) / kRingBM, (p.N + kRingBN - 1) / kRingBN, rb, cb);
-    const int m0 = rb * kRingBM, n0 = cb * kRingBN;
-    const int64_t ldb = z == 2 ? p.ldb_last : p.ldb;
-    const int KT = (p.R + kPK - 1) / kPK;
-
-    const RingOperand<LA> a0(p.a[SEG == 2 ? 0 : z], p.lda, p.M, p.R, m0, wave, lane);
-    const RingOperand<LB> b0(p.b[SEG == 2 || NB == 2 ? 0 : z], ldb, p.N, p.R, n0, wave, lane);
-    const RingOperand<LA> a1(SEG == 2 ? p.a[1] : p.a[0], p.lda, p.M, p.R, m0, wave, lane);
-    const RingOperand<LB> b1(SEG == 2 || NB == 2 ? p.b[1] : p.b[0], ldb, p.N, p.R, n0, wave, lane);
-    auto issue = [&](int kt, char *st) {
-        char *d = st + wave * 1024;
-        if (SEG == 2 && kt >= KT) {
-            a1.issue(kt - KT, d);
-            b1.issue(kt - KT, d + kRingPart);
-        } else {
-            a0.issue(kt, d);
-            b0.issue(kt, d + kRingPart);
-            if constexpr (NB == 2) b1.issue(kt, d + 2 * kRingPart);
-        }
-    };
-    auto fragment = [&](auto layout, const char *part, int row, int s) {
-        if constexpr (decltype(layout)::value == kRows) return frag(part, row, s, lane);
-        else return col_frag(part, row, s, lane);
-    };
-    f32x16 acc[NB][2];
-#pragma unroll
-    for (int o = 0; o < NB; ++o)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[o][i] = f32x16{};
-    u32x4 fa[2][2], fb[2][NB];
-    auto load = [&](const char *st, int s, int buf) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            fa[buf][i] = fragment(std::integral_constant<int, LA>{}, st, wm * 64 + 32 * i, s);
-#pragma unroll
-        for (int o = 0; o < NB; ++o)
-            fb[buf][o] = fragment(std::integral_constant<int, LB>{}, st + (1 + o) * kRingPart,
-                                  wn * 32, s);
-    };
-    // the second operand's rows are the instruction's first ones, so that a
-    // lane holds 4 consecutive n of one m
-    auto mma = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int o = 0; o < NB; ++o) acc[o][i] = mfma32(fb[buf][o], fa[buf][i], acc[o][i]);
-    };
-    const int all = SEG * KT, per = (all + p.splits - 1) / p.splits;
-    kloop_pipelined<kRingS, NI>(min(sp * per, all), min(sp * per + per, all), smem, STAGE, issue,
-                                load, mma);
-    const int part = p.splits > 1 ? (sp * p.groups + z) * (int)gridDim.x + (int)blockIdx.x : -1;
-    const Place at{z, m0, n0, kRingBM, part};
-    if constexpr (Epi::kStats) __syncthreads();  // finish() uses the ring's memory
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int m = m0 + wm * 64 + 32 * i + l32;
-        typename Epi::Row row(epi, epi.raw(min(m, p.M - 1)));
-        auto each = [&](auto f) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[4], u[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] = acc[0][i][4 * q + e];
-                    u[e] = acc[NB - 1][i][4 * q + e];
-                }
-                f(n0 + wn * 32 + 8 * q + 4 * (lane >> 5), v, u);
-            }
-        };
-        if constexpr (Epi::kStats) {
-            each([&](int n, auto &v, auto &) { epi.template most<4, false>(row, n, v); });
-            each([&](int n, auto &v, auto &) { epi.template add<4, false>(row, n, v); });
-            epi.template join<32>(row);
-            if (lane < 32) epi.put(row, smem, wn, wm * 64 + 32 * i + l32);
-        } else if (m < p.M) {
-            each([&](int n, auto &v, auto &u) {
-                float out[Epi::kOuts][4];
-                if (n >= epi.dest(0, at).cols) return;
-                epi.template values<4, false>(row, m, n, v, u, out);
-#pragma unroll
-                for (int o = 0; o < Epi::kOuts; ++o) put_out<4>(epi.dest(o, at), m, n, out[o]);
-            });
-        }
-    }
-    if constexpr (Epi::kStats) {
-        __syncthreads();
-        if (tid < kRingBM && m0 + tid < p.M) epi.template finish<4>(smem, tid, m0 + tid, cb);
-    }
-}
-
-template <int LA, int LB, int NB, int SEG, class Epi>
-hipError_t launch_ring(const TileArgs &p, const Epi &epi, hipStream_t s) {
-    constexpr auto kernel = &ring_tiles_kernel<LA, LB, NB, SEG, Epi>;
-    constexpr int lds = kRingS * (1 + NB) * kRingPart;
-    const hipError_t e = lds_limit_once<kernel>(lds);
-    if (e != hipSuccess) return e;
-    const int64_t tiles = ((int64_t)p.M + kRingBM - 1) / kRingBM *
-                          (((int64_t)p.N + kRingBN - 1) / kRingBN);
-    if (tiles == 0) return hipSuccess;
-    kernel<<<dim3((unsigned)tiles, p.groups, p.splits), 512, lds, s>>>(p, epi);
-    return hipGetLastError();
-}
+struct NoFetch {};
 
 // ----------------------------- 256 x 256 tiles ------------------------------
 // 256 x 256 outputs (NB = 2: 256 x 128 of each weight matrix) a workgroup of 8
@@ -325,18 +125,24 @@ hipError_t launch_ring(const TileArgs &p, const Epi &epi, hipStream_t s) {
 // 2 f(r), f = r % 4 + 4 (r / 8 % 2): the 8 rows that 32 lanes read, two
 // chunks of each, fill the 16 chunks of a row of banks once.  Loads of either
 // cover whole 128-byte lines.
-constexpr int kWideTile = 256, kWideK = 64, kWideThreads = 512;
+constexpr int kWideCols = 256, kWideK = 64;
 constexpr int kWideLine = 128;                    // bytes of a kRows row in a stage
-constexpr int kWidePart = 256 * kWideLine;        // one operand of a stage
-constexpr int kWideSlot = 2 * kWidePart;
-constexpr int kWideRegion = kWideK * 256;         // half of a kCols operand
+constexpr int kWideRegion = kWideK * 256;         // 128 columns of a kCols operand
 constexpr int kWideOut = 4096;                    // a wave's outputs on their way to memory
-constexpr int kWideBytes = 2 * kWideSlot + 8 * kWideOut;
 constexpr int kWideGrid = 256;                    // workgroups: one a CU
+// WR wave rows of 64, two wave columns of 128.
+template <int WR>
+struct Wide {
+    static constexpr int kWaves = 2 * WR, kThreads = 64 * kWaves, kRowsOf = 64 * WR;
+    static constexpr int kA = kRowsOf * kWideLine, kB = kWideCols * kWideLine;  // a stage's operands
+    static constexpr int kSlot = kA + kB, kBytes = 2 * kSlot + kWaves * kWideOut;
+    static constexpr int kPair = 8 / WR;          // loads of a wave for two column blocks
+    static constexpr int kFirst = 4 + kPair;      // ... for A and two column blocks
+};
 
 __device__ __forceinline__ int line_swz(int r) { return (r >> 1) & 7; }
 
-// wait_vmcnt<N + more>, `more` a multiple of 8 up to 48.
+// wait_vmcnt<N + more> (63 at most), `more` a multiple of 8 up to 48.
 template <int N>
 __device__ __forceinline__ void wait_besides(int more) {
     switch (more) {
@@ -344,15 +150,17 @@ __device__ __forceinline__ void wait_besides(int more) {
     case 16: wait_vmcnt<N + 16>(); break;
     case 24: wait_vmcnt<N + 24>(); break;
     case 32: wait_vmcnt<N + 32>(); break;
-    case 48: wait_vmcnt<N + 48>(); break;
+    case 48: wait_vmcnt<(N + 48 < 63 ? N + 48 : 63)>(); break;
     default: wait_vmcnt<N>(); break;
     }
 }
 
-template <int LA, int LB, int NB, int SEG, class Epi>
-__global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, int row_regions, Epi epi) {
+template <int WR, int LA, int LB, int NB, int SEG, class Epi>
+__global__ __launch_bounds__(Wide<WR>::kThreads) void wide_tiles_kernel(TileArgs p, int row_regions,
+                                                                        Epi epi) {
+    using W = Wide<WR>;
     static_assert(NB == 1 || (LB == kRows && SEG == 1), "two weight matrices: rows, one term");
-    constexpr int BN = kWideTile / NB;
+    constexpr int BM = W::kRowsOf, BN = kWideCols / NB;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -360,7 +168,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     const int l16 = lane & 15;
     const int KT = (p.R + kWideK - 1) / kWideK;  // stages of one term
     const int all = SEG * KT, per = (all + p.splits - 1) / p.splits;
-    const int nbm = (p.M + kWideTile - 1) / kWideTile, nbn = (p.N + BN - 1) / BN;
+    const int nbm = (p.M + BM - 1) / BM, nbn = (p.N + BN - 1) / BN;
     // Items: the first p.full tiles whole, then the others in p.splits parts.
     const int tiles = nbm * nbn, rest = tiles * p.groups - p.full;
     const int items = p.full + rest * p.splits;
@@ -369,9 +177,8 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     int m0, n0, z, part, k0, kn;
     int64_t ldb;
     rsrc_t ra[SEG], rb[SEG == 2 ? 2 : NB];  // (kRows)
-    // Lane's place in a load.  kRows: 8 rows of a group of 64, rows 8 wave ..+7,
-    // a chunk of 8 lanes each; kCols: 4 reduction rows of a region, rows 4 wave
-    // ..+3 of each half of 32, 16 chunks each.
+    // Lane's place in a load.  kRows: rows 8 wave ..+7 of 16 WR, a chunk of 8 lanes
+    // each; kCols: reduction rows 4 wave ..+3 of 8 WR, 16 chunks each.
     const int lrow = 8 * wave + (lane >> 3);
     const int chunk = (lane & 7) ^ line_swz(lrow);
     const int crow = 4 * wave + (lane >> 4);
@@ -396,11 +203,11 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         if (row_regions == 8) xcd_tile<8>(tile, nbm, nbn, bm, bn);
         else if (row_regions == 4) xcd_tile<4>(tile, nbm, nbn, bm, bn);
         else xcd_tile<2>(tile, nbm, nbn, bm, bn);
-        m0 = bm * kWideTile;
+        m0 = bm * BM;
         n0 = bn * BN;
         const int pad = (p.R + 7) & ~7;  // a row's last piece may lie in its padding
         if constexpr (LA == kRows) {
-            const int rows = min(kWideTile, p.M - m0);
+            const int rows = min(BM, p.M - m0);
 #pragma unroll
             for (int g = 0; g < SEG; ++g)
                 ra[g] = make_rsrc((SEG == 2 ? p.a[g] : z == 0 ? p.a[0] : z == 1 ? p.a[1] : p.a[2]) +
@@ -438,7 +245,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     // operand may be larger than 32-bit offsets reach)
     auto col_rsrc = [&](const uint16_t *base, int64_t ld, int kt, int i0, int I) {
         const int rows = min(kWideK, p.R - kt * kWideK);
-        const int cols = (min(kWideTile, I - i0) + 7) & ~7;
+        const int cols = (min(kWideCols, I - i0) + 7) & ~7;
         return make_rsrc(base + (int64_t)kt * kWideK * ld + i0,
                          ((uint64_t)(rows - 1) * ld + cols) * 2);
     };
@@ -446,9 +253,8 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         return SEG == 2 ? (kt >= KT ? q[1] : q[0]) : z == 0 ? q[0] : z == 1 ? q[1] : q[2];
     };
     // The loads of the item's stage i, begun together and issued one by one: put_a 0 ..
-    // 3, put_b of pair q of the column blocks (0: B0, B1; 1: B2, B3), 0 and 1.  kRows:
-    // groups of 64 rows; of one matrix 2 g + q, g the wave column, of two matrix q, its
-    // groups g.
+    // 3, put_b of pair q of the column blocks (0: B0, B1; 1: B2, B3; two matrices: the
+    // gate's, the up's), 0 .. kPair - 1.
     struct Loads {
         rsrc_t d[2];  // of one operand, or two matrices
         uint32_t v[2], soff;
@@ -457,7 +263,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     auto begin_a = [&](int i) {
         const int kt = k0 + i, ks = SEG == 2 && kt >= KT ? kt - KT : kt;
         Loads l;
-        l.slot = smem + (i & 1) * kWideSlot;
+        l.slot = smem + (i & 1) * W::kSlot;
         l.soff = ks * kWideLine;
         if constexpr (LA == kRows) {
             l.d[0] = SEG == 2 && kt >= KT ? ra[SEG - 1] : ra[0];
@@ -472,7 +278,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     auto begin_b = [&](int i) {
         const int kt = k0 + i, ks = SEG == 2 && kt >= KT ? kt - KT : kt;
         Loads l;
-        l.slot = smem + (i & 1) * kWideSlot + kWidePart;
+        l.slot = smem + (i & 1) * W::kSlot + W::kA;
         l.soff = ks * kWideLine;
         if constexpr (LB == kRows) {
             l.d[0] = SEG == 2 && kt >= KT ? rb[SEG - 1] : rb[0];
@@ -487,23 +293,25 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     };
     auto put_a = [&](const Loads &l, int g) {
         if constexpr (LA == kRows)
-            dma16(l.d[0], l.v[0] + g * (64u * (uint32_t)p.lda * 2), l.soff,
-                  l.slot + (64 * g + 8 * wave) * kWideLine);
+            dma16(l.d[0], l.v[0] + g * ((uint32_t)(16 * WR) * (uint32_t)p.lda * 2), l.soff,
+                  l.slot + (16 * WR * g + 8 * wave) * kWideLine);
         else
-            dma16(l.d[0], l.v[g >> 1] + (g & 1) * (32u * (uint32_t)p.lda * 2), 0,
-                  l.slot + (g >> 1) * kWideRegion + (32 * (g & 1) + 4 * wave) * 256);
+            dma16(l.d[0], l.v[g / W::kPair] + g % W::kPair * ((uint32_t)(8 * WR) * (uint32_t)p.lda * 2),
+                  0, l.slot + g / W::kPair * kWideRegion + (8 * WR * (g % W::kPair) + 4 * wave) * 256);
     };
     auto put_b = [&](const Loads &l, int q, int g) {
         if constexpr (LB == kRows) {
-            const int at = NB == 1 ? 2 * g + q : 2 * q + g;
-            dma16(l.d[NB == 2 ? q : 0], l.v[0] + (NB == 1 ? at : g) * (64u * (uint32_t)ldb * 2),
-                  l.soff, l.slot + (64 * at + 8 * wave) * kWideLine);
+            // row 16 WR g of the pair's: 64 of each wave column, or 128 of matrix q
+            const int r = 16 * WR * g;
+            const int row = NB == 1 ? r / 64 * 128 + q * 64 + r % 64 : r;
+            dma16(l.d[NB == 2 ? q : 0], l.v[0] + row * ((uint32_t)ldb * 2), l.soff,
+                  l.slot + ((NB == 2 ? q * 128 : 0) + row + 8 * wave) * kWideLine);
         } else {
-            dma16(l.d[0], l.v[q] + g * (32u * (uint32_t)ldb * 2), 0,
-                  l.slot + q * kWideRegion + (32 * g + 4 * wave) * 256);
+            dma16(l.d[0], l.v[q] + g * ((uint32_t)(8 * WR) * (uint32_t)ldb * 2), 0,
+                  l.slot + q * kWideRegion + (8 * WR * g + 4 * wave) * 256);
         }
     };
-    constexpr int kAB = 6, kB = 2;  // loads of a wave in each part
+    constexpr int kAB = W::kFirst, kB = W::kPair;  // loads of a wave in each part
     auto load_first = [&] {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -512,7 +320,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
 #pragma unroll
             for (int g = 0; g < 4; ++g) put_a(a, g);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) put_b(b, g >> 1, g & 1);
+            for (int g = 0; g < 2 * kB; ++g) put_b(b, g / kB, g % kB);
         }
     };
     // Fragment of 16 rows (columns of the product's other operand) from `row` on,
@@ -536,13 +344,13 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
     };
     auto read_a = [&](int k, int i, int s) {  // 16 rows i of the wave's 64
-        const char *part = smem + (k & 1) * kWideSlot;
+        const char *part = smem + (k & 1) * W::kSlot;
         if constexpr (LA == kRows) return read_rows(part, wm * 64 + 16 * i, s);
         else return read_cols(part + (wm >> 1) * kWideRegion, (wm & 1) * 8 + 2 * i, s);
     };
     u32x4 fa[2][4], fb[2][2][2];  // [sub-step][16 rows], [register set][sub-step][16 columns]
     auto read_b = [&](int k, int j, int s, int h) {  // half h of block j of 32 columns
-        const char *part = smem + (k & 1) * kWideSlot + kWidePart;
+        const char *part = smem + (k & 1) * W::kSlot + W::kA;
         if constexpr (LB == kRows)
             fb[j & 1][s][h] = read_rows(
                 part,
@@ -599,7 +407,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     load_first();
     for (int t = blockIdx.x; t < items; t += gridDim.x) {
         const int mt = m0, nt = n0, n = kn;  // m0, ... move on below
-        const Place at{z, m0, n0, kWideTile, part};
+        const Place at{z, m0, n0, BM, BN, part};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -627,7 +435,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                 step(1, [&](int q) {
                     read_next(k, 2, q);
                     if (q < 4) put_a(la, q);
-                    else if (q < 6) put_b(lb, 0, q - 4);
+                    else if (q < 4 + kB) put_b(lb, 0, q - 4);
                 });
                 step(2, [&](int q) { read_next(k, 3, q); });
                 if (k) after = 0;
@@ -636,7 +444,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                 wait_lgkm0();
                 __builtin_amdgcn_s_barrier();  // Y
                 last_step(k, [&](int q) {
-                    if (q >= 4 && q < 6) put_b(lb, 1, q - 4);
+                    if (q >= 4 && q < 4 + kB) put_b(lb, 1, q - 4);
                 });
             }
             if (k + 1 < n) {
@@ -678,7 +486,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
         asm volatile("" : "+v"(ln));
         const int lr = ln & 15, lc = 4 * (ln >> 4);
         const int mw = mt + wm * 64, nw = nt + wn * (BN / 2);  // the wave's outputs
-        char *out = smem + 2 * kWideSlot + wave * kWideOut;
+        char *out = smem + 2 * W::kSlot + wave * kWideOut;
         // ALL: every row and column of the wave's outputs is one of the product's
         auto write = [&](auto whole) {
             constexpr bool ALL = decltype(whole)::value;
@@ -699,7 +507,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                     epi.template join<16>(row);
                     epi.template join<32>(row);
                     const int m = mw + 16 * i + lr;
-                    if (ln < 16 && (ALL || (m < p.M && nw < p.N))) epi.whole(row, m, nw / 128);
+                    if (ln < 16 && (ALL || (m < p.M && nw < p.N))) epi.put(row, m, nw / 128);
                 }
             } else if constexpr (NB == 1) {
                 // 16 rows of 64 columns at a time go through LDS, 256 bytes a row, chunk c
@@ -716,6 +524,16 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                     __builtin_amdgcn_wave_barrier();
                 };
                 const int cols = epi.dest(0, at).cols;
+                // what 8 rows of a block need besides, as many of the 16 ahead as there are
+                // registers for
+                constexpr int kAhead = WR == 4 ? 2 : 16;
+                typename Epi::Fetched got[kAhead];
+                auto fetch = [&](int f) {
+                    got[f % kAhead] = epi.fetch(min(mw + 8 * (f & 1) + 16 * (f >> 2) + r8, p.M - 1),
+                                                min(nw + 64 * (f >> 1 & 1) + 8 * c8, cols - 8));
+                };
+#pragma unroll
+                for (int f = 0; f < kAhead; ++f) fetch(f);
                 enter(0);
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
@@ -737,11 +555,14 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                         const int r = 16 * i + 8 * q + r8, m = mw + r;
                         typename Epi::Row row(epi, raw.of(r));
                         float o[Epi::kOuts][8];
-                        if (!ALL && (m >= p.M || n >= cols)) continue;
-                        epi.template values<8, ALL>(row, m, n, v[q], v[q], o);
+                        const bool in = ALL || (m < p.M && n < cols);
+                        if (in) epi.template values<8, ALL>(row, got[(2 * b + q) % kAhead], n, v[q],
+                                                    v[q], o);
+                        if (2 * b + q + kAhead < 16) fetch(2 * b + q + kAhead);
+                        if (!in) continue;
 #pragma unroll
                         for (int k = 0; k < Epi::kOuts; ++k)
-                            put_out<8>(epi.dest(k, at), m, n, o[k]);
+                            put_out(epi.dest(k, at), m, n, o[k]);
                     }
                 }
             } else {
@@ -761,7 +582,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                                 v[e] = acc[i0 + i][j][e];
                                 u[e] = acc[i0 + i][4 + j][e];
                             }
-                            epi.template values<4, ALL>(row, 0, 0, v, u, o[i][j]);
+                            epi.template values<4, ALL>(row, {}, 0, v, u, o[i][j]);
                         }
                     }
 #pragma unroll
@@ -794,7 +615,7 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
                 }
             }
         };
-        const bool inside = mt + kWideTile <= p.M && nt + BN <= p.N;
+        const bool inside = mt + BM <= p.M && nt + BN <= p.N;
         if (inside) write(std::true_type{});
         else write(std::false_type{});
         // at least so many stores of this tile are younger than the next one's loads
@@ -803,40 +624,54 @@ __global__ __launch_bounds__(kWideThreads) void wide_tiles_kernel(TileArgs p, in
     }
 }
 
-template <int NB>
+template <int WR, int NB>
 int64_t wide_tiles(const TileArgs &p) {  // of all products
-    return ((int64_t)p.M + kWideTile - 1) / kWideTile *
-           (((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB)) * p.groups;
+    return ((int64_t)p.M + 64 * WR - 1) / (64 * WR) *
+           (((int64_t)p.N + kWideCols / NB - 1) / (kWideCols / NB)) * p.groups;
 }
 
-template <int LA, int LB, int NB, int SEG, class Epi>
+template <int WR, int LA, int LB, int NB, int SEG, class Epi>
 hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
-    constexpr auto kernel = &wide_tiles_kernel<LA, LB, NB, SEG, Epi>;
-    const hipError_t e = lds_limit_once<kernel>(kWideBytes);
+    using W = Wide<WR>;
+    constexpr auto kernel = &wide_tiles_kernel<WR, LA, LB, NB, SEG, Epi>;
+    const hipError_t e = lds_limit_once<kernel>(W::kBytes);
     if (e != hipSuccess) return e;
-    const int64_t nbm = ((int64_t)p.M + kWideTile - 1) / kWideTile;
-    const int64_t nbn = ((int64_t)p.N + kWideTile / NB - 1) / (kWideTile / NB);
-    const int64_t items = p.full + (wide_tiles<NB>(p) - p.full) * p.splits;
-    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), kWideThreads, kWideBytes, s>>>(
+    const int64_t nbm = ((int64_t)p.M + W::kRowsOf - 1) / W::kRowsOf;
+    const int64_t nbn = ((int64_t)p.N + kWideCols / NB - 1) / (kWideCols / NB);
+    const int64_t items = p.full + (wide_tiles<WR, NB>(p) - p.full) * p.splits;
+    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), W::kThreads, W::kBytes, s>>>(
         p, wide_row_regions(nbm, nbn), epi);
     return hipGetLastError();
 }
 
-// The larger tiles where their number leaves few CUs idle (to be measured).
+// Estimated time (us) of `items` tiles of 64 WR rows over `stages` stages each.  A stage
+// takes 1.0 to 1.6 us in the larger tiles and 0.55 to 0.95 in the smaller ones, the more
+// the more CUs draw power and load; 8 us come before the first and after the last.
+template <int WR>
+double tiles_us(int64_t items, int64_t stages) {
+    const double least = WR == 4 ? 1.0 : 0.55, more = WR == 4 ? 0.6 : 0.4;
+    const int64_t rounds = items / kWideGrid, rest = items % kWideGrid;
+    return 8.0 + stages * (rounds * (least + more) +
+                           (rest ? least + more * rest / kWideGrid : 0.0));
+}
+
+// Measured (us, tiles of 128 and of 256 rows): gate and up 777 x 1000 x 2728 25, 29; 2048 x
+// 2048 x 5632 91, 96; 777 x 2048 x 5632 70, 50; 4096 x 1024 x 4096 71, 61.
 template <int LA, int LB, int NB, int SEG, class Epi>
 hipError_t launch_tiles(TileArgs p, const Epi &epi, hipStream_t s) {
-    static const char *force = getenv("TW_FORCE");
-    if (p.R > 0 && (force ? force[0] == 'w' : wide_tiles<NB>(p) >= 128)) {
-        p.full = (int)wide_tiles<NB>(p);
-        return launch_wide<LA, LB, NB, SEG>(p, epi, s);
+    const int64_t stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
+    if (tiles_us<4>(wide_tiles<4, NB>(p), stages) <= tiles_us<2>(wide_tiles<2, NB>(p), stages)) {
+        p.full = (int)wide_tiles<4, NB>(p);
+        return launch_wide<4, LA, LB, NB, SEG>(p, epi, s);
     }
-    return launch_ring<LA, LB, NB, SEG>(p, epi, s);
+    p.full = (int)wide_tiles<2, NB>(p);
+    return launch_wide<2, LA, LB, NB, SEG>(p, epi, s);
 }
 
 // ------------------------------- epilogues ----------------------------------
 // Outputs stored as they are: to out[z] in its type, or, where a tile takes a part of
 // the reduction, to that part in fp32 (added to what is there with `more`: a later
-// piece of the reduction).  A part holds its tile alone, side x side.
+// piece of the reduction).  A part holds its tile alone.
 struct EpiStore {
     static constexpr bool kStats = false;
     static constexpr int kOuts = 1;
@@ -855,13 +690,15 @@ struct EpiStore {
     }
     __device__ __forceinline__ Dest dest(int, const Place &p) const {
         if (p.part >= 0)
-            return {parts + (int64_t)p.part * p.side * p.side - ((int64_t)p.m0 * p.side + p.n0),
-                    TW_T_F32, p.side, N, more != 0};
+            return {parts + (int64_t)p.part * p.rows * p.cols - ((int64_t)p.m0 * p.cols + p.n0),
+                    TW_T_F32, p.cols, N, more != 0};
         return {p.z == 0 ? out[0] : p.z == 1 ? out[1] : out[2], type, N, N, false};
     }
+    typedef NoFetch Fetched;
+    __device__ Fetched fetch(int, int) const { return {}; }
     template <int W, bool ALL>
-    __device__ __forceinline__ void values(Row &, int, int, const float (&v)[W], const float (&)[W],
-                                           float (&o)[kOuts][W]) const {
+    __device__ __forceinline__ void values(Row &, const Fetched &, int, const float (&v)[W],
+                                           const float (&)[W], float (&o)[kOuts][W]) const {
 #pragma unroll
         for (int e = 0; e < W; ++e) o[0][e] = v[e];
     }
@@ -887,12 +724,12 @@ inline hipError_t launch_sum_parts(const float *part, int splits, int64_t n, voi
     return hipGetLastError();
 }
 
-// The same for tiles of SIDE x SIDE: part s of tile full + i lies at (s rest + i) SIDE^2.
-template <int SIDE>
+// The same for tiles of 64 WR x 256: part s of tile full + i is number s rest + i.
+template <int WR>
 __global__ __launch_bounds__(256) void sum_tiles_kernel(const float *__restrict__ parts, int splits,
                                                         int rest, int full, int row_regions,
                                                         int nbm, int nbn, EpiStore epi, int M) {
-    constexpr int kBlocks = SIDE * SIDE / 1024;  // workgroups a tile
+    constexpr int kSize = 64 * WR * kWideCols, kBlocks = kSize / 1024;  // workgroups a tile
     const int i = blockIdx.x / kBlocks;
     int tile = full + i;
     const int z = tile / (nbm * nbn);
@@ -902,83 +739,73 @@ __global__ __launch_bounds__(256) void sum_tiles_kernel(const float *__restrict_
     else if (row_regions == 4) xcd_tile<4>(tile, nbm, nbn, bm, bn);
     else xcd_tile<2>(tile, nbm, nbn, bm, bn);
     const int at = (blockIdx.x % kBlocks * 256 + threadIdx.x) * 4;
-    const int m = bm * SIDE + at / SIDE, n = bn * SIDE + at % SIDE;
+    const int m = bm * 64 * WR + at / kWideCols, n = bn * kWideCols + at % kWideCols;
     if (m >= M || n >= epi.N) return;
-    const float *q = parts + (int64_t)i * (SIDE * SIDE) + at;
+    const float *q = parts + (int64_t)i * kSize + at;
     f32x4 v = *reinterpret_cast<const f32x4 *>(q);
 #pragma unroll 4
     for (int s = 1; s < splits; ++s)
-        v += *reinterpret_cast<const f32x4 *>(q + (int64_t)s * rest * (SIDE * SIDE));
+        v += *reinterpret_cast<const f32x4 *>(q + (int64_t)s * rest * kSize);
     store4(z == 0 ? epi.out[0] : z == 1 ? epi.out[1] : epi.out[2], epi.type,
            (int64_t)m * epi.N + n, v);
 }
 
-// How a product stored as it is takes its tiles: the first `full` of the larger ones whole
-// and the rest in `splits` parts, or the smaller tiles in `splits` parts.
+// How a product stored as it is takes its tiles: the first `full` whole and the rest in
+// `splits` parts of the reduction.
 struct SplitPlan {
-    bool wide;
+    int rows;  // of a tile: 256 or 128
     int splits, full;
     size_t bytes;  // of the parts
 };
-// The plan of the least estimated time (us): 1.6 a stage and round of the larger tiles,
-// 0.7 of the smaller ones' 32-deep stages; the parts' way through memory, 8 bytes an
-// output and part at 4.5 TB/s.  `pieces`: the reduction comes in pieces, every
-// tile keeps its parts from one to the next.
-template <int NB, int SEG>
+// The plan of the least estimated time: tiles_us for the tiles taken whole, in rounds of
+// the chip, and for the parts of the others; the parts' way through memory, 8 bytes an
+// output and part at 4.5 TB/s, and 3 us for the kernel that adds them.  `pieces`: the
+// reduction comes in pieces, every tile keeps its parts from one to the next.
+template <int SEG>
 SplitPlan split_plan(const TileArgs &p, bool pieces) {
-    const int64_t big = wide_tiles<NB>(p), stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
-    const int64_t small = ((int64_t)p.M + 127) / 128 * (((int64_t)p.N + 127) / 128) * p.groups;
-    SplitPlan best{};
+    const int64_t stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
+    SplitPlan best{128, 1, (int)wide_tiles<2, 1>(p), 0};
     double least = 1e30;
-    auto offer = [&](bool wide, int64_t full, int s, double us) {
-        if (us >= least) return;
-        least = us;
-        const int64_t rest = wide ? big - full : small, side = wide ? 256 : 128;
-        const bool parts = pieces || s > 1;
-        best = {wide, s, (int)(parts ? full : wide ? big : 0),
-                parts ? (size_t)rest * s * side * side * 4 : 0};
+    auto offer = [&](auto wr) {
+        constexpr int WR = decltype(wr)::value;
+        const int64_t tiles = wide_tiles<WR, 1>(p), size = 64 * WR * kWideCols;
+        for (int s = 1; s <= 64 && s <= stages; ++s) {
+            const int64_t per = (stages + s - 1) / s;
+            if ((stages + per - 1) / per != s) continue;  // (every part has a stage)
+            const bool parts = pieces || s > 1;
+            const int64_t full = !parts ? tiles : pieces ? 0 : tiles / kWideGrid * kWideGrid;
+            const int64_t rest = tiles - full;
+            double us = tiles_us<WR>(full, stages) + (rest ? tiles_us<WR>(rest * s, per) : 8.0) - 8.0;
+            if (parts) us += 3.0 + (double)rest * s * size * 8 / 4.5e6;
+            if (us >= least) continue;
+            least = us;
+            best = {64 * WR, s, (int)full, parts ? (size_t)rest * s * size * 4 : 0};
+        }
     };
-    const int64_t whole = pieces ? 0 : big / kWideGrid * kWideGrid;
-    for (int s = 1; s <= 64 && s <= stages; ++s) {
-        const int64_t per = (stages + s - 1) / s;
-        if ((stages + per - 1) / per != s) continue;  // (every part has a stage)
-        auto parts_us = [&](int64_t tiles, int64_t side) {
-            return s == 1 && !pieces ? 0.0 : 3.0 + (double)tiles * s * side * side * 8 / 4.5e6;
-        };
-        const int64_t full = s == 1 ? 0 : whole, rest = big - full;
-        offer(true, full, s,
-              1.6 * (full / kWideGrid * stages + (rest * s + kWideGrid - 1) / kWideGrid * per) +
-                  parts_us(rest, 256));
-        if (!pieces)
-            offer(false, 0, s,
-                  0.7 * ((small * s + kWideGrid - 1) / kWideGrid) * 2 * per + parts_us(small, 128));
-    }
+    offer(std::integral_constant<int, 4>{});
+    offer(std::integral_constant<int, 2>{});
     return best;
 }
 
 // A product stored as it is.  parts: split_plan's bytes; `last`: the sums are to be
 // stored (with pieces: of the last one).
-template <int LA, int LB, int NB, int SEG>
-hipError_t launch_split(TileArgs p, const SplitPlan &plan, EpiStore epi, bool last, hipStream_t s) {
+template <int LA, int LB, int SEG>
+hipError_t launch_split(TileArgs p, const SplitPlan &plan, const EpiStore &epi, bool last,
+                        hipStream_t s) {
     p.splits = plan.splits;
     p.full = plan.full;
-    if (p.R == 0) {  // zeros
-        p.splits = 1;
-        return launch_ring<LA, LB, NB, SEG>(p, epi, s);
-    }
-    const hipError_t e = plan.wide ? launch_wide<LA, LB, NB, SEG>(p, epi, s)
-                                   : launch_ring<LA, LB, NB, SEG>(p, epi, s);
+    const hipError_t e = plan.rows == 256 ? launch_wide<4, LA, LB, 1, SEG>(p, epi, s)
+                                          : launch_wide<2, LA, LB, 1, SEG>(p, epi, s);
     if (e != hipSuccess || !plan.bytes || !last) return e;
-    const int side = plan.wide ? 256 : 128;
-    const int nbm = (p.M + side - 1) / side, nbn = (p.N + side - 1) / side;
-    const int rest = nbm * nbn * p.groups - plan.full;
-    const unsigned grid = (unsigned)(side * side / 1024) * rest;
-    if (plan.wide)
-        sum_tiles_kernel<256><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full,
-                                                   wide_row_regions(nbm, nbn), nbm, nbn, epi, p.M);
+    const int nbm = (p.M + plan.rows - 1) / plan.rows, nbn = (p.N + kWideCols - 1) / kWideCols;
+    const int rest = nbm * nbn * p.groups - plan.full, regions = wide_row_regions(nbm, nbn);
+    const unsigned grid = (unsigned)(plan.rows * kWideCols / 1024) * rest;
+    if (plan.rows == 256)
+        sum_tiles_kernel<4><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full, regions,
+                                                 nbm, nbn, epi, p.M);
     else
-        sum_tiles_kernel<128><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, 0, 2, nbm, nbn,
-                                                   epi, p.M);
+        sum_tiles_kernel<2><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full, regions,
+                                                 nbm, nbn, epi, p.M);
     return hipGetLastError();
 }
 
