@@ -169,7 +169,7 @@ __global__ __launch_bounds__(kFewThreads) void few_hidden_kernel(
     for (int m = 0; m < MB; ++m) xp[m] = x + min(16 * m + (lane & 15), M - 1) * x_stride + k8;
     const int steps = (K + 31) / 32, per = (steps + NW - 1) / NW;
     f32x4 acc[NM * C][MB] = {};
-    constexpr int U = 10 / (NM * C + MB) < 1 ? 1 : 10 / (NM * C + MB);  // steps in a batch
+    constexpr int U = 6 / (NM * C + MB) < 1 ? 1 : 6 / (NM * C + MB);  // steps in a batch
     few_product<NM * C, MB, U>(wp, xp, K, wave * per, min(wave * per + per, steps), acc);
 #pragma unroll
     for (int b = 0; b < NM * C; ++b)
@@ -225,109 +225,132 @@ hipError_t few_hidden(const uint16_t *x, int64_t x_stride, const uint16_t *w0, c
 }
 
 // ------------------ rows times a matrix of reduction rows --------------------
-// part[split][m][k] = sum over n of the split of h[m][n] w[n][k]: w rows are read
-// whole, 128 columns a workgroup (16 lanes of 16 bytes, 4 rows a wave), the products
-// on the vector units (a matrix instruction would need w transposed), h from LDS.
-constexpr int kFewDownMax = 16;  // token rows
-constexpr int kDownThreads = 512, kDownRows = 256;  // reduction rows between two barriers
+// part[split][m][k] = sum over n of the split of h[m][n] w[n][k], for up to 64 token
+// rows.  A wave reads 32 rows of w, 128 columns wide, 16 bytes a lane: lane l has the 8
+// rows from 8 (l / 16) on of the 8 columns from 8 (l % 16) on.  A matrix instruction
+// wants one column's 8 rows in a lane, so pairs of rows are interleaved (one permute a
+// register) and instruction j of 8 takes every lane's column j.
+constexpr int kFewDownMax = 64;  // token rows
+constexpr int kDownGrid = 256;
+template <int MB>
+constexpr int kDownWaves = MB == 4 ? 4 : 8;  // (their sums are 8 MB KB of LDS each)
 
-template <int MT>
-__global__ __launch_bounds__(kDownThreads) void few_down_kernel(const uint16_t *__restrict__ h,
+template <int MB>
+__global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(const uint16_t *__restrict__ h,
                                                                 const uint16_t *__restrict__ w,
                                                                 int M, int K, int N, int per,
                                                                 float *__restrict__ part) {
-    constexpr int NW = kDownThreads / kWave, STEPS = kDownRows / (4 * NW);
-    __shared__ float hs[MT][kDownRows];
-    __shared__ __attribute__((aligned(16))) float sums[NW / 2][MT][128];
+    constexpr int NW = kDownWaves<MB>;
+    extern __shared__ __attribute__((aligned(16))) char smem[];  // [NW][8 MB][64] f32x4
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = blockIdx.x * 128 + 8 * (lane & 15);
-    const int at = col < K ? col : K - 8;  // (columns past K repeat the last ones)
+    const int l16 = lane & 15, r8 = 8 * (lane >> 4);
+    const int at = min(blockIdx.x * 128 + 8 * l16, K - 8);  // (past K: the last columns again)
     const int n0 = blockIdx.y * per, n1 = min(n0 + per, N);
-    const int r0 = 4 * wave + (lane >> 4);
-    float acc[MT][8] = {};
-    for (int c = n0; c < n1; c += kDownRows) {
-        u32x4 v[STEPS];
+    const uint16_t *hp[MB];
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int n = c + 4 * NW * i + r0;
-            v[i] = ld16(w + (int64_t)min(n, n1 - 1) * K + at);
+    for (int m = 0; m < MB; ++m) hp[m] = h + (int64_t)min(16 * m + l16, M - 1) * N;
+    struct Step {
+        u32x4 w[8], h[MB];
+    };
+    // rows past the split (n1 is a multiple of 8): the first ones again, used as zeros
+    auto load = [&](Step &s, int n) {
+        const int row = n + r8 < n1 ? n + r8 : n0;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) s.h[m] = ld16(hp[m] + row);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s.w[r] = ld16(w + (int64_t)(row + r) * K + at);
+    };
+    f32x4 acc[8][MB] = {};
+    auto multiply = [&](Step &s, int n) {
+        if (n + r8 >= n1) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s.w[r] = u32x4{};
+#pragma unroll
+            for (int m = 0; m < MB; ++m) s.h[m] = u32x4{};
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < MT * kDownRows; i += kDownThreads) {
-            const int m = i / kDownRows, n = c + i % kDownRows;
-            hs[m][i % kDownRows] =
-                m < M && n < n1 ? bf_lo((uint32_t)h[(int64_t)m * N + n]) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            u32x4 v;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                v[p] = __builtin_amdgcn_perm(s.w[2 * p + 1][j >> 1], s.w[2 * p][j >> 1],
+                                             j & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                acc[j][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, s.h[m]), acc[j][m],
+                    0, 0, 0);
         }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-            const int r = 4 * NW * i + r0;
-            // (rows past the split repeat its last one, which must not enter: 0 times
-            // an infinity is NaN)
-            const bool in = c + r < n1;
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] = in ? (e & 1 ? bf_hi(v[i][e >> 1]) : bf_lo(v[i][e >> 1])) : 0.0f;
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const float hv = hs[m][r];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[m][e] = fmaf(hv, f[e], acc[m][e]);
-            }
+    };
+    constexpr int kStep = 32 * NW;
+    int n = n0 + 32 * wave;
+    if (n < n1) {
+        Step a, b;
+        load(a, n);
+        for (;; n += 2 * kStep) {
+            if (n + kStep < n1) load(b, n + kStep);
+            multiply(a, n);
+            if (n + kStep >= n1) break;
+            if (n + 2 * kStep < n1) load(a, n + 2 * kStep);
+            multiply(b, n + kStep);
+            if (n + 2 * kStep >= n1) break;
         }
     }
+    // The waves' sums meet in LDS.  Lane l of acc[j][m] holds token l % 16, columns 8 (4
+    // (l / 16) + e) + j; a thread then adds the 8 columns of one token.
+    f32x4 *sums = reinterpret_cast<f32x4 *>(smem);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            acc[m][e] += __shfl_xor(acc[m][e], 16);
-            acc[m][e] += __shfl_xor(acc[m][e], 32);
-        }
-    // the waves' sums, halves of them at a time
+        for (int m = 0; m < MB; ++m) sums[((wave * 8 + j) * MB + m) * kWave + lane] = acc[j][m];
+    __syncthreads();
+    const float *f = reinterpret_cast<const float *>(smem);
+    for (int t = threadIdx.x; t < 256 * MB; t += 64 * NW) {
+        const int mb = t >> 8, m = 16 * mb + (t & 15), i = t >> 4 & 15;
+        const int col = blockIdx.x * 128 + 8 * i;
+        if (m >= M || col >= K) continue;
+        float s[8] = {};
 #pragma unroll
-    for (int half = NW / 2; half >= 1; half /= 2) {
-        __syncthreads();
-        if (wave >= half && wave < 2 * half && lane < 16)
+        for (int q = 0; q < NW; ++q)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sums[wave - half][m][8 * lane + e] = acc[m][e];
-        __syncthreads();
-        if (wave < half && lane < 16)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[m][e] += sums[wave][m][8 * lane + e];
-    }
-    if (wave || lane >= 16 || col >= K) return;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (m >= M) continue;
-        float *p = part + ((int64_t)blockIdx.y * M + m) * K + col;
-        *reinterpret_cast<f32x4 *>(p) = f32x4{acc[m][0], acc[m][1], acc[m][2], acc[m][3]};
-        *reinterpret_cast<f32x4 *>(p + 4) = f32x4{acc[m][4], acc[m][5], acc[m][6], acc[m][7]};
+            for (int j = 0; j < 8; ++j)
+                s[j] += f[((((q * 8 + j) * MB + mb) * kWave) + (i >> 2) * 16 + (m & 15)) * 4 + (i & 3)];
+        f32x4 *out = reinterpret_cast<f32x4 *>(part + ((int64_t)blockIdx.y * M + m) * K + col);
+        out[0] = f32x4{s[0], s[1], s[2], s[3]};
+        out[1] = f32x4{s[4], s[5], s[6], s[7]};
     }
 }
 
-// Splits of N that give every CU a workgroup, none of fewer than 32 rows.
-int few_down_splits(int K, int N) {
-    const int cols = (K + 127) / 128, most = (N + 31) / 32;
-    const int want = (256 + cols - 1) / cols;
-    return want < most ? want : most;
+// Parts of N: about kDownGrid workgroups, each with as many steps of 32 rows for every
+// one of its waves.
+struct DownSplit {
+    int splits, per;
+};
+DownSplit few_down_split(int M, int K, int N) {
+    const int rows = 32 * (M <= 32 ? kDownWaves<1> : kDownWaves<4>);
+    const int cols = (K + 127) / 128, rounds = (N + rows - 1) / rows;
+    const int most = kDownGrid / cols > 1 ? kDownGrid / cols : 1;
+    const int each = (rounds + most - 1) / most;
+    return {(rounds + each - 1) / each, rows * each};
 }
 
-hipError_t launch_few_down(const uint16_t *h, const uint16_t *w, int M, int K, int N,
-                                  float *part, hipStream_t s) {
-    const int splits = few_down_splits(K, N);
-    const int per = (N + splits - 1) / splits;
-    const dim3 grid((K + 127) / 128, splits);
-    if (M == 1) few_down_kernel<1><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
-    else if (M == 2) few_down_kernel<2><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
-    else if (M <= 4) few_down_kernel<4><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
-    else if (M <= 8) few_down_kernel<8><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
-    else few_down_kernel<16><<<grid, kDownThreads, 0, s>>>(h, w, M, K, N, per, part);
+template <int MB>
+hipError_t few_down_as(const uint16_t *h, const uint16_t *w, int M, int K, int N, float *part,
+                       hipStream_t s) {
+    constexpr auto kernel = &few_down_kernel<MB>;
+    constexpr int lds = kDownWaves<MB> * 8 * MB * kWave * 16;
+    const hipError_t e = lds_limit_once<kernel>(lds);
+    if (e != hipSuccess) return e;
+    const DownSplit d = few_down_split(M, K, N);
+    kernel<<<dim3((K + 127) / 128, d.splits), 64 * kDownWaves<MB>, lds, s>>>(h, w, M, K, N, d.per, part);
     return hipGetLastError();
+}
+
+hipError_t few_down(const uint16_t *h, const uint16_t *w, int M, int K, int N, float *part,
+                    hipStream_t s) {
+    const int mb = few_blocks_of(M);
+    if (mb == 1) return few_down_as<1>(h, w, M, K, N, part, s);
+    return mb == 2 ? few_down_as<2>(h, w, M, K, N, part, s) : few_down_as<4>(h, w, M, K, N, part, s);
 }
 
 template <int ACT>
@@ -360,7 +383,7 @@ static SplitPlan dw_plan(int M, int K, int N) {
 }
 
 size_t ffn_fwd_part_bytes(int M, int K, int N) {
-    if (M <= kFewDownMax) return (size_t)few_down_splits(K, N) * M * K * 4;
+    if (M <= kFewDownMax) return (size_t)few_down_split(M, K, N).splits * M * K * 4;
     return down_plan(M, K, N).bytes;
 }
 size_t ffn_bwd_part_bytes(int M, int K, int N) {
@@ -380,9 +403,9 @@ hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg
 hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, int N, void *y,
                            int y_type, float *part, hipStream_t s) {
     if (M <= kFewDownMax) {
-        const hipError_t e = launch_few_down(h, wd, M, K, N, part, s);
+        const hipError_t e = few_down(h, wd, M, K, N, part, s);
         if (e != hipSuccess) return e;
-        return launch_sum_parts(part, few_down_splits(K, N), (int64_t)M * K, y, y_type, s);
+        return launch_sum_parts(part, few_down_split(M, K, N).splits, (int64_t)M * K, y, y_type, s);
     }
     return launch_split<kRows, kCols, 1>(TileArgs{{h}, {wd}, N, K, M, K, N},
                                             down_plan(M, K, N), EpiStore{{y}, y_type, K, part},

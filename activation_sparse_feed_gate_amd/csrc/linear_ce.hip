@@ -82,36 +82,36 @@ struct EpiSoft {
 
 // Up to 64 token rows (16 MB): a wave takes 32 words and all of K, a workgroup of 4
 // waves the 128 of a column block.
-constexpr int kFewSoftThreads = 256;
+constexpr int kSoftBlocks = 2, kFewSoftThreads = 512 / kSoftBlocks;
 template <int MB>
 __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
     const uint16_t *__restrict__ x, int64_t x_stride, const uint16_t *__restrict__ w, int M, int K,
     int V, Soft *__restrict__ part) {
     __shared__ Soft all[kFewSoftThreads / kWave][16 * MB];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int v0 = blockIdx.x * 128 + 32 * wave;
+    const int v0 = blockIdx.x * 128 + 16 * kSoftBlocks * wave;
     const int k8 = 8 * (lane >> 4);
-    const uint16_t *wp[2], *xp[MB];
+    const uint16_t *wp[kSoftBlocks], *xp[MB];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < kSoftBlocks; ++b)
         wp[b] = w + (int64_t)min(v0 + 16 * b + (lane & 15), V - 1) * K + k8;
 #pragma unroll
     for (int m = 0; m < MB; ++m) xp[m] = x + min(16 * m + (lane & 15), M - 1) * x_stride + k8;
-    f32x4 acc[2][MB] = {};
-    few_product<2, MB, 18 / (2 + MB)>(wp, xp, K, 0, (K + 31) / 32, acc);
+    f32x4 acc[kSoftBlocks][MB] = {};
+    few_product<kSoftBlocks, MB, 9 / (kSoftBlocks + MB)>(wp, xp, K, 0, (K + 31) / 32, acc);
     const EpiSoft epi{part, M, V};
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
         EpiSoft::Row row(epi, {});
-        float l[2][4];
+        float l[kSoftBlocks][4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kSoftBlocks; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) l[b][e] = acc[b][m][e];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) epi.most<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+        for (int b = 0; b < kSoftBlocks; ++b) epi.most<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) epi.add<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+        for (int b = 0; b < kSoftBlocks; ++b) epi.add<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
         epi.join<16>(row);
         epi.join<32>(row);
         if (lane < 16) all[wave][16 * m + lane] = {row.top, row.sum};
@@ -122,6 +122,15 @@ __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
 #pragma unroll
     for (int i = 1; i < kFewSoftThreads / kWave; ++i) j = join_soft(j, all[i][threadIdx.x]);
     part[(int64_t)blockIdx.x * M + threadIdx.x] = j;
+}
+
+// Whether few_soft_kernel takes a product.  A wave of it reads the token rows from the L2
+// for its own 32 words, which from 17 rows on costs more than tiles save, unless these
+// (256 words wide) would leave half of the CUs idle.  Measured (us, this kernel and
+// tiles): 16 rows, 1024 x 32768 20, 30; 2048 x 49999 52, 48 (from memory 87, 93); 32
+// rows 24, 30 and 66, 49; 64 rows 32, 31.
+bool streams_words(int M, int V) {
+    return M <= 16 || (M <= 32 && V <= kWideCols * kWideGrid / 2);
 }
 
 // Joins the column blocks of a row and takes the target's logit.  TPR threads a row:
@@ -198,7 +207,8 @@ struct EpiD {
         }
     };
     // A row without a target has scale 0 and an infinite top, below which every
-    // exponential is 0.
+    // exponential is 0.  A row of scale 0 has a D of 0 also where its logits are NaN or
+    // infinite.
     struct Row {
         float top, scale;
         int t;  // the target's column of the piece, or -1
@@ -237,6 +247,10 @@ struct EpiD {
         }
 #pragma unroll
         for (int e = 0; e < W; ++e) o[0][e] = ALL || n + e < N ? p[e] * r.scale : 0.0f;
+        if (r.scale == 0.0f) {
+#pragma unroll
+            for (int e = 0; e < W; ++e) o[0][e] = 0.0f;
+        }
     }
 };
 
@@ -277,21 +291,19 @@ hipError_t launch_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *w,
     const TileArgs p{{x}, {w}, x_stride, K, M, V, K};
     Soft *part = static_cast<Soft *>(ws);
     hipError_t e;
-    if (M <= kFewRowsMax) {
-        const int mb = few_blocks_of(M), grid = (V + 127) / 128;
-        if (mb == 1)
+    if (streams_words(M, V)) {
+        const int grid = (V + 127) / 128;
+        if (few_blocks_of(M) == 1)
             few_soft_kernel<1><<<grid, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
-        else if (mb == 2)
-            few_soft_kernel<2><<<grid, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
         else
-            few_soft_kernel<4><<<grid, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
+            few_soft_kernel<2><<<grid, kFewSoftThreads, 0, s>>>(x, x_stride, w, M, K, V, part);
         e = hipGetLastError();
     } else {
         e = launch_tiles<kRows, kRows, 1, 1>(p, EpiSoft{part, M, V}, s);
     }
     if (e != hipSuccess) return e;
     const int blocks = (V + 127) / 128;
-    if (M <= 256)
+    if (M <= 512)
         ce_rows_kernel<256><<<M, 256, 0, s>>>(part, blocks, x, x_stride, w, t, M, K, V, loss, lse);
     else
         ce_rows_kernel<16><<<(M + 15) / 16, 256, 0, s>>>(part, blocks, x, x_stride, w, t, M, K, V,

@@ -37,7 +37,7 @@ struct TileArgs {
     int64_t lda, ldb;  // elements between rows
     int M, N, R;
     int splits = 1;  // parts of the reduction, where it is taken in parts
-    int full = 0;    // (larger tiles) the first tiles, which take the reduction whole
+    int full = 0;    // the first tiles, which take the reduction whole
     int groups = 1;  // products of the same shape: a[z], b[z]
     int64_t ldb_last = 0;  // ldb of the third product
 };
@@ -87,8 +87,8 @@ __device__ __forceinline__ void put_out(const Dest &d, int m, int n, const float
 //                                n .. n + W - 1 from those of the product (u: of the
 //                                second weights); ALL: these columns are all within N,
 //   dest(o, place)               says where output o of a tile goes,
-//   stores(place)                how many stores a wave of the larger tiles makes of a
-//                                tile inside the product, or,
+//   stores(place)                how many stores a wave makes of a tile inside the
+//                                product (0, 8, 16, 24, 32 or 48), or,
 // where it reduces over the columns (kStats),
 //   most<W, ALL>(row, n, v), add<W, ALL>(row, n, v)   two passes over a lane's columns,
 //   join<L>(row)                            lanes l and l ^ L hold one row,
@@ -98,13 +98,14 @@ struct NoRaw {
 };
 struct NoFetch {};
 
-// ----------------------------- 256 x 256 tiles ------------------------------
-// 256 x 256 outputs (NB = 2: 256 x 128 of each weight matrix) a workgroup of 8
+// --------------------------------- tiles ------------------------------------
+// 64 WR x 256 outputs (NB = 2: 64 WR x 128 of each weight matrix) a workgroup of 2 WR
 // waves, 64 x 128 outputs each (wave row wm, wave column wn); a workgroup a CU,
 // walking tiles, the next tile's first stages on their way while a tile is
-// written.  A stage is 64 reduction elements, 32 KB of each operand; two stages
-// fill 128 KB of LDS, and the loads of the stage after next enter a stage's slot in two
-// parts, as soon as no wave reads what they replace:
+// written.  WR is 4, or 2 where a product has too few tiles for the chip.  A stage is
+// 64 reduction elements, 128 bytes of each of the tile's 64 WR + 256 rows; two stages
+// fill 128 KB of LDS (WR = 2: 96 KB), and the loads of the stage after next enter a
+// stage's slot in two parts, as soon as no wave reads what they replace:
 //
 //   step   matrix instructions   fragments read              loads into this slot
 //   0      A x B0                B1 of this stage
@@ -118,13 +119,22 @@ struct NoFetch {};
 // matrix instructions of 16 x 16 x 32, so its reads are there when the next one
 // begins.
 //
-// A kRows operand lies in LDS as 256 rows of 128 bytes, chunk c of row r at c ^ ((r
+// A kRows operand lies in LDS as rows of 128 bytes, chunk c of row r at c ^ ((r
 // >> 1) & 7): 16 consecutive rows of one chunk fall on 16 different bank groups.
-// A kCols operand is two regions of 64 reduction rows of 128 columns (256
+// A kCols operand is regions of 64 reduction rows of 128 columns (256
 // bytes), read with the transposing ds_read_b64_tr_b16; chunk c of row r lies at c ^
 // 2 f(r), f = r % 4 + 4 (r / 8 % 2): the 8 rows that 32 lanes read, two
-// chunks of each, fill the 16 chunks of a row of banks once.  Loads of either
-// cover whole 128-byte lines.
+// chunks of each, fill the 16 chunks of a row of banks once (no conflicts counted).
+// Loads of either cover whole 128-byte lines.
+//
+// A wave's 64 x 128 outputs are 128 accumulator registers a lane, which leave room for a
+// second set of B's fragments; they read 24 KB of LDS for 128 matrix instructions.  128 x
+// 128 a wave would read a third less, but did not fit: its accumulators spill.
+// What bounds a large product is power: on operands of zeros, where nothing toggles,
+// 16384 x 8192 x 2048 and its like run at 1740 to 1830 TFLOP/s (kRows x kRows), on
+// normal ones at 1330 to 1390; kRows x kCols 1650 and 1300.  16 x 16 x 32
+// instructions draw less than 32 x 32 x 16 ones for the same work (alone on normal
+// operands: 1957 and 1770 TFLOP/s).
 constexpr int kWideCols = 256, kWideK = 64;
 constexpr int kWideLine = 128;                    // bytes of a kRows row in a stage
 constexpr int kWideRegion = kWideK * 256;         // 128 columns of a kCols operand
@@ -704,23 +714,37 @@ struct EpiStore {
     }
 };
 
-// out = the sum of the parts, in their order.
+// out = the sum of the parts: each of a workgroup's 4 waves takes every fourth part of
+// the same 256 outputs, 4 at a time, so that the latencies of 16 parts are one.
 template <int T>
-__global__ __launch_bounds__(64) void sum_parts_kernel(const float *__restrict__ part, int splits,
-                                                       int64_t n, void *__restrict__ out) {
-    const int64_t at = ((int64_t)blockIdx.x * 64 + threadIdx.x) * 4;
-    if (at >= n) return;
-    f32x4 v = *reinterpret_cast<const f32x4 *>(part + at);
-#pragma unroll 8
-    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4 *>(part + s * n + at);
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float *__restrict__ part, int splits,
+                                                        int64_t n, void *__restrict__ out) {
+    __shared__ f32x4 sums[3][kWave];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t at = ((int64_t)blockIdx.x * kWave + lane) * 4;
+    f32x4 v{};
+    if (at < n)
+        for (int s = wave; s < splits; s += 16) {
+            f32x4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = *reinterpret_cast<const f32x4 *>(part + min(s + 4 * i, splits - 1) * n + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v += s + 4 * i < splits ? w[i] : f32x4{};
+        }
+    if (wave) sums[wave - 1][lane] = v;
+    __syncthreads();
+    if (wave || at >= n) return;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v += sums[i][lane];
     store4(out, T, at, v);
 }
 inline hipError_t launch_sum_parts(const float *part, int splits, int64_t n, void *out, int type,
                                    hipStream_t s) {
     if (n == 0) return hipSuccess;
     const unsigned grid = (unsigned)((n / 4 + 63) / 64);
-    if (type == TW_T_F32) sum_parts_kernel<TW_T_F32><<<grid, 64, 0, s>>>(part, splits, n, out);
-    else sum_parts_kernel<TW_T_BF16><<<grid, 64, 0, s>>>(part, splits, n, out);
+    if (type == TW_T_F32) sum_parts_kernel<TW_T_F32><<<grid, 256, 0, s>>>(part, splits, n, out);
+    else sum_parts_kernel<TW_T_BF16><<<grid, 256, 0, s>>>(part, splits, n, out);
     return hipGetLastError();
 }
 
@@ -742,10 +766,16 @@ __global__ __launch_bounds__(256) void sum_tiles_kernel(const float *__restrict_
     const int m = bm * 64 * WR + at / kWideCols, n = bn * kWideCols + at % kWideCols;
     if (m >= M || n >= epi.N) return;
     const float *q = parts + (int64_t)i * kSize + at;
-    f32x4 v = *reinterpret_cast<const f32x4 *>(q);
-#pragma unroll 4
-    for (int s = 1; s < splits; ++s)
-        v += *reinterpret_cast<const f32x4 *>(q + (int64_t)s * rest * kSize);
+    f32x4 v{};
+    for (int s = 0; s < splits; s += 4) {  // (4 latencies in one)
+        f32x4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            w[k] = *reinterpret_cast<const f32x4 *>(q + (int64_t)min(s + k, splits - 1) * rest *
+                                                            kSize);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v += s + k < splits ? w[k] : f32x4{};
+    }
     store4(z == 0 ? epi.out[0] : z == 1 ? epi.out[1] : epi.out[2], epi.type,
            (int64_t)m * epi.N + n, v);
 }

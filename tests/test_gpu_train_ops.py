@@ -389,6 +389,27 @@ def test_ce_targets_outside(tw, M):
     assert (out["loss"] == 0).all() and (got["dx"] == 0).all() and (got["dw"] == 0).all()
 
 
+@pytest.mark.parametrize("M", [6, 300])
+def test_ce_rows_left_out_hold_anything(tw, M):
+    """NaN and infinities in rows that are left out, or whose dloss is 0: their dx is 0
+    and the others' as it was."""
+    K, V = 136, 700
+    x, w, t = ce_case(M, K, V)
+    t[:] = t.clamp(min=0)
+    t[0], t[M - 1] = -100, -100
+    dloss = rnd(7, M, dtype=F32)
+    dloss[2] = 0.0
+    lse = tw.linear_ce(x, w, t)["lse"]
+    ws = torch.empty(tw.tw_linear_ce_bwd_workspace_bytes(M, K, V), dtype=torch.uint8, device="cuda")
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    tw.tw_linear_ce_bwd(dloss, x, w, t, lse, ws, dx=a)
+    odd = x.clone()
+    odd[0, 3], odd[2, 7], odd[M - 1] = float("nan"), float("inf"), float("-inf")
+    lse = tw.linear_ce(odd, w, t)["lse"]
+    tw.tw_linear_ce_bwd(dloss, odd, w, t, lse, ws, dx=b)
+    assert torch.equal(a, b) and (b[[0, 2, M - 1]] == 0).all() and (b[1] != 0).any()
+
+
 def test_ce_no_rows(tw):
     x, w, t = rnd(1, 0, 64), rnd(2, 100, 64), torch.empty(0, dtype=torch.int64, device="cuda")
     out = tw.linear_ce(x, w, t)
@@ -441,6 +462,108 @@ def test_ce_gradient_by_differences(tw):
             down = (R.ce(x, w, t)[0] * dloss).sum()
             v[at] = keep
             assert abs(((up - down) / (2 * h) - ref[name][0][at]).item()) < 1e-6
+
+
+@pytest.mark.parametrize("M", [16, 17, 32, 33, 64, 65, 256, 257])
+def test_at_the_rules_row_counts(tw, M):
+    """Row counts on both sides of where another kernel takes over."""
+    K, N, V = 264, 1040, 1000
+    x, w, dy = rnd(M, M, K), weights(K, N), rnd(M + 1, M, K)
+    out = tw.gated_ffn(x, *w, keep=True)
+    check_ffn(x, w, "silu", out)
+    got = tw.gated_ffn_backward(dy, x, *w, out["g"], out["u"])
+    for k, (v, e) in R.ffn_bwd(d64(dy), d64(x), *(d64(t) for t in w), d64(out["g"]),
+                               d64(out["u"]), "silu").items():
+        R.close(got[k], v, e)
+    x, w, t = ce_case(M, K, V)
+    out = tw.linear_ce(x, w, t)
+    loss, el, lse, es = R.ce(d64(x), d64(w), t)
+    R.close(out["lse"], lse, es)
+    R.close(out["loss"], loss, el)
+
+
+# ---------------------------------------------------------- past 32-bit offsets --
+def test_ffn_past_32_bits(tw):
+    """Hidden rows past 2^31 elements: the last rows' outputs, and the weight gradients of
+    the first and last neurons, which every row enters."""
+    M, K, N = 540_000, 64, 4096
+    assert M * N > 1 << 31
+    x, dy, w = rnd(1, M, K), rnd(2, M, K), weights(K, N)
+    out = tw.gated_ffn(x, *w, keep=True)
+    g, u = out["g"], out["u"]
+    for rows in (slice(0, 40), slice(M - 300, M)):
+        check_ffn(x[rows], w, "silu", {k: v[rows] for k, v in out.items()})
+    got = tw.gated_ffn_backward(dy, x, *w, g, u, dx_dtype=F32, dw_dtype=F32)
+    for rows in (slice(0, 40), slice(M - 300, M)):
+        ref = R.ffn_bwd(d64(dy[rows]), d64(x[rows]), *(d64(t) for t in w), d64(g[rows]),
+                        d64(u[rows]), "silu")
+        R.close(got["dx"][rows], *ref["dx"])
+    for of in (slice(0, 8), slice(N - 8, N)):
+        ref = R.ffn_bwd(d64(dy), d64(x), *(d64(t[of]) for t in w), d64(g[:, of]), d64(u[:, of]),
+                        "silu")
+        for k in ("dwg_t", "dwu_t", "dwd"):
+            R.close(got[k][of], *ref[k])
+    del out, g, u, got
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_ce_past_32_bits(tw, M):
+    """A projection of more than 2^31 elements, words at its end."""
+    K, V = 2048, 1_060_000
+    assert K * V > 1 << 31
+    g = torch.Generator("cuda").manual_seed(M)
+    w = torch.empty(V, K, dtype=BF, device="cuda").normal_(0, 2 * K ** -0.5, generator=g)
+    x = rnd(M, M, K)
+    t = torch.arange(V - M, V, device="cuda")
+    t[1] = 5
+    out = tw.linear_ce(x, w, t)
+    wide = d64(w)
+    loss, el, lse, es = R.ce(d64(x), wide, t)
+    R.close(out["lse"], lse, es)
+    R.close(out["loss"], loss, el)
+    dloss = rnd(7, M, dtype=F32)
+    got = tw.linear_ce_backward(dloss, x, w, t, out["lse"])
+    for k, (v, e) in R.ce_bwd(d64(dloss), d64(x), wide, t, d64(out["lse"])).items():
+        R.close(got[k], v, e)
+    del w, wide, got, loss, el, v, e
+    torch.cuda.empty_cache()
+
+
+def test_rms_past_32_bits(tw):
+    M, K = 1_050_000, 2048
+    assert M * K > 1 << 31
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.empty(M, K, dtype=BF, device="cuda").normal_(generator=g)
+    gamma = rnd(3, K, dtype=F32)
+    out = tw.rmsnorm(x, gamma)
+    q = tw.rmsnorm_quantize(x, gamma)
+    back = tw.rmsnorm_backward(x, x, gamma, out["rstd"])
+    for rows in (slice(0, 5), slice(M - 100, M)):
+        a = tw.rmsnorm(x[rows], gamma)
+        assert torch.equal(a["y"], out["y"][rows]) and torch.equal(a["rstd"], out["rstd"][rows])
+        assert torch.equal(tw.rmsnorm_quantize(x[rows], gamma)["q"], q["q"][rows])
+        assert torch.equal(tw.rmsnorm_backward(x[rows], x[rows], gamma, a["rstd"])["dx"],
+                           back["dx"][rows])
+    del x, out, q, back
+    torch.cuda.empty_cache()
+
+
+def test_clip_past_32_bits(tw):
+    n = (1 << 31) + 5001
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.empty(n, dtype=BF, device="cuda").normal_(generator=g)
+    ends = [x[:1000].clone(), x[-9000:].clone()]
+    ref = math.sqrt(sum(float((d64(c) ** 2).sum()) for c in x.split(1 << 28)))
+    # at most 2048 x 256 threads with 8 sums each, and the tree
+    rel = (n / (2048 * 256 * 8) + 64) * R.U
+    norm = tw.clip_grads([x], 1.0)
+    assert abs(float(norm) - ref) <= rel * ref
+    for was, now in zip(ends, (x[:1000], x[-9000:])):
+        want = d64(was) / (ref + 1e-6)
+        R.close(now, want, (2 * rel + 4 * R.U) * want.abs())
+    del x
+    torch.cuda.empty_cache()
 
 
 # ------------------------------------------------------------------- clipping --
