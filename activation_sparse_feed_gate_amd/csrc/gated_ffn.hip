@@ -11,6 +11,13 @@
 // dz, du and h feed the matrix cores, so they are rounded to bf16 (half a unit
 // of 2^-8 a term, averaged out over the sums they enter); every sum is fp32.
 //
+// What bounds them (bf16, normal operands): 16384 x 2048 x 8192 forward 1254 us, 1315
+// TFLOP/s, the chip's power (tw_tiles.hpp); backward 4096 x 1024 x 4096 224 us, of
+// which dh takes 56 (one round of tiles, whose 170 MB of g, u, dz, du and h pass only
+// after it: 23 us of products, 36 us of memory), dx 73 and the weight gradients 95 (64
+// to 192 tiles on 256 CUs, split and added).  One row, 2048 x 5632: 17.5 us for 69 MB
+// of weights, 4 TB/s.
+//
 // Activations of the form g s(a(g)) with the logistic function s: SiLU has
 // a = g, the tanh form of GELU a = 2 sqrt(2 / pi) (g + 0.044715 g^3), since
 // (1 + tanh(v)) / 2 = s(2 v).  Their derivative is s + g s (1 - s) a'.
@@ -57,6 +64,7 @@ __device__ __forceinline__ Slope activate_slope(float g) {
 template <int ACT>
 struct EpiGlu {
     static constexpr bool kStats = false;
+    static constexpr int kWalk = 4;
     static constexpr int kOuts = 3;
     uint16_t *h, *g, *u;  // g, u or null
     int N;
@@ -86,6 +94,7 @@ struct EpiGlu {
 template <int ACT>
 struct EpiDh {
     static constexpr bool kStats = false;
+    static constexpr int kWalk = 4;
     static constexpr int kOuts = 3;
     const uint16_t *g, *u;
     uint16_t *dz, *du, *h;
@@ -122,7 +131,9 @@ struct EpiDh {
 };
 
 // Up to 64 token rows (16 MB): a workgroup takes up to 16 C hidden neurons of NM
-// matrices, its 8 waves a slice of K each; their sums meet in LDS.
+// matrices, its 8 waves a slice of K each; their sums meet in LDS.  Bound by the stream
+// of weights.  Measured (us, these kernels and tiles): gate and up, 1 row 1024 x 4096
+// 7.6, 17.8, 64 rows 11.9, 18.1; 64 rows 2048 x 5632 20, 28; dh of 64 rows 21, 35.
 template <int ACT>
 struct FewUp {
     static constexpr int NM = 2;
@@ -169,7 +180,9 @@ __global__ __launch_bounds__(kFewThreads) void few_hidden_kernel(
     for (int m = 0; m < MB; ++m) xp[m] = x + min(16 * m + (lane & 15), M - 1) * x_stride + k8;
     const int steps = (K + 31) / 32, per = (steps + NW - 1) / NW;
     f32x4 acc[NM * C][MB] = {};
-    constexpr int U = 6 / (NM * C + MB) < 1 ? 1 : 6 / (NM * C + MB);  // steps in a batch
+    // Steps in a batch of loads: few, as 8 waves have one each on its way (2 x 1024 x 4096:
+    // 7.6 us with 6 loads in a batch, 8.8 with 10, 8.6 with 20).
+    constexpr int U = 6 / (NM * C + MB) < 1 ? 1 : 6 / (NM * C + MB);
     few_product<NM * C, MB, U>(wp, xp, K, wave * per, min(wave * per + per, steps), acc);
 #pragma unroll
     for (int b = 0; b < NM * C; ++b)
@@ -209,7 +222,8 @@ hipError_t few_hidden_as(const uint16_t *x, int64_t x_stride, const uint16_t *w0
 template <class Put>
 hipError_t few_hidden(const uint16_t *x, int64_t x_stride, const uint16_t *w0, const uint16_t *w1,
                       int M, int K, int N, const Put &put, hipStream_t s) {
-    // an even share of the neurons for each of 256 workgroups, at most 32
+    // An even share of the neurons for each of 256 workgroups, at most 32.  (512: 1024 x
+    // 4096 10.0 us for 8.8; 16 at most: 2048 x 5632 16.1 for 12.8.)
     int share = (N + 255) / 256;
     share = share < 4 ? 4 : share > 32 ? 32 : share;
     auto go = [&](auto c, auto mb) {
@@ -229,9 +243,11 @@ hipError_t few_hidden(const uint16_t *x, int64_t x_stride, const uint16_t *w0, c
 // rows.  A wave reads 32 rows of w, 128 columns wide, 16 bytes a lane: lane l has the 8
 // rows from 8 (l / 16) on of the 8 columns from 8 (l % 16) on.  A matrix instruction
 // wants one column's 8 rows in a lane, so pairs of rows are interleaved (one permute a
-// register) and instruction j of 8 takes every lane's column j.
+// register) and instruction j of 8 takes every lane's column j.  Bound by the stream of w
+// (2048 x 5632, with the sum of the parts: 10.7 us for one row, 11.1 for 16, 16.8 for
+// 64; in tiles 17, 18 and 20.  Products on the vector units took 32 us for 16).
 constexpr int kFewDownMax = 64;  // token rows
-constexpr int kDownGrid = 256;
+constexpr int kDownGrid = 256;   // (512: 64 rows 22 us)
 template <int MB>
 constexpr int kDownWaves = MB == 4 ? 4 : 8;  // (their sums are 8 MB KB of LDS each)
 

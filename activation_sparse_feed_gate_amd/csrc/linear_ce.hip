@@ -13,6 +13,11 @@
 //
 // A row whose target is outside [0, V) is left out: its loss and its row of D
 // are 0.
+//
+// What bounds it (bf16, normal operands): 4096 x 1024 x 32768 forward 206 us, 1330
+// TFLOP/s, the chip's power (tw_tiles.hpp); backward 4096 x 1024 x 49999 1123 us for
+// three products of 419 GFLOP, D's exponentials (3 us a tile, while the matrix cores
+// wait) and its 410 MB written and read twice.  4 rows 1024 x 32768: 16.6 us for 67 MB.
 #include <algorithm>
 
 #include "tw_few.hpp"
@@ -45,6 +50,7 @@ __device__ __forceinline__ Soft join_soft(Soft a, Soft b) {
 
 struct EpiSoft {
     static constexpr bool kStats = true;
+    static constexpr int kWalk = 8;
     Soft *part;  // [column blocks][M]
     int M, N;
     typedef NoRaw Raw;
@@ -80,8 +86,10 @@ struct EpiSoft {
     }
 };
 
-// Up to 64 token rows (16 MB): a wave takes 32 words and all of K, a workgroup of 4
-// waves the 128 of a column block.
+// Up to 32 token rows (16 MB): a wave takes 32 words and all of K, a workgroup of 4
+// waves the 128 of a column block.  (16 words a wave: the tokens' fragments, read anew
+// by each, cost more than the shorter waves gain; 16 rows 1024 x 32768 26 us for 22.
+// Batches of 9 loads: 20 us, of 18 22.)
 constexpr int kSoftBlocks = 2, kFewSoftThreads = 512 / kSoftBlocks;
 template <int MB>
 __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
@@ -135,7 +143,9 @@ bool streams_words(int M, int V) {
 
 // Joins the column blocks of a row and takes the target's logit.  TPR threads a row:
 // 16 where rows are many (16 neighbouring rows of a block are then read together),
-// a workgroup where they are few.
+// a workgroup where they are few.  Bound by latency.  Measured (us with the products, a
+// workgroup and 16 threads a row): 4 rows 20.4, 22.6; 300 37.4, 38.9; 512 39.6, 41.0;
+// 1024 66.6, 65.5; 4096 238, 225.
 template <int TPR>
 __global__ __launch_bounds__(256) void ce_rows_kernel(const Soft *__restrict__ part, int blocks,
                                                       const uint16_t *__restrict__ x,
@@ -192,6 +202,7 @@ __global__ __launch_bounds__(256) void ce_rows_kernel(const Soft *__restrict__ p
 // D of a piece of the vocabulary, columns first .. first + N - 1 of V.
 struct EpiD {
     static constexpr bool kStats = false;
+    static constexpr int kWalk = 4;
     static constexpr int kOuts = 1;
     const float *lse, *dloss;
     Targets t;

@@ -1,4 +1,4 @@
-// tw_few.hpp -- products of up to 64 token rows with a weight matrix that is
+// tw_few.hpp -- products of few token rows (up to 64) with a weight matrix that is
 // streamed once from memory: the rows of a decoded batch.
 //
 // Weight fragments come straight from memory into registers (no other wave reads
@@ -12,7 +12,7 @@
 
 namespace tw {
 
-constexpr int kFewRowsMax = 64;   // of the products that stream weight rows
+constexpr int kFewRowsMax = 64;  // of the FFN's products
 
 // Blocks of 16 token rows that M rows take, rounded up to a power of 2.
 constexpr int few_blocks_of(int M) { return M <= 16 ? 1 : M <= 32 ? 2 : 4; }

@@ -79,8 +79,8 @@ __device__ __forceinline__ void put_out(const Dest &d, int m, int n, const float
     }
 }
 
-// An epilogue has, for a row m of the tile, a Raw (what it loads: raw(m); of(l): lane
-// l's) and a Row made of it, and
+// An epilogue has kWalk, the row blocks that walk_tile takes at a time, and, for a row m of
+// the tile, a Raw (what it loads: raw(m); of(l): lane l's) and a Row made of it, and
 //   Fetched, fetch(m, n)         what it loads of the 8 columns n .. n + 7 of row m,
 //                                ahead of
 //   values<W, ALL>(row, fetched, n, v, u, o)  which makes its kOuts outputs of columns
@@ -165,9 +165,31 @@ __device__ __forceinline__ void wait_besides(int more) {
     }
 }
 
+// Which tile or part an XCD works on.  Workgroups are dealt to the 8 XCDs in turn (index
+// t % 8), so item t is number shared(t) of T: each XCD gets a run of neighbours, and what
+// they share comes into its L2 once.  (Measured against tiles dealt in turn, where the
+// grid does not divide into rectangles: gate and up 777 x 1000 x 2728 24.1 -> 21.4 us; parts
+// of dx 777 x 2048 x 5632 77 -> 52 us.)
+__device__ __forceinline__ int shared(int t, int T) {
+    const int x = t & 7, more = T & 7;
+    return x * (T >> 3) + min(x, more) + (t >> 3);
+}
+// Tile number `tile` of a grid: G row blocks at a time, column block by column block, so
+// that 32 neighbours share G blocks of A and 32 / G of B.  G is 8 for products stored as
+// they are and for the loss, 4 where wide rows of bf16 are written (and read): dh 8192 x
+// 1024 x 4096 130 -> 108 us with 4, gate and up 4096 x 2048 x 8192 with g and u 220 ->
+// 212, the loss's backward pass 8192 x 2048 x 32768 2486 -> 2452; dx 8192 x 1024 x 4096
+// 121 with 8, 128 with 4.
+template <int G>
+__device__ __forceinline__ void walk_tile(int tile, int nbm, int nbn, int &bm, int &bn) {
+    const int group = tile / (G * nbn), gm = min(G, nbm - group * G);
+    const int at = tile - group * G * nbn;
+    bm = group * G + at % gm;
+    bn = at / gm;
+}
+
 template <int WR, int LA, int LB, int NB, int SEG, class Epi>
-__global__ __launch_bounds__(Wide<WR>::kThreads) void wide_tiles_kernel(TileArgs p, int row_regions,
-                                                                        Epi epi) {
+__global__ __launch_bounds__(Wide<WR>::kThreads) void wide_tiles_kernel(TileArgs p, Epi epi) {
     using W = Wide<WR>;
     static_assert(NB == 1 || (LB == kRows && SEG == 1), "two weight matrices: rows, one term");
     constexpr int BM = W::kRowsOf, BN = kWideCols / NB;
@@ -195,24 +217,23 @@ __global__ __launch_bounds__(Wide<WR>::kThreads) void wide_tiles_kernel(TileArgs
     const int cchunk = (lane & 15) ^ (2 * ((crow & 3) | ((crow >> 3) & 1) << 2));
     uint32_t va[2], vb[2];  // offsets; kCols: of the two regions
     auto at_item = [&](int t) {
-        int tile = t;
+        int tile;
         part = -1;
         k0 = 0;
         kn = all;
-        if (t >= p.full) {
-            const int sp = (t - p.full) / rest;
-            part = t - p.full;
+        if (t < p.full) {
+            tile = shared(t, p.full);
+        } else {
+            part = shared(t - p.full, rest * p.splits);
+            const int sp = part / rest;
             tile = p.full + part - sp * rest;
             k0 = min(sp * per, all);
             kn = min(k0 + per, all) - k0;
         }
         z = tile / tiles;
-        tile -= z * tiles;
-        ldb = z == 2 ? p.ldb_last : p.ldb;
         int bm, bn;
-        if (row_regions == 8) xcd_tile<8>(tile, nbm, nbn, bm, bn);
-        else if (row_regions == 4) xcd_tile<4>(tile, nbm, nbn, bm, bn);
-        else xcd_tile<2>(tile, nbm, nbn, bm, bn);
+        walk_tile<Epi::kWalk>(tile - z * tiles, nbm, nbn, bm, bn);
+        ldb = z == 2 ? p.ldb_last : p.ldb;
         m0 = bm * BM;
         n0 = bn * BN;
         const int pad = (p.R + 7) & ~7;  // a row's last piece may lie in its padding
@@ -646,17 +667,16 @@ hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
     constexpr auto kernel = &wide_tiles_kernel<WR, LA, LB, NB, SEG, Epi>;
     const hipError_t e = lds_limit_once<kernel>(W::kBytes);
     if (e != hipSuccess) return e;
-    const int64_t nbm = ((int64_t)p.M + W::kRowsOf - 1) / W::kRowsOf;
-    const int64_t nbn = ((int64_t)p.N + kWideCols / NB - 1) / (kWideCols / NB);
     const int64_t items = p.full + (wide_tiles<WR, NB>(p) - p.full) * p.splits;
-    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), W::kThreads, W::kBytes, s>>>(
-        p, wide_row_regions(nbm, nbn), epi);
+    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), W::kThreads, W::kBytes, s>>>(p, epi);
     return hipGetLastError();
 }
 
 // Estimated time (us) of `items` tiles of 64 WR rows over `stages` stages each.  A stage
 // takes 1.0 to 1.6 us in the larger tiles and 0.55 to 0.95 in the smaller ones, the more
-// the more CUs draw power and load; 8 us come before the first and after the last.
+// the more CUs draw power and load; 8 us come before the first and after the last.  (A
+// third stage of loads ahead in the smaller tiles' LDS changed nothing for the better: 1 x
+// 64 stages 47 -> 55 us.)
 template <int WR>
 double tiles_us(int64_t items, int64_t stages) {
     const double least = WR == 4 ? 1.0 : 0.55, more = WR == 4 ? 0.6 : 0.4;
@@ -665,8 +685,8 @@ double tiles_us(int64_t items, int64_t stages) {
                            (rest ? least + more * rest / kWideGrid : 0.0));
 }
 
-// Measured (us, tiles of 128 and of 256 rows): gate and up 777 x 1000 x 2728 25, 29; 2048 x
-// 2048 x 5632 91, 96; 777 x 2048 x 5632 70, 50; 4096 x 1024 x 4096 71, 61.
+// Measured (us, tiles of 128 and of 256 rows): gate and up 777 x 1000 x 2728 21, 29; 2048 x
+// 2048 x 5632 82, 90; 777 x 2048 x 5632 55, 46; 4096 x 1024 x 4096 66, 57.
 template <int LA, int LB, int NB, int SEG, class Epi>
 hipError_t launch_tiles(TileArgs p, const Epi &epi, hipStream_t s) {
     const int64_t stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
@@ -684,6 +704,7 @@ hipError_t launch_tiles(TileArgs p, const Epi &epi, hipStream_t s) {
 // piece of the reduction).  A part holds its tile alone.
 struct EpiStore {
     static constexpr bool kStats = false;
+    static constexpr int kWalk = 8;
     static constexpr int kOuts = 1;
     void *out[3];
     int type;
@@ -715,7 +736,8 @@ struct EpiStore {
 };
 
 // out = the sum of the parts: each of a workgroup's 4 waves takes every fourth part of
-// the same 256 outputs, 4 at a time, so that the latencies of 16 parts are one.
+// the same 256 outputs, 4 at a time, so that the latencies of 16 parts are one (a wave
+// that took them all, 8 at a time, cost a decoded row 2.5 us more).
 template <int T>
 __global__ __launch_bounds__(256) void sum_parts_kernel(const float *__restrict__ part, int splits,
                                                         int64_t n, void *__restrict__ out) {
@@ -751,17 +773,15 @@ inline hipError_t launch_sum_parts(const float *part, int splits, int64_t n, voi
 // The same for tiles of 64 WR x 256: part s of tile full + i is number s rest + i.
 template <int WR>
 __global__ __launch_bounds__(256) void sum_tiles_kernel(const float *__restrict__ parts, int splits,
-                                                        int rest, int full, int row_regions,
-                                                        int nbm, int nbn, EpiStore epi, int M) {
+                                                        int rest, int full, int nbm, int nbn,
+                                                        EpiStore epi, int M) {
     constexpr int kSize = 64 * WR * kWideCols, kBlocks = kSize / 1024;  // workgroups a tile
     const int i = blockIdx.x / kBlocks;
     int tile = full + i;
     const int z = tile / (nbm * nbn);
     tile -= z * (nbm * nbn);
     int bm, bn;
-    if (row_regions == 8) xcd_tile<8>(tile, nbm, nbn, bm, bn);
-    else if (row_regions == 4) xcd_tile<4>(tile, nbm, nbn, bm, bn);
-    else xcd_tile<2>(tile, nbm, nbn, bm, bn);
+    walk_tile<EpiStore::kWalk>(tile, nbm, nbn, bm, bn);
     const int at = (blockIdx.x % kBlocks * 256 + threadIdx.x) * 4;
     const int m = bm * 64 * WR + at / kWideCols, n = bn * kWideCols + at % kWideCols;
     if (m >= M || n >= epi.N) return;
@@ -791,6 +811,9 @@ struct SplitPlan {
 // the chip, and for the parts of the others; the parts' way through memory, 8 bytes an
 // output and part at 4.5 TB/s, and 3 us for the kernel that adds them.  `pieces`: the
 // reduction comes in pieces, every tile keeps its parts from one to the next.
+// Measured (us, tiles of 128 and of 256 rows, each with its best split): down 777 x 1000
+// x 2728 23, 29; 4096 x 2048 x 5632 80, 93; weight gradients 4096 x 1024 x 4096 121, 95;
+// 4096 x 2048 x 5632 266, 235.
 template <int SEG>
 SplitPlan split_plan(const TileArgs &p, bool pieces) {
     const int64_t stages = SEG * (((int64_t)p.R + kWideK - 1) / kWideK);
@@ -828,14 +851,14 @@ hipError_t launch_split(TileArgs p, const SplitPlan &plan, const EpiStore &epi, 
                                           : launch_wide<2, LA, LB, 1, SEG>(p, epi, s);
     if (e != hipSuccess || !plan.bytes || !last) return e;
     const int nbm = (p.M + plan.rows - 1) / plan.rows, nbn = (p.N + kWideCols - 1) / kWideCols;
-    const int rest = nbm * nbn * p.groups - plan.full, regions = wide_row_regions(nbm, nbn);
+    const int rest = nbm * nbn * p.groups - plan.full;
     const unsigned grid = (unsigned)(plan.rows * kWideCols / 1024) * rest;
     if (plan.rows == 256)
-        sum_tiles_kernel<4><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full, regions,
-                                                 nbm, nbn, epi, p.M);
+        sum_tiles_kernel<4><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full, nbm, nbn,
+                                                 epi, p.M);
     else
-        sum_tiles_kernel<2><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full, regions,
-                                                 nbm, nbn, epi, p.M);
+        sum_tiles_kernel<2><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full, nbm, nbn,
+                                                 epi, p.M);
     return hipGetLastError();
 }
 

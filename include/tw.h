@@ -634,15 +634,15 @@ tw_status tw_linear_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *
  * Its gradient, for dloss[m] = dLoss/dloss[m] (fp32) and the forward's lse:
  *     D[m][v] = dloss[m] (exp(l[m][v] - lse[m]) - [v = t]),
  *     dx = D w,   dw = D^T x
- * (rows of D of rows that are left out are 0; their x enters dw times 0, so it
- * has to be finite).  The logits are computed again, a piece of the vocabulary
+ * (rows of D of rows that are left out, or whose dloss is 0, are 0 whatever they
+ * hold; their x enters dw times 0, so for dw it has to be finite).  The logits are computed again, a piece of the vocabulary
  * at a time, and D is rounded to bf16; sums are fp32.
  *
  *   dx      [M][K]  bf16 or fp32, or NULL;  dw [V][K] bf16 or fp32, or NULL
  *
  * Limits as in the forward.  With M = 0, dw is zeros.  ws_bytes >=
  * tw_linear_ce_bwd_workspace_bytes(M, K, V): a piece of D (at most 512 MB, or
- * 256 columns) and fp32 sums of dx.
+ * 256 columns) and fp32 parts of dx and of a piece's dw.
  */
 size_t tw_linear_ce_bwd_workspace_bytes(int M, int K, int V);
 tw_status tw_linear_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride,
