@@ -3,6 +3,8 @@
 // MFMA GEMM here, the bf16 MFMA wrapper and a DPP wavefront reduction.
 #pragma once
 
+#include <atomic>
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -89,14 +91,20 @@ __device__ __forceinline__ float wave_sum(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Raise a kernel's dynamic LDS limit once per process: the first call sets
-// the attribute and every later call returns that result (a function-local
-// static is initialised exactly once, also when several host threads launch
-// concurrently).
+// Raise a kernel's dynamic LDS limit, once for each device: the first call on it sets
+// the attribute and notes that (setting it twice, as host threads that meet in their
+// first call do, is harmless).
 template <auto Kernel>
 inline hipError_t lds_limit_once(int bytes) {
-    static const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done{0};
+    int device = 0;
+    hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+    if (done.load(std::memory_order_acquire) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
 
