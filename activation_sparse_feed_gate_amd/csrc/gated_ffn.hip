@@ -187,7 +187,8 @@ __global__ __launch_bounds__(kFewThreads) void few_hidden_kernel(
 #pragma unroll
     for (int b = 0; b < NM * C; ++b)
 #pragma unroll
-        for (int m = 0; m < MB; ++m) sums[((wave * NM * C + b) * MB + m) * kWave + lane] = acc[b][m];
+        for (int m = 0; m < MB; ++m)
+            sums[((wave * NM * C + b) * MB + m) * kWave + lane] = acc[b][m];
     __syncthreads();
     for (int i = wave; i < C * MB; i += NW) {  // block i / MB of neurons, i % MB of rows
         f32x4 s[2] = {};
@@ -252,10 +253,9 @@ template <int MB>
 constexpr int kDownWaves = MB == 4 ? 4 : 8;  // (their sums are 8 MB KB of LDS each)
 
 template <int MB>
-__global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(const uint16_t *__restrict__ h,
-                                                                const uint16_t *__restrict__ w,
-                                                                int M, int K, int N, int per,
-                                                                float *__restrict__ part) {
+__global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(
+    const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, int M, int K, int N, int per,
+    float *__restrict__ part) {
     constexpr int NW = kDownWaves<MB>;
     extern __shared__ __attribute__((aligned(16))) char smem[];  // [NW][8 MB][64] f32x4
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -330,7 +330,8 @@ __global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(const uin
         for (int q = 0; q < NW; ++q)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                s[j] += f[((((q * 8 + j) * MB + mb) * kWave) + (i >> 2) * 16 + (m & 15)) * 4 + (i & 3)];
+                s[j] += f[(((q * 8 + j) * MB + mb) * kWave + (i >> 2) * 16 + (m & 15)) * 4 +
+                          (i & 3)];
         f32x4 *out = reinterpret_cast<f32x4 *>(part + ((int64_t)blockIdx.y * M + m) * K + col);
         out[0] = f32x4{s[0], s[1], s[2], s[3]};
         out[1] = f32x4{s[4], s[5], s[6], s[7]};
@@ -358,7 +359,8 @@ hipError_t few_down_as(const uint16_t *h, const uint16_t *w, int M, int K, int N
     const hipError_t e = lds_limit_once<kernel>(lds);
     if (e != hipSuccess) return e;
     const DownSplit d = few_down_split(M, K, N);
-    kernel<<<dim3((K + 127) / 128, d.splits), 64 * kDownWaves<MB>, lds, s>>>(h, w, M, K, N, d.per, part);
+    const dim3 grid((K + 127) / 128, d.splits);
+    kernel<<<grid, 64 * kDownWaves<MB>, lds, s>>>(h, w, M, K, N, d.per, part);
     return hipGetLastError();
 }
 
@@ -366,7 +368,8 @@ hipError_t few_down(const uint16_t *h, const uint16_t *w, int M, int K, int N, f
                     hipStream_t s) {
     const int mb = few_blocks_of(M);
     if (mb == 1) return few_down_as<1>(h, w, M, K, N, part, s);
-    return mb == 2 ? few_down_as<2>(h, w, M, K, N, part, s) : few_down_as<4>(h, w, M, K, N, part, s);
+    if (mb == 2) return few_down_as<2>(h, w, M, K, N, part, s);
+    return few_down_as<4>(h, w, M, K, N, part, s);
 }
 
 template <int ACT>

@@ -1,9 +1,9 @@
-// tw_calls.cpp -- the allocating calls of the Python binding (layer and RMS
-// norm, int8 products, gated FFN, cross entropy, gradient clipping) in native
-// code: checks of the tensors, allocation of the outputs and the call of the C ABI.  A decoded token's norm runs 4 us on the GPU;
-// the same steps in interpreted Python took 20 us of host time, which then
-// set the pace of a loop of small calls (here 6 us, of which 2.6 are the launch
-// and 0.7 each of the four outputs).
+// tw_calls.cpp -- the allocating calls of the Python binding (layer and RMS norm,
+// int8 products, gated FFN, cross entropy, gradient clipping) in native code: checks
+// of the tensors, allocation of the outputs and the call of the C ABI.  A decoded
+// token's norm runs 4 us on the GPU; the same steps in interpreted Python took 20 us of
+// host time, which then set the pace of a loop of small calls (here 6 us, of which 2.6
+// are the launch and 0.7 each of the four outputs).
 //
 // Each function returns its tensor or a dict of them, or None when anything
 // about its arguments is not as the library needs it or the library refuses

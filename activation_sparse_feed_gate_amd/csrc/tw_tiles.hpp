@@ -11,7 +11,6 @@
 #pragma once
 
 #include "tw_gemm.hpp"
-#include "tw_quant_rules.hpp"
 #include "tw_rows.hpp"
 
 namespace tw {
@@ -144,7 +143,8 @@ constexpr int kWideGrid = 256;                    // workgroups: one a CU
 template <int WR>
 struct Wide {
     static constexpr int kWaves = 2 * WR, kThreads = 64 * kWaves, kRowsOf = 64 * WR;
-    static constexpr int kA = kRowsOf * kWideLine, kB = kWideCols * kWideLine;  // a stage's operands
+    // a stage's operands
+    static constexpr int kA = kRowsOf * kWideLine, kB = kWideCols * kWideLine;
     static constexpr int kSlot = kA + kB, kBytes = 2 * kSlot + kWaves * kWideOut;
     static constexpr int kPair = 8 / WR;          // loads of a wave for two column blocks
     static constexpr int kFirst = 4 + kPair;      // ... for A and two column blocks
@@ -327,8 +327,10 @@ __global__ __launch_bounds__(Wide<WR>::kThreads) void wide_tiles_kernel(TileArgs
             dma16(l.d[0], l.v[0] + g * ((uint32_t)(16 * WR) * (uint32_t)p.lda * 2), l.soff,
                   l.slot + (16 * WR * g + 8 * wave) * kWideLine);
         else
-            dma16(l.d[0], l.v[g / W::kPair] + g % W::kPair * ((uint32_t)(8 * WR) * (uint32_t)p.lda * 2),
-                  0, l.slot + g / W::kPair * kWideRegion + (8 * WR * (g % W::kPair) + 4 * wave) * 256);
+            dma16(l.d[0],
+                  l.v[g / W::kPair] + g % W::kPair * ((uint32_t)(8 * WR) * (uint32_t)p.lda * 2), 0,
+                  l.slot + g / W::kPair * kWideRegion +
+                      (8 * WR * (g % W::kPair) + 4 * wave) * 256);
     };
     auto put_b = [&](const Loads &l, int q, int g) {
         if constexpr (LB == kRows) {
@@ -369,7 +371,8 @@ __global__ __launch_bounds__(Wide<WR>::kThreads) void wide_tiles_kernel(TileArgs
         i16x4 v[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            v[h] = lds_tr16((const lds_i16x4 *)(region + fo + ((c ^ fx) << 4) + (32 * s + 4 * h) * 256));
+            v[h] = lds_tr16(
+                (const lds_i16x4 *)(region + fo + ((c ^ fx) << 4) + (32 * s + 4 * h) * 256));
         const u32x2 lo = __builtin_bit_cast(u32x2, v[0]);
         const u32x2 hi = __builtin_bit_cast(u32x2, v[1]);
         return u32x4{lo[0], lo[1], hi[0], hi[1]};
@@ -385,7 +388,8 @@ __global__ __launch_bounds__(Wide<WR>::kThreads) void wide_tiles_kernel(TileArgs
         if constexpr (LB == kRows)
             fb[j & 1][s][h] = read_rows(
                 part,
-                (NB == 1 ? wn * 128 + j * 32 : (j >> 1) * 128 + wn * 64 + (j & 1) * 32) + 16 * h, s);
+                (NB == 1 ? wn * 128 + j * 32 : (j >> 1) * 128 + wn * 64 + (j & 1) * 32) + 16 * h,
+                s);
         else
             fb[j & 1][s][h] =
                 read_cols(part + (j >> 1) * kWideRegion, wn * 8 + (j & 1) * 4 + 2 * h, s);
@@ -668,7 +672,8 @@ hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
     const hipError_t e = lds_limit_once<kernel>(W::kBytes);
     if (e != hipSuccess) return e;
     const int64_t items = p.full + (wide_tiles<WR, NB>(p) - p.full) * p.splits;
-    kernel<<<(unsigned)(items < kWideGrid ? items : kWideGrid), W::kThreads, W::kBytes, s>>>(p, epi);
+    const unsigned grid = (unsigned)(items < kWideGrid ? items : kWideGrid);
+    kernel<<<grid, W::kThreads, W::kBytes, s>>>(p, epi);
     return hipGetLastError();
 }
 
@@ -828,7 +833,8 @@ SplitPlan split_plan(const TileArgs &p, bool pieces) {
             const bool parts = pieces || s > 1;
             const int64_t full = !parts ? tiles : pieces ? 0 : tiles / kWideGrid * kWideGrid;
             const int64_t rest = tiles - full;
-            double us = tiles_us<WR>(full, stages) + (rest ? tiles_us<WR>(rest * s, per) : 8.0) - 8.0;
+            double us = tiles_us<WR>(full, stages) - 8.0;
+            us += rest ? tiles_us<WR>(rest * s, per) : 8.0;
             if (parts) us += 3.0 + (double)rest * s * size * 8 / 4.5e6;
             if (us >= least) continue;
             least = us;
