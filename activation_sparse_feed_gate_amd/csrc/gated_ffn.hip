@@ -241,12 +241,13 @@ hipError_t few_hidden(const uint16_t *x, int64_t x_stride, const uint16_t *w0, c
 
 // ------------------ rows times a matrix of reduction rows --------------------
 // part[split][m][k] = sum over n of the split of h[m][n] w[n][k], for up to 64 token
-// rows.  A wave reads 32 rows of w, 128 columns wide, 16 bytes a lane: lane l has the 8
+// rows; with a second pair of h and w (dx) its splits behind the first one's.  A wave reads 32 rows of w, 128 columns wide, 16 bytes a lane: lane l has the 8
 // rows from 8 (l / 16) on of the 8 columns from 8 (l % 16) on.  A matrix instruction
 // wants one column's 8 rows in a lane, so pairs of rows are interleaved (one permute a
 // register) and instruction j of 8 takes every lane's column j.  Bound by the stream of w
 // (2048 x 5632, with the sum of the parts: 10.7 us for one row, 11.1 for 16, 16.8 for
-// 64; in tiles 17, 18 and 20.  Products on the vector units took 32 us for 16).
+// 64; in tiles 17, 18 and 20; dx 14, 15, 21 and 20, 21, 23.  Products on the vector
+// units took 32 us for 16).
 constexpr int kFewDownMax = 64;  // token rows
 constexpr int kDownGrid = 256;   // (512: 64 rows 22 us)
 template <int MB>
@@ -254,8 +255,10 @@ constexpr int kDownWaves = MB == 4 ? 4 : 8;  // (their sums are 8 MB KB of LDS e
 
 template <int MB>
 __global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(
-    const uint16_t *__restrict__ h, const uint16_t *__restrict__ w, int M, int K, int N, int per,
+    const uint16_t *__restrict__ h0, const uint16_t *__restrict__ w0,
+    const uint16_t *__restrict__ h1, const uint16_t *__restrict__ w1, int M, int K, int N, int per,
     float *__restrict__ part) {
+    const uint16_t *const h = blockIdx.z ? h1 : h0, *const w = blockIdx.z ? w1 : w0;
     constexpr int NW = kDownWaves<MB>;
     extern __shared__ __attribute__((aligned(16))) char smem[];  // [NW][8 MB][64] f32x4
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -332,7 +335,8 @@ __global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(
             for (int j = 0; j < 8; ++j)
                 s[j] += f[(((q * 8 + j) * MB + mb) * kWave + (i >> 2) * 16 + (m & 15)) * 4 +
                           (i & 3)];
-        f32x4 *out = reinterpret_cast<f32x4 *>(part + ((int64_t)blockIdx.y * M + m) * K + col);
+        const int64_t split = blockIdx.z * gridDim.y + blockIdx.y;
+        f32x4 *out = reinterpret_cast<f32x4 *>(part + (split * M + m) * K + col);
         out[0] = f32x4{s[0], s[1], s[2], s[3]};
         out[1] = f32x4{s[4], s[5], s[6], s[7]};
     }
@@ -343,33 +347,36 @@ __global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(
 struct DownSplit {
     int splits, per;
 };
-DownSplit few_down_split(int M, int K, int N) {
+DownSplit few_down_split(int pairs, int M, int K, int N) {
     const int rows = 32 * (M <= 32 ? kDownWaves<1> : kDownWaves<4>);
     const int cols = (K + 127) / 128, rounds = (N + rows - 1) / rows;
-    const int most = kDownGrid / cols > 1 ? kDownGrid / cols : 1;
+    const int most = kDownGrid / (pairs * cols) > 1 ? kDownGrid / (pairs * cols) : 1;
     const int each = (rounds + most - 1) / most;
     return {(rounds + each - 1) / each, rows * each};
 }
 
 template <int MB>
-hipError_t few_down_as(const uint16_t *h, const uint16_t *w, int M, int K, int N, float *part,
-                       hipStream_t s) {
+hipError_t few_down_as(const uint16_t *const (&h)[2], const uint16_t *const (&w)[2], int pairs,
+                       int M, int K, int N, float *part, hipStream_t s) {
     constexpr auto kernel = &few_down_kernel<MB>;
     constexpr int lds = kDownWaves<MB> * 8 * MB * kWave * 16;
     const hipError_t e = lds_limit_once<kernel>(lds);
     if (e != hipSuccess) return e;
-    const DownSplit d = few_down_split(M, K, N);
-    const dim3 grid((K + 127) / 128, d.splits);
-    kernel<<<grid, 64 * kDownWaves<MB>, lds, s>>>(h, w, M, K, N, d.per, part);
+    const DownSplit d = few_down_split(pairs, M, K, N);
+    const dim3 grid((K + 127) / 128, d.splits, pairs);
+    kernel<<<grid, 64 * kDownWaves<MB>, lds, s>>>(h[0], w[0], h[1], w[1], M, K, N, d.per, part);
     return hipGetLastError();
 }
 
-hipError_t few_down(const uint16_t *h, const uint16_t *w, int M, int K, int N, float *part,
-                    hipStream_t s) {
+hipError_t few_down(const uint16_t *const (&h)[2], const uint16_t *const (&w)[2], int pairs, int M,
+                    int K, int N, float *part, void *out, int type, hipStream_t s) {
     const int mb = few_blocks_of(M);
-    if (mb == 1) return few_down_as<1>(h, w, M, K, N, part, s);
-    if (mb == 2) return few_down_as<2>(h, w, M, K, N, part, s);
-    return few_down_as<4>(h, w, M, K, N, part, s);
+    const hipError_t e = mb == 1   ? few_down_as<1>(h, w, pairs, M, K, N, part, s)
+                         : mb == 2 ? few_down_as<2>(h, w, pairs, M, K, N, part, s)
+                                   : few_down_as<4>(h, w, pairs, M, K, N, part, s);
+    if (e != hipSuccess) return e;
+    return launch_sum_parts(part, pairs * few_down_split(pairs, M, K, N).splits, (int64_t)M * K, out,
+                            type, s);
 }
 
 template <int ACT>
@@ -402,11 +409,13 @@ static SplitPlan dw_plan(int M, int K, int N) {
 }
 
 size_t ffn_fwd_part_bytes(int M, int K, int N) {
-    if (M <= kFewDownMax) return (size_t)few_down_split(M, K, N).splits * M * K * 4;
+    if (M <= kFewDownMax) return (size_t)few_down_split(1, M, K, N).splits * M * K * 4;
     return down_plan(M, K, N).bytes;
 }
 size_t ffn_bwd_part_bytes(int M, int K, int N) {
-    const size_t a = dx_plan(M, K, N).bytes, b = dw_plan(M, K, N).bytes;
+    const size_t a = M <= kFewDownMax ? (size_t)2 * few_down_split(2, M, K, N).splits * M * K * 4
+                                      : dx_plan(M, K, N).bytes;
+    const size_t b = dw_plan(M, K, N).bytes;
     return a > b ? a : b;
 }
 
@@ -422,9 +431,7 @@ hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg
 hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, int N, void *y,
                            int y_type, float *part, hipStream_t s) {
     if (M <= kFewDownMax) {
-        const hipError_t e = few_down(h, wd, M, K, N, part, s);
-        if (e != hipSuccess) return e;
-        return launch_sum_parts(part, few_down_split(M, K, N).splits, (int64_t)M * K, y, y_type, s);
+        return few_down({h, nullptr}, {wd, nullptr}, 1, M, K, N, part, y, y_type, s);
     }
     return launch_split<kRows, kCols, 1>(TileArgs{{h}, {wd}, N, K, M, K, N},
                                             down_plan(M, K, N), EpiStore{{y}, y_type, K, part},
@@ -443,6 +450,8 @@ hipError_t launch_ffn_dh(const uint16_t *dy, const uint16_t *wd, int act, const 
 hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t *wg_t,
                          const uint16_t *wu_t, int M, int K, int N, void *dx, int dx_type,
                          float *part, hipStream_t s) {
+    if (M <= kFewDownMax)
+        return few_down({dz, du}, {wg_t, wu_t}, 2, M, K, N, part, dx, dx_type, s);
     return launch_split<kRows, kCols, 2>(TileArgs{{dz, du}, {wg_t, wu_t}, N, K, M, K, N},
                                             dx_plan(M, K, N), EpiStore{{dx}, dx_type, K, part},
                                             true, s);
