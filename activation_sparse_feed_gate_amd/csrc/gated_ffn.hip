@@ -239,146 +239,6 @@ hipError_t few_hidden(const uint16_t *x, int64_t x_stride, const uint16_t *w0, c
     return mb == 1 ? go(two, one) : mb == 2 ? go(two, two) : go(two, four);
 }
 
-// ------------------ rows times a matrix of reduction rows --------------------
-// part[split][m][k] = sum over n of the split of h[m][n] w[n][k], for up to 64 token
-// rows; with a second pair of h and w (dx) its splits behind the first one's.  A wave reads 32 rows of w, 128 columns wide, 16 bytes a lane: lane l has the 8
-// rows from 8 (l / 16) on of the 8 columns from 8 (l % 16) on.  A matrix instruction
-// wants one column's 8 rows in a lane, so pairs of rows are interleaved (one permute a
-// register) and instruction j of 8 takes every lane's column j.  Bound by the stream of w
-// (2048 x 5632, with the sum of the parts: 10.7 us for one row, 11.1 for 16, 16.8 for
-// 64; in tiles 17, 18 and 20; dx 14, 15, 21 and 20, 21, 23.  Products on the vector
-// units took 32 us for 16).
-constexpr int kFewDownMax = 64;  // token rows
-constexpr int kDownGrid = 256;   // (512: 64 rows 22 us)
-template <int MB>
-constexpr int kDownWaves = MB == 4 ? 4 : 8;  // (their sums are 8 MB KB of LDS each)
-
-template <int MB>
-__global__ __launch_bounds__(64 * kDownWaves<MB>) void few_down_kernel(
-    const uint16_t *__restrict__ h0, const uint16_t *__restrict__ w0,
-    const uint16_t *__restrict__ h1, const uint16_t *__restrict__ w1, int M, int K, int N, int per,
-    float *__restrict__ part) {
-    const uint16_t *const h = blockIdx.z ? h1 : h0, *const w = blockIdx.z ? w1 : w0;
-    constexpr int NW = kDownWaves<MB>;
-    extern __shared__ __attribute__((aligned(16))) char smem[];  // [NW][8 MB][64] f32x4
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int l16 = lane & 15, r8 = 8 * (lane >> 4);
-    const int at = min(blockIdx.x * 128 + 8 * l16, K - 8);  // (past K: the last columns again)
-    const int n0 = blockIdx.y * per, n1 = min(n0 + per, N);
-    const uint16_t *hp[MB];
-#pragma unroll
-    for (int m = 0; m < MB; ++m) hp[m] = h + (int64_t)min(16 * m + l16, M - 1) * N;
-    struct Step {
-        u32x4 w[8], h[MB];
-    };
-    // rows past the split (n1 is a multiple of 8): the first ones again, used as zeros
-    auto load = [&](Step &s, int n) {
-        const int row = n + r8 < n1 ? n + r8 : n0;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) s.h[m] = ld16(hp[m] + row);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) s.w[r] = ld16(w + (int64_t)(row + r) * K + at);
-    };
-    f32x4 acc[8][MB] = {};
-    auto multiply = [&](Step &s, int n) {
-        if (n + r8 >= n1) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) s.w[r] = u32x4{};
-#pragma unroll
-            for (int m = 0; m < MB; ++m) s.h[m] = u32x4{};
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            u32x4 v;
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                v[p] = __builtin_amdgcn_perm(s.w[2 * p + 1][j >> 1], s.w[2 * p][j >> 1],
-                                             j & 1 ? 0x07060302u : 0x05040100u);
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-                acc[j][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, s.h[m]), acc[j][m],
-                    0, 0, 0);
-        }
-    };
-    constexpr int kStep = 32 * NW;
-    int n = n0 + 32 * wave;
-    if (n < n1) {
-        Step a, b;
-        load(a, n);
-        for (;; n += 2 * kStep) {
-            if (n + kStep < n1) load(b, n + kStep);
-            multiply(a, n);
-            if (n + kStep >= n1) break;
-            if (n + 2 * kStep < n1) load(a, n + 2 * kStep);
-            multiply(b, n + kStep);
-            if (n + 2 * kStep >= n1) break;
-        }
-    }
-    // The waves' sums meet in LDS.  Lane l of acc[j][m] holds token l % 16, columns 8 (4
-    // (l / 16) + e) + j; a thread then adds the 8 columns of one token.
-    f32x4 *sums = reinterpret_cast<f32x4 *>(smem);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int m = 0; m < MB; ++m) sums[((wave * 8 + j) * MB + m) * kWave + lane] = acc[j][m];
-    __syncthreads();
-    const float *f = reinterpret_cast<const float *>(smem);
-    for (int t = threadIdx.x; t < 256 * MB; t += 64 * NW) {
-        const int mb = t >> 8, m = 16 * mb + (t & 15), i = t >> 4 & 15;
-        const int col = blockIdx.x * 128 + 8 * i;
-        if (m >= M || col >= K) continue;
-        float s[8] = {};
-#pragma unroll
-        for (int q = 0; q < NW; ++q)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s[j] += f[(((q * 8 + j) * MB + mb) * kWave + (i >> 2) * 16 + (m & 15)) * 4 +
-                          (i & 3)];
-        const int64_t split = blockIdx.z * gridDim.y + blockIdx.y;
-        f32x4 *out = reinterpret_cast<f32x4 *>(part + (split * M + m) * K + col);
-        out[0] = f32x4{s[0], s[1], s[2], s[3]};
-        out[1] = f32x4{s[4], s[5], s[6], s[7]};
-    }
-}
-
-// Parts of N: about kDownGrid workgroups, each with as many steps of 32 rows for every
-// one of its waves.
-struct DownSplit {
-    int splits, per;
-};
-DownSplit few_down_split(int pairs, int M, int K, int N) {
-    const int rows = 32 * (M <= 32 ? kDownWaves<1> : kDownWaves<4>);
-    const int cols = (K + 127) / 128, rounds = (N + rows - 1) / rows;
-    const int most = kDownGrid / (pairs * cols) > 1 ? kDownGrid / (pairs * cols) : 1;
-    const int each = (rounds + most - 1) / most;
-    return {(rounds + each - 1) / each, rows * each};
-}
-
-template <int MB>
-hipError_t few_down_as(const uint16_t *const (&h)[2], const uint16_t *const (&w)[2], int pairs,
-                       int M, int K, int N, float *part, hipStream_t s) {
-    constexpr auto kernel = &few_down_kernel<MB>;
-    constexpr int lds = kDownWaves<MB> * 8 * MB * kWave * 16;
-    const hipError_t e = lds_limit_once<kernel>(lds);
-    if (e != hipSuccess) return e;
-    const DownSplit d = few_down_split(pairs, M, K, N);
-    const dim3 grid((K + 127) / 128, d.splits, pairs);
-    kernel<<<grid, 64 * kDownWaves<MB>, lds, s>>>(h[0], w[0], h[1], w[1], M, K, N, d.per, part);
-    return hipGetLastError();
-}
-
-hipError_t few_down(const uint16_t *const (&h)[2], const uint16_t *const (&w)[2], int pairs, int M,
-                    int K, int N, float *part, void *out, int type, hipStream_t s) {
-    const int mb = few_blocks_of(M);
-    const hipError_t e = mb == 1   ? few_down_as<1>(h, w, pairs, M, K, N, part, s)
-                         : mb == 2 ? few_down_as<2>(h, w, pairs, M, K, N, part, s)
-                                   : few_down_as<4>(h, w, pairs, M, K, N, part, s);
-    if (e != hipSuccess) return e;
-    return launch_sum_parts(part, pairs * few_down_split(pairs, M, K, N).splits, (int64_t)M * K, out,
-                            type, s);
-}
-
 template <int ACT>
 hipError_t ffn_up(const TileArgs &p, uint16_t *g, uint16_t *u, uint16_t *h, hipStream_t s) {
     if (p.M <= kFewRowsMax)
@@ -431,7 +291,7 @@ hipError_t launch_ffn_up(const uint16_t *x, int64_t x_stride, const uint16_t *wg
 hipError_t launch_ffn_down(const uint16_t *h, const uint16_t *wd, int M, int K, int N, void *y,
                            int y_type, float *part, hipStream_t s) {
     if (M <= kFewDownMax) {
-        return few_down({h, nullptr}, {wd, nullptr}, 1, M, K, N, part, y, y_type, s);
+        return few_down({h, nullptr}, {wd, nullptr}, 1, N, M, K, N, part, y, y_type, s);
     }
     return launch_split<kRows, kCols, 1>(TileArgs{{h}, {wd}, N, K, M, K, N},
                                             down_plan(M, K, N), EpiStore{{y}, y_type, K, part},
@@ -451,7 +311,7 @@ hipError_t launch_ffn_dx(const uint16_t *dz, const uint16_t *du, const uint16_t 
                          const uint16_t *wu_t, int M, int K, int N, void *dx, int dx_type,
                          float *part, hipStream_t s) {
     if (M <= kFewDownMax)
-        return few_down({dz, du}, {wg_t, wu_t}, 2, M, K, N, part, dx, dx_type, s);
+        return few_down({dz, du}, {wg_t, wu_t}, 2, N, M, K, N, part, dx, dx_type, s);
     return launch_split<kRows, kCols, 2>(TileArgs{{dz, du}, {wg_t, wu_t}, N, K, M, K, N},
                                             dx_plan(M, K, N), EpiStore{{dx}, dx_type, K, part},
                                             true, s);

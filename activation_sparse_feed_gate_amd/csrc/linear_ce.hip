@@ -271,8 +271,9 @@ constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // dx's sums in parts that every piece adds to, a piece's dw.
 struct Pieces {
     int width;
+    bool few;  // dx in one piece by the kernel of few rows
     SplitPlan dx;
-    size_t d_bytes, part_bytes;
+    size_t d_bytes, dx_bytes, part_bytes;
 };
 SplitPlan dw_plan(int M, int K, int width) {
     return split_plan<1>(TileArgs{{}, {}, 0, 0, width, K, M}, false);
@@ -286,7 +287,11 @@ Pieces pieces_of(int M, int K, int V) {
     // the weight gradient's parts behind them, since dx's stay
     size_t dw = dw_plan(M, K, p.width).bytes;
     if (V % p.width) dw = std::max(dw, dw_plan(M, K, V % p.width).bytes);
-    p.part_bytes = up256(p.dx.bytes) + up256(dw);
+    // Measured (us of D and dx; few rows' kernel, tiles): 1 row 1024 x 32768 33, 40; 64 rows
+    // 45, 46; 4 rows 2048 x 49999 69, 72.
+    p.few = M <= kFewDownMax && p.width == V;
+    p.dx_bytes = up256(p.few ? (size_t)few_down_split(1, M, K, V).splits * M * K * 4 : p.dx.bytes);
+    p.part_bytes = p.dx_bytes + up256(dw);
     return p;
 }
 
@@ -333,7 +338,7 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
     const Pieces pc = pieces_of(M, K, V);
     uint16_t *d = static_cast<uint16_t *>(ws);
     float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + pc.d_bytes);
-    float *dw_parts = parts + up256(pc.dx.bytes) / 4;
+    float *dw_parts = parts + pc.dx_bytes / 4;
     hipError_t e = hipSuccess;
     for (int first = 0; first < V && e == hipSuccess; first += pc.width) {
         const int N = V - first < pc.width ? V - first : pc.width;
@@ -342,7 +347,9 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
         if (M > 0)
             e = launch_tiles<kRows, kRows, 1, 1>(TileArgs{{x}, {wp}, x_stride, K, M, N, K},
                                                  EpiD{lse, dloss, t, d, ldd, N, first, V}, s);
-        if (e == hipSuccess && dx && M > 0)
+        if (e == hipSuccess && dx && M > 0 && pc.few)
+            e = few_down({d, nullptr}, {wp, nullptr}, 1, ldd, M, K, N, parts, dx, dx_type, s);
+        else if (e == hipSuccess && dx && M > 0)
             e = launch_split<kRows, kCols, 1>(
                 TileArgs{{d}, {wp}, ldd, K, M, K, N}, pc.dx,
                 EpiStore{{dx}, dx_type, K, parts, first > 0}, first + N == V, s);
