@@ -1,10 +1,11 @@
 // tw_few.hpp -- products of few token rows (up to 64) with a weight matrix that is
 // streamed once from memory: the rows of a decoded batch.
 //
-// Weight fragments come straight from memory into registers (no other wave reads
-// them), the tokens' from the L2, and 16 weight rows meet 16 token rows in one
-// matrix instruction of 32 reduction elements; token rows past the last
-// repeat it.  What bounds these products is the stream of weights, so a wave keeps
+// few_product takes weight rows of reduction elements, few_down_kernel weight rows that
+// are the reduction's own.  Weight fragments come straight from memory into registers
+// (no other wave reads them), the tokens' from the L2, and 16 weight rows or columns
+// meet 16 token rows in one matrix instruction of 32 reduction elements; token rows past
+// the last repeat it.  What bounds these products is the stream of weights, so a wave keeps
 // two batches of loads: one in flight while the other is multiplied.
 #pragma once
 
