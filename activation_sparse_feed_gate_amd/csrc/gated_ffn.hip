@@ -38,11 +38,16 @@ __device__ __forceinline__ float logistic(float a) {
 constexpr float kGelu = 1.59576912160573071176f;  // 2 sqrt(2 / pi)
 constexpr float kGelu3 = 0.044715f;
 
+// g s(a) with s = s(a(g)): below -128, where s is 0 for every activation here, g is
+// taken at -128, so that minus infinity gives the limit and not infinity times 0.  (s of a
+// NaN is NaN.)
+__device__ __forceinline__ float gated(float g, float s) { return fmaxf(g, -128.0f) * s; }
+
 template <int ACT>
 __device__ __forceinline__ float activate(float g) {
     if constexpr (ACT == TW_A_RELU) return g <= 0.0f ? 0.0f : g;  // NaN stays NaN
-    else if constexpr (ACT == TW_A_SILU) return g * logistic(g);
-    else return g * logistic(kGelu * g * (1.0f + kGelu3 * g * g));
+    else if constexpr (ACT == TW_A_SILU) return gated(g, logistic(g));
+    else return gated(g, logistic(kGelu * g * (1.0f + kGelu3 * g * g)));
 }
 
 struct Slope {
@@ -51,13 +56,15 @@ struct Slope {
 template <int ACT>
 __device__ __forceinline__ Slope activate_slope(float g) {
     if constexpr (ACT == TW_A_RELU) return {g <= 0.0f ? 0.0f : g, g <= 0.0f ? 0.0f : 1.0f};
-    // s (1 + g a' (1 - s)).  GELU's g a' grows as g^3, but s is 0 or 1 long before |g| =
-    // 16, so it is taken there: 0 times an infinity would be NaN.
+    // s (1 + g a' (1 - s)), with g a' taken at a bound past which s is 0 or 1 - s is: 0
+    // times an infinity would be NaN.  For SiLU that holds from |g| = 128 on; GELU's g a'
+    // grows as g^3, but its s is 0 or 1 long before |g| = 16.
     const bool silu = ACT == TW_A_SILU;
+    const float most = silu ? 128.0f : 16.0f;
     const float s = logistic(silu ? g : kGelu * g * (1.0f + kGelu3 * g * g));
-    const float c = fminf(fmaxf(g, -16.0f), 16.0f);
-    const float d = silu ? g : kGelu * c * (1.0f + 3.0f * kGelu3 * c * c);
-    return {g * s, s * fmaf(d, 1.0f - s, 1.0f)};
+    const float c = fminf(fmaxf(g, -most), most);
+    const float d = silu ? c : kGelu * c * (1.0f + 3.0f * kGelu3 * c * c);
+    return {gated(g, s), s * fmaf(d, 1.0f - s, 1.0f)};
 }
 
 // Gate and up projections -> h (and g, u).
