@@ -106,7 +106,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(Table t, const float
     } else {
         all = *norm;
     }
-    const float c = max_norm / (all + eps);
+    // (a max_norm of 0 makes zeros, also of gradients whose norm is 0: 0 / 0 there)
+    const float c = max_norm > 0.0f || all != all ? max_norm / (all + eps) : 0.0f;
     const float by = c >= 1.0f ? 1.0f : c;  // a norm of NaN makes every gradient NaN
     walk(t, [&](auto type, const char *g, int n, int i, int64_t at) {
         constexpr int T = decltype(type)::value;

@@ -659,8 +659,9 @@ tw_status tw_linear_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stri
  * call.  A buffer's type is TW_BF16 or TW_F32; its address is aligned to its
  * type and may be NULL where n is 0.  out[i] may be g[i] itself (of the same
  * type); otherwise no output may overlap another buffer of the call, which is
- * checked.  A norm that is NaN makes every output NaN.  n[i] at most 2^34;
- * count at most 2^20.  ws_bytes >= tw_grad_norm_workspace_bytes(count, n).
+ * checked.  A norm that is NaN makes every output NaN; with max_norm 0 the
+ * factor is otherwise 0, whatever the norm.  n[i] at most 2^34; count at most
+ * 2^20.  ws_bytes >= tw_grad_norm_workspace_bytes(count, n).
  * Squares are summed in fp32, in a fixed order (bit-identical run to run).
  * norm: one fp32, aligned to 4.  events of tw_grad_norm: [0] before, [1] after;
  * of tw_grad_clip: [0] before, [1] after the squares' sums, [2] after.
