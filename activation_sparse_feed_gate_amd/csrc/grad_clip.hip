@@ -127,8 +127,9 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(Table t, const float
     });
 }
 
-// Runs f(table) over the buffers, kTableMax of those with elements at a time
-// (of at most 2^34 elements each: their chunks stay within 32 bits).
+// Runs f(table) over the buffers, kTableMax of those with elements at a time (their
+// chunks stay within 32 bits).
+static_assert(kTableMax * (kClipMost / kChunk + 1) < (int64_t(1) << 31), "");
 template <typename F>
 hipError_t over_tables(int count, const void *const *g, const int64_t *n, const int *g_type,
                        void *const *out, const int *out_type, F f) {

@@ -1029,7 +1029,7 @@ tw_status check_buffers(int count, const void *const *g, const int64_t *n, const
         if (!float_type(types[i]))
             return fail(TW_EINVAL, "%s[%d]: type %d, TW_BF16 or TW_F32", what, i, types[i]);
         if (n[i] < 0) return fail(TW_EINVAL, "n[%d]=%lld: need n >= 0", i, (long long)n[i]);
-        if (n[i] > (int64_t(1) << 34))
+        if (n[i] > tw::kClipMost)
             return fail(TW_EUNSUPPORTED, "n[%d]=%lld: at most 2^34", i, (long long)n[i]);
         if (n[i] == 0) continue;
         if (!g[i]) return fail(TW_EINVAL, "%s[%d] is NULL", what, i);
@@ -1295,6 +1295,7 @@ tw_status tw_linear_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stri
 
 size_t tw_grad_norm_workspace_bytes(int count, const int64_t *n) {
     if (count < 0 || count > kMostBuffers || (count && !n)) return 0;
+    if (std::any_of(n, n + count, [](int64_t k) { return k > tw::kClipMost; })) return 0;
     return tw::grad_norm_bytes(count, n);
 }
 

@@ -64,8 +64,9 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
                          const uint16_t *w, Targets t, const float *lse, int M, int K, int V,
                          void *dx, int dx_type, void *dw, int dw_type, void *ws, hipStream_t s);
 
-// Gradient clipping (grad_clip.hip) over `count` buffers of n[i] elements;
-// part: grad_norm_bytes.
+// Gradient clipping (grad_clip.hip) over `count` buffers of n[i] elements each, at
+// most kClipMost; part: grad_norm_bytes.
+constexpr int64_t kClipMost = int64_t(1) << 34;
 size_t grad_norm_bytes(int count, const int64_t *n);
 hipError_t launch_grad_norm(int count, const void *const *g, const int64_t *n, const int *g_type,
                             float *norm, float *part, hipStream_t s);

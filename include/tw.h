@@ -661,7 +661,9 @@ tw_status tw_linear_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stri
  * type); otherwise no output may overlap another buffer of the call, which is
  * checked.  A norm that is NaN makes every output NaN; with max_norm 0 the
  * factor is otherwise 0, whatever the norm.  n[i] at most 2^34; count at most
- * 2^20.  ws_bytes >= tw_grad_norm_workspace_bytes(count, n).
+ * 2^20.  ws_bytes >= tw_grad_norm_workspace_bytes(count, n), which is 0 where
+ * one of these is exceeded (a negative n[i], which the calls reject, counts as
+ * no elements there).
  * Squares are summed in fp32, in a fixed order (bit-identical run to run).
  * norm: one fp32, aligned to 4.  events of tw_grad_norm: [0] before, [1] after;
  * of tw_grad_clip: [0] before, [1] after the squares' sums, [2] after.
