@@ -1039,6 +1039,26 @@ tw_status check_buffers(int count, const void *const *g, const int64_t *n, const
     return TW_OK;
 }
 
+size_t buffer_bytes(int type, int64_t n) { return (size_t)n * (type == TW_F32 ? 4 : 2); }
+bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p < q + b_bytes && q < p + a_bytes;
+}
+// The norm and the bytes of the workspace that the call writes are written while
+// buffers are read, or read while they are written.
+tw_status check_apart(int count, const void *const *p, const int64_t *n, const int *types,
+                      const char *what, const float *norm, const void *ws, size_t ws_bytes) {
+    for (int i = 0; i < count; ++i) {
+        const size_t bytes = buffer_bytes(types[i], n[i]);
+        if (!bytes) continue;
+        if (overlap(p[i], bytes, norm, 4))
+            return fail(TW_EINVAL, "%s[%d] and norm overlap", what, i);
+        if (overlap(p[i], bytes, ws, ws_bytes))
+            return fail(TW_EINVAL, "%s[%d] and the workspace overlap", what, i);
+    }
+    return TW_OK;
+}
+
 tw_status check_grad_norm(int count, const void *const *g, const int64_t *n, const int *g_type,
                           const float *norm, const void *ws, size_t ws_bytes) {
     if (count < 0) return fail(TW_EINVAL, "count=%d: need count >= 0", count);
@@ -1047,7 +1067,10 @@ tw_status check_grad_norm(int count, const void *const *g, const int64_t *n, con
     TW_TRY(check_buffers(count, g, n, g_type, "g"));
     if (!norm) return fail(TW_EINVAL, "norm is NULL");
     if (reinterpret_cast<uintptr_t>(norm) % 4) return fail(TW_EINVAL, "norm is not aligned to 4");
-    return check_ws(ws, ws_bytes, tw_grad_norm_workspace_bytes(count, n));
+    const size_t need = tw_grad_norm_workspace_bytes(count, n);
+    TW_TRY(check_ws(ws, ws_bytes, need));
+    if (overlap(norm, 4, ws, need)) return fail(TW_EINVAL, "norm and the workspace overlap");
+    return check_apart(count, g, n, g_type, "g", norm, ws, need);
 }
 
 // No output may overlap another output, or a gradient other than its own in
@@ -1060,11 +1083,10 @@ tw_status check_overlaps(int count, const void *const *g, const int64_t *n, cons
     };
     std::vector<Span> spans;
     spans.reserve(count);
-    auto bytes = [](int type, int64_t k) { return (uintptr_t)k * (type == TW_F32 ? 4 : 2); };
     for (int i = 0; i < count; ++i) {
         if (!n[i]) continue;
         const uintptr_t at = reinterpret_cast<uintptr_t>(out[i]);
-        spans.push_back({at, at + bytes(out_type[i], n[i]), i});
+        spans.push_back({at, at + buffer_bytes(out_type[i], n[i]), i});
     }
     std::sort(spans.begin(), spans.end(),
               [](const Span &a, const Span &b) { return a.begin < b.begin; });
@@ -1074,7 +1096,7 @@ tw_status check_overlaps(int count, const void *const *g, const int64_t *n, cons
     for (int i = 0; i < count; ++i) {
         if (!n[i]) continue;
         const uintptr_t at = reinterpret_cast<uintptr_t>(g[i]);
-        const uintptr_t end = at + bytes(g_type[i], n[i]);
+        const uintptr_t end = at + buffer_bytes(g_type[i], n[i]);
         // the first output that ends after g[i] begins (they are disjoint, so
         // their ends ascend too)
         auto k = std::upper_bound(spans.begin(), spans.end(), at,
@@ -1317,6 +1339,8 @@ tw_status tw_grad_clip(int count, const void *const *g, const int64_t *n, const 
     if (!(eps >= 0.0f)) return fail(TW_EINVAL, "eps=%g: need eps >= 0", (double)eps);
     if (count && (!out || !out_type)) return fail(TW_EINVAL, "out or out_type is NULL");
     TW_TRY(check_buffers(count, out, n, out_type, "out"));
+    TW_TRY(check_apart(count, out, n, out_type, "out", norm, ws,
+                       tw_grad_norm_workspace_bytes(count, n)));
     try {
         TW_TRY(check_overlaps(count, g, n, g_type, out, out_type));
     } catch (const std::bad_alloc &) {

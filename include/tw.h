@@ -658,7 +658,8 @@ tw_status tw_linear_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stri
  * The arrays g, n, g_type, out and out_type are read on the host during the
  * call.  A buffer's type is TW_BF16 or TW_F32; its address is aligned to its
  * type and may be NULL where n is 0.  out[i] may be g[i] itself (of the same
- * type); otherwise no output may overlap another buffer of the call, which is
+ * type); otherwise no output may overlap another buffer of the call, and no
+ * buffer the norm or what is needed of the workspace, nor these each other: all
  * checked.  A norm that is NaN makes every output NaN; with max_norm 0 the
  * factor is otherwise 0, whatever the norm.  n[i] at most 2^34; count at most
  * 2^20.  ws_bytes >= tw_grad_norm_workspace_bytes(count, n), which is 0 where
