@@ -250,6 +250,18 @@ struct Workspace {
     }
 };
 
+// Address of a row's values at 16 bytes, as the library takes it: a contiguous tensor
+// that begins elsewhere (tokens[1:]) is copied, on the current stream of its device.
+struct Aligned {
+    Tensor own;
+    const void *p;
+    Aligned(PyObject *o, const void *at) : p(at) {
+        if (reinterpret_cast<uintptr_t>(at) % 16 == 0) return;
+        own = THPVariable_Unpack(o).clone();
+        p = own.data_ptr();
+    }
+};
+
 // Rows of a weight matrix (its first dimension).
 int64_t rows_of(Call &c, PyObject *o) {
     const Tensor *t = c.tensor(o);
@@ -378,7 +390,7 @@ PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t M = x->size(0), K = x->size(1);
         const void *dy = c.matrix(a[0], &dt, M, K);
         auto gamma = (const float *)c.need(a[2], at::kFloat, K);
-        auto rstd = (const float *)c.need(a[3], at::kFloat, M);
+        const void *rstd = c.need(a[3], at::kFloat, M);
         const at::ScalarType os = c.dtype(a[5], &ot);
         const void *dres = c.opt(a[4], os, M, K);
         if (!c.ok) return none();
@@ -386,9 +398,10 @@ PyObject *rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const size_t nws = tw_rmsnorm_bwd_workspace_bytes((int)M, (int)K);
         Tensor dx = c.empty({M, K}, os), dg = c.empty({K}, at::kFloat),
                ws = c.empty({(int64_t)nws}, at::kByte);
-        if (tw_rmsnorm_bwd(dy, dt, x->data_ptr(), xt, stride, gamma, rstd, dres, (int)M, (int)K,
-                           dx.data_ptr(), ot, dg.data_ptr<float>(), ws.data_ptr(), nws, c.stream(),
-                           nullptr) != TW_OK)
+        const Aligned ra(a[3], rstd);
+        if (tw_rmsnorm_bwd(dy, dt, x->data_ptr(), xt, stride, gamma, (const float *)ra.p, dres,
+                           (int)M, (int)K, dx.data_ptr(), ot, dg.data_ptr<float>(), ws.data_ptr(),
+                           nws, c.stream(), nullptr) != TW_OK)
             return none();
         return dict_of({{"dx", dx}, {"dgamma", dg}});
     });
@@ -504,10 +517,11 @@ PyObject *linear_ce(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const c10::DeviceGuard guard(c.device);
         Tensor loss = c.empty({M}, at::kFloat), lse = c.empty({M}, at::kFloat);
         const Workspace ws(c, a[3], tw_linear_ce_workspace_bytes((int)M, (int)K, (int)V));
-        if (!c.ok || tw_linear_ce_fwd((const uint16_t *)x->data_ptr(), stride, w, t, tt, (int)M,
-                                      (int)K, (int)V, loss.data_ptr<float>(),
-                                      lse.data_ptr<float>(), ws.p, ws.bytes, c.stream(),
-                                      nullptr) != TW_OK)
+        if (!c.ok) return none();
+        const Aligned ta(a[2], t);
+        if (tw_linear_ce_fwd((const uint16_t *)x->data_ptr(), stride, w, ta.p, tt, (int)M, (int)K,
+                             (int)V, loss.data_ptr<float>(), lse.data_ptr<float>(), ws.p, ws.bytes,
+                             c.stream(), nullptr) != TW_OK)
             return none();
         return dict_of({{"loss", loss}, {"lse", lse}});
     });
@@ -522,20 +536,21 @@ PyObject *linear_ce_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Tensor *x = bf16_rows(c, a[1], &stride);
         if (!x) return none();
         const int64_t M = x->size(0), K = x->size(1), V = rows_of(c, a[2]);
-        auto dloss = (const float *)c.need(a[0], at::kFloat, M);
+        const void *dloss = c.need(a[0], at::kFloat, M);
         auto w = (const uint16_t *)c.need(a[2], at::kBFloat16, V, K);
         int tt, xt, wt;
         const void *t = targets(c, a[3], M, &tt);
-        auto lse = (const float *)c.need(a[4], at::kFloat, M);
+        const void *lse = c.need(a[4], at::kFloat, M);
         const at::ScalarType xs = c.dtype(a[5], &xt), wts = c.dtype(a[6], &wt);
         if (!c.ok) return none();
         const c10::DeviceGuard guard(c.device);
         Tensor dx = c.empty({M, K}, xs), dw = c.empty({V, K}, wts);
         const Workspace ws(c, a[7], tw_linear_ce_bwd_workspace_bytes((int)M, (int)K, (int)V));
-        if (!c.ok || tw_linear_ce_bwd(dloss, (const uint16_t *)x->data_ptr(), stride, w, t, tt,
-                                      lse, (int)M, (int)K, (int)V, dx.data_ptr(), xt,
-                                      dw.data_ptr(), wt, ws.p, ws.bytes, c.stream(),
-                                      nullptr) != TW_OK)
+        if (!c.ok) return none();
+        const Aligned da(a[0], dloss), ta(a[3], t), la(a[4], lse);
+        if (tw_linear_ce_bwd((const float *)da.p, (const uint16_t *)x->data_ptr(), stride, w, ta.p,
+                             tt, (const float *)la.p, (int)M, (int)K, (int)V, dx.data_ptr(), xt,
+                             dw.data_ptr(), wt, ws.p, ws.bytes, c.stream(), nullptr) != TW_OK)
             return none();
         return dict_of({{"dx", dx}, {"dw", dw}});
     });

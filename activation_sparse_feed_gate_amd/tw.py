@@ -1257,6 +1257,14 @@ def quant_gateup(x, wg, g_scale, wu, u_scale, gamma=None, beta=None, eps=1e-5, x
     return h
 
 
+def _aligned(t):
+    """A contiguous tensor of a value a row at an address that the library takes: copied
+    where it begins at another row of a longer one (tokens[1:])."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.data_ptr() % 16:
+        return t.clone()
+    return t
+
+
 def rmsnorm(x, gamma, eps=1e-5, add=None, out_dtype=torch.bfloat16):
     """RMS norm of the rows of x (+ add).  Returns a dict: y, rstd (fp32, for
     ``rmsnorm_backward``), and sum = x + add in x's type (None without add)."""
@@ -1288,7 +1296,7 @@ def rmsnorm_backward(dy, x, gamma, rstd, dres=None, dx_dtype=torch.float32):
         "dgamma": torch.empty((K,), dtype=_F32, device=dev),
     }
     ws = torch.empty((tw_rmsnorm_bwd_workspace_bytes(M, K),), dtype=_U8T, device=dev)
-    tw_rmsnorm_bwd(dy, x, gamma, rstd, out["dx"], out["dgamma"], dres=dres, ws=ws)
+    tw_rmsnorm_bwd(dy, x, gamma, _aligned(rstd), out["dx"], out["dgamma"], dres=dres, ws=ws)
     return out
 
 
@@ -1352,7 +1360,8 @@ def gated_ffn_backward(dy, x, wg_t, wu_t, wd, g, u, act="silu", dx_dtype=torch.b
 
 def linear_ce(x, w, target, ws=None):
     """Cross entropy of the logits x w^T against one target a row (w: [V][K];
-    a target outside [0, V) leaves its row out).  Returns a dict: loss and lse
+    a target outside [0, V) leaves its row out).  The targets are contiguous and may
+    begin anywhere in a longer tensor (tokens[1:]).  Returns a dict: loss and lse
     (log-sum-exp) of every row, fp32."""
     got = _calls.linear_ce(x, w, target, ws)
     if got is not None:
@@ -1361,7 +1370,7 @@ def linear_ce(x, w, target, ws=None):
     V = _dims2(w, "w", "linear_ce")[0]
     out = {k: torch.empty((M,), dtype=_F32, device=x.device) for k in ("loss", "lse")}
     ws = _scratch(tw_linear_ce_workspace_bytes(M, K, V), x.device) if ws is None else ws
-    tw_linear_ce_fwd(x, w, target, out["loss"], out["lse"], ws)
+    tw_linear_ce_fwd(x, w, _aligned(target), out["loss"], out["lse"], ws)
     return out
 
 
@@ -1377,7 +1386,7 @@ def linear_ce_backward(dloss, x, w, target, lse, dx_dtype=torch.bfloat16, dw_dty
     out = {"dx": torch.empty((M, K), dtype=dx_dtype, device=x.device),
            "dw": torch.empty((V, K), dtype=dw_dtype, device=x.device)}
     ws = _scratch(tw_linear_ce_bwd_workspace_bytes(M, K, V), x.device) if ws is None else ws
-    tw_linear_ce_bwd(dloss, x, w, target, lse, ws, **out)
+    tw_linear_ce_bwd(_aligned(dloss), x, w, _aligned(target), _aligned(lse), ws, **out)
     return out
 
 
