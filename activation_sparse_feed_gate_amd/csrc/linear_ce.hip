@@ -267,8 +267,9 @@ struct EpiD {
 
 constexpr size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The backward pass's pieces of the vocabulary: columns of D in at most 512 MB,
-// dx's sums in parts that every piece adds to, a piece's dw.
+// The backward pass's pieces of the vocabulary: columns of D in at most 512 MB (or 256
+// of them), and at most kTileStrideMost where tiles read D's rows; dx's sums in parts
+// that every piece adds to, a piece's dw.
 struct Pieces {
     int width;
     bool few;  // dx in one piece by the kernel of few rows
@@ -280,16 +281,17 @@ SplitPlan dw_plan(int M, int K, int width) {
 }
 Pieces pieces_of(int M, int K, int V) {
     Pieces p;
-    const int64_t most = (int64_t)(512 << 20) / 2 / (M > 0 ? M : 1) / 256 * 256;
+    int64_t most = (int64_t)(512 << 20) / 2 / (M > 0 ? M : 1) / 256 * 256;
+    // Measured (us of D and dx; few rows' kernel, tiles): 1 row 1024 x 32768 33, 40; 64 rows
+    // 45, 46; 4 rows 2048 x 49999 69, 72.
+    p.few = M <= kFewDownMax && most >= V;
+    if (!p.few) most = std::min(most, kTileStrideMost);
     p.width = (int)(most < 256 ? 256 : most < V ? most : V);
     p.d_bytes = up256((size_t)M * ((p.width + 7) / 8 * 8) * 2);
     p.dx = split_plan<1>(TileArgs{{}, {}, 0, 0, M, K, p.width}, p.width < V);
     // the weight gradient's parts behind them, since dx's stay
     size_t dw = dw_plan(M, K, p.width).bytes;
     if (V % p.width) dw = std::max(dw, dw_plan(M, K, V % p.width).bytes);
-    // Measured (us of D and dx; few rows' kernel, tiles): 1 row 1024 x 32768 33, 40; 64 rows
-    // 45, 46; 4 rows 2048 x 49999 69, 72.
-    p.few = M <= kFewDownMax && p.width == V;
     p.dx_bytes = up256(p.few ? (size_t)few_down_split(1, M, K, V).splits * M * K * 4 : p.dx.bytes);
     p.part_bytes = p.dx_bytes + up256(dw);
     return p;

@@ -945,18 +945,17 @@ namespace {
 // ---- the dense training step -------------------------------------------------
 
 // Rows of bf16 that the tile kernels read in 16-byte pieces.
-constexpr int kTileMost = 1 << 20;  // elements of a row, and between rows
 tw_status check_tile_rows(int K, int64_t x_stride) {
     if (x_stride < K)
         return fail(TW_EINVAL, "x_stride=%lld is below K=%d", (long long)x_stride, K);
-    if (x_stride % 8 || x_stride > kTileMost)
+    if (x_stride % 8 || x_stride > tw::kTileRowMost)
         return fail(TW_EUNSUPPORTED, "x_stride=%lld: must be a multiple of 8, at most 2^20",
                     (long long)x_stride);
     return TW_OK;
 }
 tw_status check_tile_sizes(int M, int K) {
     if (M < 0 || K <= 0) return fail(TW_EINVAL, "M=%d K=%d: need M >= 0, K > 0", M, K);
-    if (K % 8 || K > kTileMost)
+    if (K % 8 || K > tw::kTileRowMost)
         return fail(TW_EUNSUPPORTED, "K=%d: must be a multiple of 8, at most 2^20", K);
     if (M > (1 << 24)) return fail(TW_EUNSUPPORTED, "M=%d: at most 2^24", M);
     return TW_OK;
@@ -972,7 +971,7 @@ tw_status check_tile_grid(int64_t a, int64_t b) {
 tw_status check_gated(int M, int K, int N) {
     TW_TRY(check_tile_sizes(M, K));
     if (N <= 0) return fail(TW_EINVAL, "N=%d: need N > 0", N);
-    if (N % 8 || N > kTileMost)
+    if (N % 8 || N > tw::kTileRowMost)
         return fail(TW_EUNSUPPORTED, "N=%d: must be a multiple of 8, at most 2^20", N);
     TW_TRY(check_tile_grid(M, N));
     TW_TRY(check_tile_grid(M, K));

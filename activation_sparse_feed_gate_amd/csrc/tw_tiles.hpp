@@ -12,15 +12,21 @@
 
 #include "tw_gemm.hpp"
 #include "tw_rows.hpp"
+#include "tw_train.hpp"
 
 namespace tw {
 
 enum { kRows = 0, kCols = 1 };
 
-// A byte offset past every descriptor made here (at most 256 rows of 2^20
-// elements).
+// A byte offset past every descriptor made here: they hold at most 256 rows of
+// kTileRowMost elements (2^29 bytes), or of a tile's rows those that are in the operand,
+// whose buffer is no larger (the loss's D, linear_ce.hip).
 constexpr uint32_t kPastEnd = 1u << 30;
-constexpr int64_t kMaxStride = 1 << 20;  // elements between operand rows
+static_assert(uint64_t(256) * kTileRowMost * 2 < kPastEnd, "");
+// Elements between rows of a kRows operand up to which the offset of any of a tile's 256
+// rows, from kPastEnd too, stays within 32 bits: one that wrapped would be read.
+constexpr int64_t kTileStrideMost = 1 << 22;
+static_assert(uint64_t(256) * kTileStrideMost * 2 + kPastEnd < (uint64_t(1) << 32), "");
 
 // A tile of an output: its product, its first row and column, its size, and its place
 // among the parts (-1: it takes the whole reduction).

@@ -25,6 +25,9 @@ hipError_t launch_rmsnorm_bwd(const void *dy, int dy_type, const void *x, int x_
                               const void *dres, int M, int K, void *dx, int dx_type, float *dgamma,
                               float *part, hipStream_t s, hipEvent_t ev_rows);
 
+// Elements of a row that the tile kernels take, and between rows (tw_tiles.hpp).
+constexpr int kTileRowMost = 1 << 20;
+
 // Activations of the gated FFN (the values of tw_act in the C ABI).
 enum { TW_A_RELU = 0, TW_A_SILU = 1, TW_A_GELU = 2 };
 
