@@ -781,34 +781,39 @@ inline hipError_t launch_sum_parts(const float *part, int splits, int64_t n, voi
     return hipGetLastError();
 }
 
-// The same for tiles of 64 WR x 256: part s of tile full + i is number s rest + i.
+// The same for tiles of 64 WR x 256: part s of tile full + i is number s rest + i.  A
+// workgroup takes 1024 outputs of a tile, and where a grid does not hold all of them (a
+// launch has at most 2^32 threads: 2^18 tiles of 256 rows) every gridDim-th.
+constexpr unsigned kSumGrid = 1u << 22;
 template <int WR>
 __global__ __launch_bounds__(256) void sum_tiles_kernel(const float *__restrict__ parts, int splits,
                                                         int rest, int full, int nbm, int nbn,
                                                         EpiStore epi, int M) {
     constexpr int kSize = 64 * WR * kWideCols, kBlocks = kSize / 1024;  // workgroups a tile
-    const int i = blockIdx.x / kBlocks;
-    int tile = full + i;
-    const int z = tile / (nbm * nbn);
-    tile -= z * (nbm * nbn);
-    int bm, bn;
-    walk_tile<EpiStore::kWalk>(tile, nbm, nbn, bm, bn);
-    const int at = (blockIdx.x % kBlocks * 256 + threadIdx.x) * 4;
-    const int m = bm * 64 * WR + at / kWideCols, n = bn * kWideCols + at % kWideCols;
-    if (m >= M || n >= epi.N) return;
-    const float *q = parts + (int64_t)i * kSize + at;
-    f32x4 v{};
-    for (int s = 0; s < splits; s += 4) {  // (4 latencies in one)
-        f32x4 w[4];
+    for (int64_t b = blockIdx.x; b < (int64_t)rest * kBlocks; b += gridDim.x) {
+        const int i = (int)(b / kBlocks);
+        int tile = full + i;
+        const int z = tile / (nbm * nbn);
+        tile -= z * (nbm * nbn);
+        int bm, bn;
+        walk_tile<EpiStore::kWalk>(tile, nbm, nbn, bm, bn);
+        const int at = ((int)(b % kBlocks) * 256 + threadIdx.x) * 4;
+        const int m = bm * 64 * WR + at / kWideCols, n = bn * kWideCols + at % kWideCols;
+        if (m >= M || n >= epi.N) continue;
+        const float *q = parts + (int64_t)i * kSize + at;
+        f32x4 v{};
+        for (int s = 0; s < splits; s += 4) {  // (4 latencies in one)
+            f32x4 w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            w[k] = *reinterpret_cast<const f32x4 *>(q + (int64_t)min(s + k, splits - 1) * rest *
-                                                            kSize);
+            for (int k = 0; k < 4; ++k)
+                w[k] = *reinterpret_cast<const f32x4 *>(
+                    q + (int64_t)min(s + k, splits - 1) * rest * kSize);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v += s + k < splits ? w[k] : f32x4{};
+            for (int k = 0; k < 4; ++k) v += s + k < splits ? w[k] : f32x4{};
+        }
+        store4(z == 0 ? epi.out[0] : z == 1 ? epi.out[1] : epi.out[2], epi.type,
+               (int64_t)m * epi.N + n, v);
     }
-    store4(z == 0 ? epi.out[0] : z == 1 ? epi.out[1] : epi.out[2], epi.type,
-           (int64_t)m * epi.N + n, v);
 }
 
 // How a product stored as it is takes its tiles: the first `full` whole and the rest in
@@ -864,7 +869,8 @@ hipError_t launch_split(TileArgs p, const SplitPlan &plan, const EpiStore &epi, 
     if (e != hipSuccess || !plan.bytes || !last) return e;
     const int nbm = (p.M + plan.rows - 1) / plan.rows, nbn = (p.N + kWideCols - 1) / kWideCols;
     const int rest = nbm * nbn * p.groups - plan.full;
-    const unsigned grid = (unsigned)(plan.rows * kWideCols / 1024) * rest;
+    const int64_t blocks = (int64_t)(plan.rows * kWideCols / 1024) * rest;
+    const unsigned grid = (unsigned)(blocks < kSumGrid ? blocks : kSumGrid);
     if (plan.rows == 256)
         sum_tiles_kernel<4><<<grid, 256, 0, s>>>(epi.parts, plan.splits, rest, plan.full, nbm, nbn,
                                                  epi, p.M);
