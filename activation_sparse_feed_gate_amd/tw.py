@@ -307,6 +307,25 @@ class _Args:
         if t.device != self.device:
             raise ValueError(f"{self.where}: {name} is on {t.device}, the inputs on {self.device}")
 
+    def apart(self, out, name, others):
+        """out and none of the named others, which the call reads after it has begun to
+        write out, share memory (any of them may be None)."""
+        if out is None or not out.numel():
+            return
+        begin, end = _span(out)
+        for other, t in others.items():
+            if t is None or not t.numel():
+                continue
+            b, e = _span(t)
+            if begin < e and b < end:
+                raise ValueError(f"{self.where}: {name} and {other} overlap")
+
+
+def _span(t):
+    """First and last address of a tensor's elements."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    return t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+
 
 def _dims2(t, name, where):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
@@ -889,6 +908,13 @@ def tw_gated_ffn_bwd(dy, x, wg_t, wu_t, wd, g, u, ws, act="silu", dx=None, dwg_t
     dw_kind = TW_BF16 if dwg_t is None else a.typed(dwg_t, "dwg_t", _FLOATS, (N, K))
     for t, name in ((dwu_t, "dwu_t"), (dwd, "dwd")):
         a.opt(t, name, _BF16 if dw_kind == TW_BF16 else _F32, (N, K))
+    # dx is written from the gate's and up's weights, the weight gradients after it from x and dy
+    a.apart(dx, "dx", {"wg_t": wg_t, "wu_t": wu_t, "dwg_t": dwg_t, "dwu_t": dwu_t, "dwd": dwd})
+    if dwg_t is not None:
+        a.apart(dx, "dx", {"x": x, "dy": dy})
+    a.apart(dwg_t, "dwg_t", {"x": x, "dy": dy, "dwu_t": dwu_t, "dwd": dwd})
+    a.apart(dwu_t, "dwu_t", {"x": x, "dy": dy, "dwd": dwd})
+    a.apart(dwd, "dwd", {"x": x, "dy": dy})
     a.bytes(ws, "ws")
     ev = _events(events)
     with _on(x):
@@ -942,6 +968,13 @@ def tw_linear_ce_bwd(dloss, x, w, target, lse, ws, dx=None, dw=None, stream=None
     a.shape(lse, "lse", _F32, (M,))
     dx_kind = TW_BF16 if dx is None else a.typed(dx, "dx", _FLOATS, (M, K))
     dw_kind = TW_BF16 if dw is None else a.typed(dw, "dw", _FLOATS, (V, K))
+    # dx is written from w, a piece's dw after it from x
+    a.apart(dx, "dx", {"w": w, "dw": dw})
+    if dw is not None:
+        a.apart(dx, "dx", {"x": x})
+        a.apart(dw, "dw", {"x": x})
+        if dw.data_ptr() != w.data_ptr() or dw.dtype != w.dtype:  # (else a piece replaces itself)
+            a.apart(dw, "dw", {"w": w})
     a.bytes(ws, "ws")
     ev = _events(events)
     with _on(x):

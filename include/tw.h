@@ -596,6 +596,10 @@ tw_status tw_gated_ffn_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *
  *   dx      [M][K]  bf16 or fp32, or NULL
  *   dwg_t, dwu_t, dwd [N][K] bf16 or fp32, all three or none (NULL)
  *
+ * The weight gradients are computed after dx, which therefore must not overlap x
+ * or dy where they are wanted; nor may it overlap wg_t or wu_t, a weight gradient
+ * x or dy, or one output another.
+ *
  * Limits as in the forward.  With M = 0 the weight gradients are zeros.
  * ws_bytes >= tw_gated_ffn_bwd_workspace_bytes(M, K, N).  events: [0] before,
  * [1] after dz, du and h, [2] after dx, [3] after the weight gradients.
@@ -639,6 +643,9 @@ tw_status tw_linear_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *
  * at a time, and D is rounded to bf16; sums are fp32.
  *
  *   dx      [M][K]  bf16 or fp32, or NULL;  dw [V][K] bf16 or fp32, or NULL
+ *
+ * dx must not overlap w, nor x where dw is wanted; nor dw x, dx or, unless it is
+ * w itself in its type, w.
  *
  * Limits as in the forward.  With M = 0, dw is zeros.  ws_bytes >=
  * tw_linear_ce_bwd_workspace_bytes(M, K, V): a piece of D (at most 512 MB, or
