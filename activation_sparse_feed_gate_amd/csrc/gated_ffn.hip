@@ -8,15 +8,20 @@
 //   dh = dy W_d^T,  du = dh act(g),  dz = dh u act'(g),  h = act(g) u  (one kernel)
 //   dx = dz W_g^T + du W_u^T                          (one sum over both terms)
 //   dW_g^T = dz^T x,  dW_u^T = du^T x,  dW_d = h^T dy           (one launch)
-// dz, du and h feed the matrix cores, so they are rounded to bf16 (half a unit
-// of 2^-8 a term, averaged out over the sums they enter); every sum is fp32.
+// h, dz and du feed the matrix cores, so they are rounded to bf16 between the products
+// (up to 2^-8 of a term, averaged out over the sums they enter); every sum is fp32.  An
+// output in bf16 is then off by 0.0023 of its norm, 0.0017 with these values in fp32:
+// its own rounding and as much again.
 //
-// What bounds them (bf16, normal operands): 16384 x 2048 x 8192 forward 1254 us, 1315
-// TFLOP/s, the chip's power (tw_tiles.hpp); backward 4096 x 1024 x 4096 224 us, of
-// which dh takes 56 (one round of tiles, whose 170 MB of g, u, dz, du and h pass only
-// after it: 23 us of products, 36 us of memory), dx 73 and the weight gradients 95 (64
-// to 192 tiles on 256 CUs, split and added).  One row, 2048 x 5632: 17.5 us for 69 MB
-// of weights, 4 TB/s.
+// What bounds them (bf16, normal operands, calls in a row): 16384 x 2048 x 8192 forward
+// 1254 to 1336 us, 1235 to 1315 TFLOP/s, the chip's power (tw_tiles.hpp); backward 4096 x
+// 1024 x 4096 224 to 239 us, of 224 dh 56 (one round of tiles, whose 170 MB of g, u, dz,
+// du and h pass only after it: 23 us of products, 36 us of memory), dx 73 (128 tiles,
+// each in two parts, and their sum) and the weight gradients 95 (192 whole tiles on 256
+// CUs).  One row, 2048 x 5632: 17.5 to 18 us for 69 MB of weights, 3.9 TB/s.  65 to about
+// 1000 rows: gate and up and dh take every tile's whole reduction, so few workgroups walk
+// a long one (4096 x 1024: 128 rows on 8 and 4 workgroups, 47 and 52 us, as much as 1024
+// rows take).
 //
 // Activations of the form g s(a(g)) with the logistic function s: SiLU has
 // a = g, the tanh form of GELU a = 2 sqrt(2 / pi) (g + 0.044715 g^3), since
@@ -140,7 +145,10 @@ struct EpiDh {
 // Up to 64 token rows (16 MB): a workgroup takes up to 16 C hidden neurons of NM
 // matrices, its 8 waves a slice of K each; their sums meet in LDS.  Bound by the stream
 // of weights.  Measured (us, these kernels and tiles): gate and up, 1 row 1024 x 4096
-// 7.6, 17.8, 64 rows 11.9, 18.1; 64 rows 2048 x 5632 20, 28; dh of 64 rows 21, 35.
+// 7.6, 17.8, 64 rows 11.9, 18.1; 64 rows 2048 x 5632 20, 28; dh of 64 rows 21, 35.  The
+// limit of 64 is not where tiles begin to win but what the waves' sums leave of the LDS
+// (128 KB): by kernel, 64 and 65 rows of 2048 x 5632 take 17, 26 (gate and up) and 18, 31
+// (dh), of 4096 x 1024 21, 45 and 20, 50.
 template <int ACT>
 struct FewUp {
     static constexpr int NM = 2;

@@ -8,7 +8,7 @@
 // a captured graph replays them.  Sums are fp32, 8 of them a thread; the
 // workgroups' sums are added in fp64, in a fixed order (no atomics: the norm does
 // not depend on timing).  Measured: 336 M elements in 146 buffers, bf16 clipped
-// into fp32, 556 us at 4.8 TB/s; 3.9 M fp32 elements in 26 buffers 13.8 us (from cache).
+// into fp32, 557 to 561 us at 4.8 TB/s; 3.9 M fp32 elements in 26 buffers 13.8 us (from cache).
 #include "tw_rows.hpp"
 #include "tw_train.hpp"
 

@@ -14,10 +14,14 @@
 // A row whose target is outside [0, V) is left out: its loss and its row of D
 // are 0.
 //
-// What bounds it (bf16, normal operands): 4096 x 1024 x 32768 forward 206 us, 1330
-// TFLOP/s, the chip's power (tw_tiles.hpp); backward 4096 x 1024 x 49999 1123 us for
-// three products of 419 GFLOP, D's exponentials (3 us a tile, while the matrix cores
-// wait) and its 410 MB written and read twice.  4 rows 1024 x 32768: 16.6 us for 67 MB.
+// D's rounding to bf16 is up to 2^-8 of a term: a gradient in bf16 is off by 0.0024 of its
+// norm, 0.0017 with D in fp32.
+//
+// What bounds it (bf16, normal operands, calls in a row): 4096 x 1024 x 32768 forward 206
+// to 225 us, 1220 to 1330 TFLOP/s, the chip's power (tw_tiles.hpp); backward 4096 x 1024
+// x 49999 1123 to 1179 us for three products of 419 GFLOP, D's exponentials (3 us a tile,
+// while the matrix cores wait) and its 410 MB written and read twice.  4 rows 1024 x
+// 32768: 16.6 to 17 us for 67 MB.
 #include <algorithm>
 
 #include "tw_few.hpp"
@@ -117,9 +121,11 @@ __global__ __launch_bounds__(kFewSoftThreads) void few_soft_kernel(
 #pragma unroll
             for (int e = 0; e < 4; ++e) l[b][e] = acc[b][m][e];
 #pragma unroll
-        for (int b = 0; b < kSoftBlocks; ++b) epi.most<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+        for (int b = 0; b < kSoftBlocks; ++b)
+            epi.most<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
 #pragma unroll
-        for (int b = 0; b < kSoftBlocks; ++b) epi.add<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
+        for (int b = 0; b < kSoftBlocks; ++b)
+            epi.add<4, false>(row, v0 + 16 * b + 4 * (lane >> 4), l[b]);
         epi.join<16>(row);
         epi.join<32>(row);
         if (lane < 16) all[wave][16 * m + lane] = {row.top, row.sum};
@@ -356,7 +362,8 @@ hipError_t launch_ce_bwd(const float *dloss, const uint16_t *x, int64_t x_stride
                 TileArgs{{d}, {wp}, ldd, K, M, K, N}, pc.dx,
                 EpiStore{{dx}, dx_type, K, parts, first > 0}, first + N == V, s);
         if (e == hipSuccess && dw) {
-            char *out = static_cast<char *>(dw) + (int64_t)first * K * (dw_type == TW_T_F32 ? 4 : 2);
+            char *out =
+                static_cast<char *>(dw) + (int64_t)first * K * (dw_type == TW_T_F32 ? 4 : 2);
             e = launch_split<kCols, kCols, 1>(TileArgs{{d}, {x}, ldd, x_stride, N, K, M},
                                                  dw_plan(M, K, N),
                                                  EpiStore{{out}, dw_type, K, dw_parts}, true, s);

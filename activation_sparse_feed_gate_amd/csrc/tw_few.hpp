@@ -215,8 +215,8 @@ inline hipError_t few_down(const uint16_t *const (&h)[2], const uint16_t *const 
                          : mb == 2 ? few_down_as<2>(h, w, pairs, ldh, M, K, N, part, s)
                                    : few_down_as<4>(h, w, pairs, ldh, M, K, N, part, s);
     if (e != hipSuccess) return e;
-    return launch_sum_parts(part, pairs * few_down_split(pairs, M, K, N).splits, (int64_t)M * K, out,
-                            type, s);
+    const int splits = pairs * few_down_split(pairs, M, K, N).splits;
+    return launch_sum_parts(part, splits, (int64_t)M * K, out, type, s);
 }
 
 }  // namespace tw

@@ -133,8 +133,9 @@ struct NoFetch {};
 // Loads of either cover whole 128-byte lines.
 //
 // A wave's 64 x 128 outputs are 128 accumulator registers a lane, which leave room for a
-// second set of B's fragments; they read 24 KB of LDS for 128 matrix instructions.  128 x
-// 128 a wave would read a third less, but did not fit: its accumulators spill.
+// second set of B's fragments; they read 48 KB of LDS for 128 matrix instructions (24 a
+// stage, for 64).  128 x 128 a wave would read a third less, but did not fit: its
+// accumulators spill.
 // What bounds a large product is power: on operands of zeros, where nothing toggles,
 // 16384 x 8192 x 2048 and its like run at 1740 to 1830 TFLOP/s (kRows x kRows), on
 // normal ones at 1330 to 1390; kRows x kCols 1650 and 1300.  16 x 16 x 32
@@ -687,7 +688,10 @@ hipError_t launch_wide(const TileArgs &p, const Epi &epi, hipStream_t s) {
 // takes 1.0 to 1.6 us in the larger tiles and 0.55 to 0.95 in the smaller ones, the more
 // the more CUs draw power and load; 8 us come before the first and after the last.  (A
 // third stage of loads ahead in the smaller tiles' LDS changed nothing for the better: 1 x
-// 64 stages 47 -> 55 us.)
+// 64 stages 47 -> 55 us.)  No epilogue is counted, though dh's, which reads 4 and writes 6
+// bytes an output, takes longer than its product: 4096 x 1024 x 4096 34 us estimated, 56
+// to 60 measured.  It is the same work in tiles of either height, and no shape was found
+// where the estimate took the slower one (dh there in the smaller tiles 72 us).
 template <int WR>
 double tiles_us(int64_t items, int64_t stages) {
     const double least = WR == 4 ? 1.0 : 0.55, more = WR == 4 ? 0.6 : 0.4;

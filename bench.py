@@ -6,7 +6,8 @@ tokens: ``tw_pack_gate`` (gate GEMM + ReLU + TwELL packing, overflow list)
 then ``tw_sparse_ffn_fwd`` (fused sparse up+down, dense fallback for the
 overflow rows).  Inputs are resident in HBM before the timed region.  The
 dense gated FFN ``tw_ffn_fwd`` is timed the same way at the same shape for
-the speedup.  Per-kernel durations come from HIP events recorded on the
+the speedup (the library's other dense forward, ``tw_gated_ffn_fwd`` with a
+ReLU, is faster at these shapes when cold).  Per-kernel durations come from HIP events recorded on the
 launch stream between the library's kernels.
 
 Prints one JSON line (rank 0, one GPU).

@@ -260,6 +260,11 @@ tw_status tw_sparse_ffn_fwd(const uint16_t *x, const uint16_t *wg_t,
  * Shapes: M >= 0, K and N positive multiples of 128, N * K < 2^31 (each
  * weight matrix under 4 GiB: 32-bit buffer offsets).  The workspace query
  * returns 0 for any other shape.
+ *
+ * tw_gated_ffn_fwd with TW_RELU computes the same for more shapes.  Measured
+ * (us, warm; this call, that one): 1 row 2048 x 5632 25, 18; 64 rows 28, 31; 128
+ * rows 32, 42; 512 rows 65, 53; 4096 x 1024 x 4096 104, 108; 4096 x 2048 x 5632
+ * 274, 218; 16384 x 2048 x 8192 1435, 1195.
  */
 size_t tw_ffn_workspace_bytes(int M, int K, int N);
 tw_status tw_ffn_fwd(const uint16_t *x, const uint16_t *wg_t,
@@ -566,7 +571,7 @@ tw_status tw_rmsnorm_bwd(const void *dy, int dy_type, const void *x, int x_type,
 /*
  * Dense gated FFN, forward: y = h W_d with h = act(g) u, g = x W_g, u = x W_u
  * (act: a tw_act).  h is rounded to bf16 between the two products; sums are
- * fp32.
+ * fp32.  (With TW_RELU also tw_ffn_fwd, which says where it is the faster one.)
  *
  *   x       [M] rows of K bf16, x_stride elements apart
  *   wg_t, wu_t, wd [N][K] bf16, as above
@@ -639,8 +644,9 @@ tw_status tw_linear_ce_fwd(const uint16_t *x, int64_t x_stride, const uint16_t *
  *     D[m][v] = dloss[m] (exp(l[m][v] - lse[m]) - [v = t]),
  *     dx = D w,   dw = D^T x
  * (rows of D of rows that are left out, or whose dloss is 0, are 0 whatever they
- * hold; their x enters dw times 0, so for dw it has to be finite).  The logits are computed again, a piece of the vocabulary
- * at a time, and D is rounded to bf16; sums are fp32.
+ * hold; their x enters dw times 0, so for dw it has to be finite).  The logits
+ * are computed again, a piece of the vocabulary at a time, and D is rounded to
+ * bf16; sums are fp32.
  *
  *   dx      [M][K]  bf16 or fp32, or NULL;  dw [V][K] bf16 or fp32, or NULL
  *
